@@ -30,6 +30,9 @@ __all__ = [
     "attn_core_gelu_fwd", "attn_core_gelu_bwd", "gelu_fwd", "gelu_bwd",
     "attn_core_fwd_varlen", "attn_core_bwd_varlen", "attn_core_bwd_varlen_workspace_bytes",
     "fwd_varlen", "bwd_varlen",
+    "ERR_DEVICE_TABLE", "RopeTable", "rope_table", "attn_core_rope_fwd", "attn_core_rope_bwd", "rope_fwd",
+    "rope_bwd", "PAGE_SIZES", "PagedBatch", "attn_core_paged_append", "attn_core_paged_fwd",
+    "attn_core_paged_workspace_bytes", "paged_append", "paged_fwd", "attn_core_page_copy", "page_copy",
 ]
 
 OK = 0
@@ -39,9 +42,11 @@ ERR_MISALIGNED = 3
 ERR_WORKSPACE_TOO_SMALL = 4
 ERR_CUDA = 5
 ERR_DEVICE_TIMEOUT = 6
+ERR_DEVICE_TABLE = 7
 FLAG_REDRAW_MASK = 0x1
 FLAG_TEST_WAIT_TIMEOUT = 0x100
 SUPPORTED_HEAD_DIMS = (64, 96, 128, 160)
+PAGE_SIZES = (16, 32, 64, 128, 256)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libattn_core.so")
@@ -80,6 +85,33 @@ class _CBytes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("layer_none", "layer_selective", "layer_full", "core_scores_avoided",
                  "core_kept", "core_recompute_state")]
+
+
+class _CRopeConfig(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("d", "rot_dim", "interleaved", "scaling")] +
+                [(n, ctypes.c_double) for n in ("base", "factor", "original_len", "low_freq", "high_freq",
+                                                "beta_fast", "beta_slow", "mscale")])
+
+
+class RopeTable(ctypes.Structure):
+    """Mirror of ``attn_core_rope_table``: made by :func:`rope_table`, kept by
+    the caller and passed to every rotation."""
+    _fields_ = [("d", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+class _CRopeParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("b", "s", "h_q", "h_kv")] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "yq_stride", "yk_stride")] +
+                [("pos0", ctypes.c_int32), ("positions", ctypes.c_void_p)])
+
+
+class _CPagedParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seq", "n_tokens", "h_q", "h_kv", "d", "page_size", "n_pages",
+                                               "max_pages", "causal")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_void_p) for n in ("cu_seqlens_q", "kv_lens", "page_table", "dev_status")] +
+                [("flags", ctypes.c_int32), ("wait_timeout_ms", ctypes.c_uint32)])
 
 
 @dataclass
@@ -176,6 +208,22 @@ def load_library(path: str = LIB_PATH):
     lib.attn_core_gelu_fwd.restype = ctypes.c_int
     lib.attn_core_gelu_bwd.argtypes = [ctypes.c_int64, vp, vp, vp, vp]
     lib.attn_core_gelu_bwd.restype = ctypes.c_int
+    RT, RP = ctypes.POINTER(RopeTable), ctypes.POINTER(_CRopeParams)
+    lib.attn_core_rope_init.argtypes = [ctypes.POINTER(_CRopeConfig), RT]
+    lib.attn_core_rope_init.restype = ctypes.c_int
+    for f in (lib.attn_core_rope_fwd, lib.attn_core_rope_bwd):
+        f.argtypes = [RP, RT, vp, vp, vp, vp, vp]
+        f.restype = ctypes.c_int
+    PP = ctypes.POINTER(_CPagedParams)
+    lib.attn_core_paged_append.argtypes = [PP, RT, vp, vp, vp, ctypes.POINTER(ctypes.c_int64), vp, vp, vp, vp]
+    lib.attn_core_paged_append.restype = ctypes.c_int
+    lib.attn_core_paged_workspace_bytes.argtypes = [PP]
+    lib.attn_core_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_core_paged_fwd.argtypes = [PP, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.attn_core_paged_fwd.restype = ctypes.c_int
+    lib.attn_core_page_copy.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp,
+                                        ctypes.c_int64, vp]
+    lib.attn_core_page_copy.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -504,3 +552,277 @@ def bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, *, causal
     if rc != OK:
         raise AttnCoreError(rc, "attn_core_bwd_varlen")
     return dq, dk, dv
+
+
+# ------------------------------------- rotary positions, the paged cache ---
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def rope_table(d: int, *, rot_dim: int = 0, base: float = 10000.0, interleaved: bool = False,
+               scaling: str = "none", factor: float = 1.0, original_len: float = 0.0, low_freq: float = 0.0,
+               high_freq: float = 0.0, beta_fast: float = 0.0, beta_slow: float = 0.0,
+               mscale: float = 0.0) -> RopeTable:
+    """The frequencies of rotary positions over the first ``rot_dim`` values of
+    each head (all, up to 256, by default); ``scaling`` is "none", "linear",
+    "bands" or "yarn" (formulas: include/attn_core.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}, got {scaling!r}")
+    c = _CRopeConfig(int(d), int(rot_dim), int(bool(interleaved)), ROPE_SCALINGS[scaling], float(base), float(factor),
+                     float(original_len), float(low_freq), float(high_freq), float(beta_fast), float(beta_slow),
+                     float(mscale))
+    t = RopeTable()
+    rc = load_library().attn_core_rope_init(ctypes.byref(c), ctypes.byref(t))
+    if rc != OK:
+        raise AttnCoreError(rc, "attn_core_rope_init")
+    return t
+
+
+def attn_core_rope_fwd(p: _CRopeParams, t: RopeTable, q: int, k: int, yq: int, yk: int, stream: int) -> int:
+    return load_library().attn_core_rope_fwd(p, t, q or None, k or None, yq or None, yk or None, stream or None)
+
+
+def attn_core_rope_bwd(p: _CRopeParams, t: RopeTable, dyq: int, dyk: int, dq: int, dk: int, stream: int) -> int:
+    return load_library().attn_core_rope_bwd(p, t, dyq or None, dyk or None, dq or None, dk or None, stream or None)
+
+
+def attn_core_paged_append(p: _CPagedParams, t, q: int, k: int, v: int, strides, q_out: int, k_pages: int,
+                           v_pages: int, stream: int) -> int:
+    """strides: three host integers (q, k, v), or None for packed tensors."""
+    st = (ctypes.c_int64 * 3)(*strides) if strides is not None else None
+    return load_library().attn_core_paged_append(p, t, q or None, k, v, st, q_out or None, k_pages, v_pages,
+                                                 stream or None)
+
+
+def attn_core_paged_workspace_bytes(p: _CPagedParams) -> int:
+    return int(load_library().attn_core_paged_workspace_bytes(p))
+
+
+def attn_core_paged_fwd(p: _CPagedParams, q: int, k_pages: int, v_pages: int, o: int, lse: int, workspace: int,
+                        workspace_bytes: int, stream: int) -> int:
+    return load_library().attn_core_paged_fwd(p, q, k_pages, v_pages, o, lse, workspace, workspace_bytes,
+                                              stream or None)
+
+
+def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: int, page_bytes: int, pairs: int,
+                        n_pairs: int, stream: int) -> int:
+    """pairs: address of host int32 [n_pairs, 2]."""
+    return load_library().attn_core_page_copy(pages, n_planes, plane_stride, n_pages, page_bytes, pairs or None,
+                                              n_pairs, stream or None)
+
+
+def _on_device(*tensors) -> None:
+    """The library launches on the current device: every tensor lives there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _rope_view(x, name, d):
+    """(b, heads, s, strides) of [b, h, s, d] or packed [tokens, h, d]; only d
+    has to be contiguous.  A dimension of one element has no stride."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if x.dim() not in (3, 4) or x.shape[-1] != d:
+        raise ValueError(f"{name} must be [b, h, s, {d}] or [tokens, h, {d}], got {tuple(x.shape)}")
+    if x.stride(-1) != 1 and d > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if x.dim() == 4:
+        (b, h, s, _), (tb, th, ts, _) = x.shape, x.stride()
+    else:
+        (s, h, _), (ts, th, _) = x.shape, x.stride()
+        b, tb = 1, 0
+    return b, h, s, (tb if b > 1 else 0, th if h > 1 else 0, ts if s > 1 else 0)
+
+
+def _rope(call, what, q, k, table, positions, pos0, out_q, out_k):
+    import torch
+    d = table.d
+    p = _CRopeParams()
+    ptr = [0, 0, 0, 0]
+    outs = [out_q, out_k]
+    lead = None
+    for i, (x, y, name) in enumerate(((q, out_q, "q"), (k, out_k, "k"))):
+        if x is None:
+            continue
+        b, h, s, st = _rope_view(x, name, d)
+        if lead not in (None, (b, s, x.dim())):
+            raise ValueError(f"q and k must have the same batch and tokens, got {tuple(q.shape)}, {tuple(k.shape)}")
+        lead = (b, s, x.dim())
+        if y is None:
+            outs[i] = y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        elif y.shape != x.shape:
+            raise ValueError(f"out_{name} must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
+        yst = _rope_view(y, "out_" + name, d)[3]
+        if i == 0:
+            p.h_q, p.q_stride[:], p.yq_stride[:] = h, st, yst
+        else:
+            p.h_kv, p.k_stride[:], p.yk_stride[:] = h, st, yst
+        ptr[i], ptr[i + 2] = x.data_ptr(), y.data_ptr()
+    if lead is None:
+        raise ValueError("q or k must be given")
+    p.b, p.s, p.pos0 = lead[0], lead[1], int(pos0)
+    if positions is not None:
+        if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
+                or positions.numel() != p.b * p.s:
+            raise ValueError(f"positions must be a contiguous int32 CUDA tensor of {p.b * p.s} values")
+        p.positions = positions.data_ptr()
+    _on_device(q, k, outs[0], outs[1], positions)
+    if p.b * p.s:
+        rc = call(p, table, *ptr, _stream())
+        if rc != OK:
+            raise AttnCoreError(rc, what)
+    return outs[0], outs[1]
+
+
+def rope_fwd(q, k, table: RopeTable, *, positions=None, pos0: int = 0, out_q=None, out_k=None):
+    """Rotary positions on q and k (either may be None): bf16 [b, h, s, d] or
+    packed [tokens, h, d] of any strides with d contiguous.  ``positions``:
+    int32, one per (batch element, token); by default pos0 + token.  ``out_q`` /
+    ``out_k`` may be the inputs themselves.  Returns (q, k) rotated."""
+    return _rope(attn_core_rope_fwd, "attn_core_rope_fwd", q, k, table, positions, pos0, out_q, out_k)
+
+
+def rope_bwd(dq, dk, table: RopeTable, *, positions=None, pos0: int = 0, out_q=None, out_k=None):
+    """Gradients of rope_fwd's inputs from those of its outputs."""
+    return _rope(attn_core_rope_bwd, "attn_core_rope_bwd", dq, dk, table, positions, pos0, out_q, out_k)
+
+
+class PagedBatch:
+    """A batch of sequences whose keys and values live in pages, as
+    paged_append and paged_fwd take it (layout: include/attn_core.h).
+
+    ``cu_seqlens_q`` [n_seq + 1], ``kv_lens`` [n_seq] and ``page_table``
+    [n_seq, max_pages] are int32 CUDA tensors, read by the kernels when they
+    run: a step's new lengths and pages are copied into them, and a captured
+    graph follows.  The batch owns the attention's workspace; calls that may
+    overlap on the GPU need a batch (or a ``workspace``) each."""
+
+    def __init__(self, cu_seqlens_q, kv_lens, page_table, *, n_tokens: int, h_q: int, h_kv: int, d: int,
+                 page_size: int, n_pages: int, causal: bool = True, scale: float = 0.0, dev_status: int = 0,
+                 flags: int = 0, wait_timeout_ms: int = 0, workspace=None):
+        import torch
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table must be [n_seq, max_pages], got {tuple(page_table.shape)}")
+        n_seq, max_pages = page_table.shape
+        _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n_seq + 1,))
+        _check(kv_lens, "kv_lens", torch.int32, (n_seq,))
+        _check(page_table, "page_table", torch.int32, (n_seq, max_pages))
+        self.tables = (cu_seqlens_q, kv_lens, page_table)
+        self.params = _CPagedParams(n_seq, int(n_tokens), int(h_q), int(h_kv), int(d), int(page_size), int(n_pages),
+                                    max_pages, int(bool(causal)), float(scale), cu_seqlens_q.data_ptr(),
+                                    kv_lens.data_ptr(), page_table.data_ptr(), dev_status or None, int(flags),
+                                    int(wait_timeout_ms))
+        need = attn_core_paged_workspace_bytes(self.params)
+        if need == 0:       # the call itself says what is wrong
+            raise AttnCoreError(ERR_UNSUPPORTED if page_size not in PAGE_SIZES or d not in SUPPORTED_HEAD_DIMS
+                                else ERR_INVALID_ARG, "PagedBatch")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=cu_seqlens_q.device)
+        self.workspace = workspace
+        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self._q_shape = torch.Size((int(n_tokens), int(h_q), int(d)))
+        self._kv_shape = torch.Size((int(n_tokens), int(h_kv), int(d)))
+        self._page_shape = torch.Size((int(n_pages), int(h_kv), int(page_size), int(d)))
+        self._lse_shape = torch.Size((int(h_q), int(n_tokens)))
+
+
+def _token_stride(x, name, shape):
+    """Elements from one token to the next of [tokens, heads, d] whose heads are
+    contiguous (a slice of a fused projection, for one)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16 or x.shape != shape:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor of shape {tuple(shape)}")
+    t, h, e = x.stride()
+    if (e != 1 and shape[2] > 1) or (h != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous in its heads and their values")
+    return t if shape[0] > 1 else shape[1] * shape[2]
+
+
+def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTable | None = None, out_q=None):
+    """Add the new tokens' k and v [n_tokens, h_kv, d] to the cache, rotated by
+    ``table`` at their positions (None: as they are), and rotate q
+    [n_tokens, h_q, d] (or None).  Returns q's rotation, packed."""
+    import torch
+    strides = [0, _token_stride(k, "k", batch._kv_shape), _token_stride(v, "v", batch._kv_shape)]
+    _check(k_pages, "k_pages", torch.bfloat16, batch._page_shape)
+    _check(v_pages, "v_pages", torch.bfloat16, batch._page_shape)
+    if q is not None:
+        strides[0] = _token_stride(q, "q", batch._q_shape)
+        if out_q is None:
+            out_q = torch.empty(batch._q_shape, dtype=torch.bfloat16, device=q.device)
+        _check(out_q, "out_q", torch.bfloat16, batch._q_shape)
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    _on_device(q, k, v, k_pages, v_pages, out_q, batch.tables[0])
+    if batch.params.n_tokens:
+        rc = attn_core_paged_append(batch.params, table, q.data_ptr() if q is not None else 0, k.data_ptr(),
+                                    v.data_ptr(), strides, out_q.data_ptr() if q is not None else 0,
+                                    k_pages.data_ptr(), v_pages.data_ptr(), _stream())
+        if rc != OK:
+            raise AttnCoreError(rc, "attn_core_paged_append")
+    return out_q
+
+
+def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
+    """Attention of the batch's new tokens q [n_tokens, h_q, d] over the cache
+    (which already holds their keys and values).  Returns (O like q, LSE fp32
+    [h_q, n_tokens])."""
+    import torch
+    _check(q, "q", torch.bfloat16, batch._q_shape)
+    _check(k_pages, "k_pages", torch.bfloat16, batch._page_shape)
+    _check(v_pages, "v_pages", torch.bfloat16, batch._page_shape)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", torch.bfloat16, batch._q_shape)
+    if lse is None:
+        lse = torch.empty(batch._lse_shape, dtype=torch.float32, device=q.device)
+    else:
+        _check(lse, "lse", torch.float32, batch._lse_shape)
+    _on_device(q, k_pages, v_pages, out, lse, batch.workspace)
+    if batch.params.n_tokens:
+        rc = attn_core_paged_fwd(batch.params, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), *batch._ws, _stream())
+        if rc != OK:
+            raise AttnCoreError(rc, "attn_core_paged_fwd")
+    return out, lse
+
+
+def page_copy(pages, pairs) -> None:
+    """Copy pages of a cache, pairs[i] = (from, to), in every plane of ``pages``
+    [planes, n_pages, h_kv, page_size, d] (or one plane, four-dimensional).
+    ``pairs``: a host list or int32 array; no target may be named twice or be
+    another copy's source."""
+    import numpy as np
+    import torch
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dim() not in (4, 5) \
+            or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous CUDA tensor [planes, n_pages, h_kv, page_size, d]")
+    if isinstance(pairs, torch.Tensor):
+        if pairs.is_cuda:
+            raise ValueError("pairs must be in host memory")
+        pairs = pairs.numpy()
+    wide = np.asarray(pairs)
+    if wide.size and wide.dtype.kind not in "iu":
+        raise ValueError("pairs must be integers")
+    if wide.size and (wide.ndim != 2 or wide.shape[1] != 2):
+        raise ValueError(f"pairs must be [n, 2], got {wide.shape}")
+    arr = np.ascontiguousarray(wide, dtype=np.int32)
+    if arr.dtype != wide.dtype and not np.array_equal(arr, wide):
+        raise ValueError("pairs must fit 32 bits")
+    _on_device(pages)
+    planes = pages.shape[0] if pages.dim() == 5 else 1
+    n_pages = pages.shape[-4]
+    if pages.numel() == 0:
+        if arr.size:
+            raise ValueError("no pages to copy")
+        return
+    page_bytes = pages.numel() // (planes * n_pages) * pages.element_size()
+    rc = attn_core_page_copy(pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes, arr.ctypes.data,
+                             arr.shape[0] if arr.size else 0, _stream())
+    if rc != OK:
+        raise AttnCoreError(rc, "attn_core_page_copy")

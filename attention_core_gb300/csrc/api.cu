@@ -3,6 +3,7 @@
 // allocated here; the caller owns every buffer.
 #include <cudaTypedefs.h>
 #include <math.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "../../include/attn_core.h"
@@ -231,6 +232,7 @@ const char* attn_core_strerror(int code)
         case ATTN_CORE_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
         case ATTN_CORE_ERR_CUDA: return "CUDA error";
         case ATTN_CORE_ERR_DEVICE_TIMEOUT: return "a kernel wait ran past its time limit";
+        case ATTN_CORE_ERR_DEVICE_TABLE: return "a device table held an entry out of range";
         default: return "unknown error";
     }
 }
@@ -733,6 +735,352 @@ int attn_core_bwd_recompute_noalloc(const attn_core_params* p, const void* q, co
     // its own mask.
     return bwd_impl(p, q, k, v, o, lse, dout, dq, dk, dv, addr, sizeof(float) * 2 * kNoAllocMaxRows, false,
                     stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rotary positions.
+static_assert(sizeof(ac::RopeTable) == sizeof(attn_core_rope_table), "the table is passed as it is");
+static_assert(ac::kStatusTable == ATTN_CORE_ERR_DEVICE_TABLE, "status code");
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586;
+
+bool positive(double x) { return x > 0.0 && !isinf(x); }
+
+int check_rope_table(const attn_core_rope_table* t)
+{
+    if (t == nullptr) return ATTN_CORE_ERR_INVALID_ARG;
+    if (t->d < 8 || t->d > 512 || t->d % 8 || t->rot_dim < 8 || t->rot_dim > 256 || t->rot_dim > t->d ||
+        t->rot_dim % 8 || (t->interleaved != 0 && t->interleaved != 1))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    return ATTN_CORE_OK;
+}
+
+// Strides of one tensor: rows 16-byte aligned and, of an output, apart: the
+// dimensions in the order of their strides each step over the whole of the
+// smaller ones.
+int check_rope_strides(const int64_t (&st)[3], int64_t b, int64_t h, int64_t s, int64_t d, bool output)
+{
+    const int64_t n[3] = {b, h, s};
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] < 0) return ATTN_CORE_ERR_INVALID_ARG;
+        if (st[i] % 8) return ATTN_CORE_ERR_MISALIGNED;
+        if (st[i] > ((int64_t)1 << 42)) return ATTN_CORE_ERR_INVALID_ARG;
+    }
+    if (!output) return ATTN_CORE_OK;
+    int64_t span = d;
+    bool used[3] = {n[0] <= 1, n[1] <= 1, n[2] <= 1};
+    for (int k = 0; k < 3; ++k) {
+        int least = -1;
+        for (int i = 0; i < 3; ++i)
+            if (!used[i] && (least < 0 || st[i] < st[least])) least = i;
+        if (least < 0) break;
+        used[least] = true;
+        if (st[least] < span) return ATTN_CORE_ERR_INVALID_ARG;
+        span += st[least] * (n[least] - 1);
+    }
+    return ATTN_CORE_OK;
+}
+
+int rope_call(const attn_core_rope_params* p, const attn_core_rope_table* t, const void* q, const void* k, void* yq,
+              void* yk, float sign, void* stream)
+{
+    int rc = check_rope_table(t);
+    if (rc) return rc;
+    if (p == nullptr || p->b <= 0 || p->s < 0 || p->h_q < 0 || p->h_kv < 0 || p->h_q + (int64_t)p->h_kv == 0 ||
+        (int64_t)p->b * p->s >= (int64_t)INT32_MAX)
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if ((p->h_q && (!q || !yq)) || (p->h_kv && (!k || !yk))) return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->h_q && ((rc = check_rope_strides(p->q_stride, p->b, p->h_q, p->s, t->d, q == yq)) ||
+                   (rc = check_rope_strides(p->yq_stride, p->b, p->h_q, p->s, t->d, true))))
+        return rc;
+    if (p->h_kv && ((rc = check_rope_strides(p->k_stride, p->b, p->h_kv, p->s, t->d, k == yk)) ||
+                    (rc = check_rope_strides(p->yk_stride, p->b, p->h_kv, p->s, t->d, true))))
+        return rc;
+    // in place means the same element at the same place
+    for (int i = 0; i < 3; ++i)
+        if ((p->h_q && q == yq && p->q_stride[i] != p->yq_stride[i]) ||
+            (p->h_kv && k == yk && p->k_stride[i] != p->yk_stride[i]))
+            return ATTN_CORE_ERR_INVALID_ARG;
+    if ((p->h_q && (!aligned16(q) || !aligned16(yq))) || (p->h_kv && (!aligned16(k) || !aligned16(yk))) ||
+        (reinterpret_cast<uintptr_t>(p->positions) & 3u))
+        return ATTN_CORE_ERR_MISALIGNED;
+    if (p->s == 0) return ATTN_CORE_OK;
+    if ((rc = check_device())) return rc;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    ac::RopeArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.yq = static_cast<uint16_t*>(yq);
+    a.yk = static_cast<uint16_t*>(yk);
+    for (int i = 0; i < 3; ++i) {
+        a.q_stride[i] = p->q_stride[i];
+        a.k_stride[i] = p->k_stride[i];
+        a.yq_stride[i] = p->yq_stride[i];
+        a.yk_stride[i] = p->yk_stride[i];
+    }
+    a.s = p->s;
+    a.h_q = p->h_q;
+    a.h_kv = p->h_kv;
+    a.pos0 = p->pos0;
+    a.positions = p->positions;
+    a.sign = sign;
+    return ac::launch_rope(*reinterpret_cast<const ac::RopeTable*>(t), a, p->b, sms,
+                           reinterpret_cast<cudaStream_t>(stream))
+               ? ATTN_CORE_ERR_CUDA
+               : ATTN_CORE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_core_rope_init(const attn_core_rope_config* c, attn_core_rope_table* out)
+{
+    if (c == nullptr || out == nullptr) return ATTN_CORE_ERR_INVALID_ARG;
+    const int32_t rot = c->rot_dim ? c->rot_dim : (c->d < 256 ? c->d : 256);
+    attn_core_rope_table t{};
+    t.d = c->d;
+    t.rot_dim = rot;
+    t.interleaved = c->interleaved;
+    int rc = check_rope_table(&t);
+    if (rc) return rc;
+    const double base = c->base != 0.0 ? c->base : 10000.0;
+    const double factor = c->factor != 0.0 ? c->factor : 1.0;
+    const bool bands = c->low_freq != 0.0 || c->high_freq != 0.0;
+    const double low = bands ? c->low_freq : 1.0, high = bands ? c->high_freq : 4.0;
+    const bool betas = c->beta_fast != 0.0 || c->beta_slow != 0.0;
+    const double fast = betas ? c->beta_fast : 32.0, slow = betas ? c->beta_slow : 1.0;
+    const bool scaled = c->scaling != ATTN_CORE_ROPE_NONE;
+    if (c->scaling < ATTN_CORE_ROPE_NONE || c->scaling > ATTN_CORE_ROPE_YARN || !positive(base) || base <= 1.0 ||
+        !positive(factor) || (c->mscale != 0.0 && !positive(c->mscale)))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if ((c->scaling == ATTN_CORE_ROPE_BANDS || c->scaling == ATTN_CORE_ROPE_YARN) && !positive(c->original_len))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if (c->scaling == ATTN_CORE_ROPE_BANDS && !(low >= 0.0 && positive(high) && low < high))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if (c->scaling == ATTN_CORE_ROPE_YARN && !(positive(slow) && positive(fast) && slow < fast))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    double lo = 0.0, hi = 0.0;
+    if (c->scaling == ATTN_CORE_ROPE_YARN) {
+        lo = floor(rot * log(c->original_len / (fast * kTwoPi)) / (2.0 * log(base)));
+        hi = ceil(rot * log(c->original_len / (slow * kTwoPi)) / (2.0 * log(base)));
+        lo = lo > 0.0 ? lo : 0.0;
+        hi = hi < rot - 1 ? hi : rot - 1;
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        double keep = scaled ? 0.0 : 1.0;           // LINEAR slows every pair
+        if (c->scaling == ATTN_CORE_ROPE_BANDS)
+            keep = (c->original_len * f / kTwoPi - low) / (high - low);
+        else if (c->scaling == ATTN_CORE_ROPE_YARN)
+            keep = 1.0 - (i - lo) / (hi - lo > 0.001 ? hi - lo : 0.001);
+        keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+        f = keep * f + (1.0 - keep) * (f / factor);
+        // turns per position, whole turns dropped, as a 64-bit fraction
+        const double turn = fmod(f / kTwoPi, 1.0);
+        const double scaled_turn = ldexp(turn, 64);
+        t.turns[i] = scaled_turn >= 18446744073709549568.0 ? ~(uint64_t)0 : (uint64_t)scaled_turn;
+    }
+    double m = c->mscale;
+    if (m == 0.0) m = (c->scaling == ATTN_CORE_ROPE_YARN && factor > 1.0) ? 0.1 * log(factor) + 1.0 : 1.0;
+    t.mscale = (float)m;
+    *out = t;
+    return ATTN_CORE_OK;
+}
+
+int attn_core_rope_fwd(const attn_core_rope_params* p, const attn_core_rope_table* t, const void* q, const void* k,
+                       void* yq, void* yk, void* stream)
+{
+    return rope_call(p, t, q, k, yq, yk, 1.0f, stream);
+}
+
+int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_table* t, const void* dyq,
+                       const void* dyk, void* dq, void* dk, void* stream)
+{
+    return rope_call(p, t, dyq, dyk, dq, dk, -1.0f, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The paged cache: append, attention, page copies.
+namespace {
+
+int check_paged(const attn_core_paged_params* p)
+{
+    if (p == nullptr) return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->n_seq <= 0 || p->n_tokens < 0 || p->h_q <= 0 || p->h_kv <= 0 || p->d <= 0 || p->n_pages <= 0 ||
+        p->max_pages <= 0 || p->h_q % p->h_kv != 0)
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if (!p->cu_seqlens_q || !p->kv_lens || !p->page_table) return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->causal != 0 && p->causal != 1) return ATTN_CORE_ERR_INVALID_ARG;
+    if (isnan(p->scale) || isinf(p->scale)) return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->flags & ~ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) return ATTN_CORE_ERR_INVALID_ARG;
+    const int ps = p->page_size;
+    if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return ATTN_CORE_ERR_UNSUPPORTED;
+    if (!supported_d(p->d) || p->h_q / p->h_kv > kBlockRows) return ATTN_CORE_ERR_UNSUPPORTED;
+    // row counts that the kernels hold in 32 bits; element offsets are 64-bit
+    if ((int64_t)p->n_pages * p->h_kv >= (int64_t)INT32_MAX ||
+        (int64_t)p->max_pages * ps >= (int64_t)INT32_MAX - 2 * kBlockRows ||
+        (int64_t)p->n_tokens * p->h_q >= (int64_t)INT32_MAX)
+        return ATTN_CORE_ERR_INVALID_ARG;
+    for (const void* t : {(const void*)p->cu_seqlens_q, (const void*)p->kv_lens, (const void*)p->page_table})
+        if (reinterpret_cast<uintptr_t>(t) & 3u) return ATTN_CORE_ERR_MISALIGNED;
+    return ATTN_CORE_OK;
+}
+
+ac::PagedTables paged_tables(const attn_core_paged_params* p)
+{
+    ac::PagedTables t{};
+    t.cu_q = p->cu_seqlens_q;
+    t.kv_lens = p->kv_lens;
+    t.page_table = p->page_table;
+    t.n_seq = p->n_seq;
+    t.n_tokens = p->n_tokens;
+    t.h_q = p->h_q;
+    t.h_kv = p->h_kv;
+    t.page_size = p->page_size;
+    for (t.page_shift = 0; (1 << t.page_shift) < p->page_size;) ++t.page_shift;
+    t.n_pages = p->n_pages;
+    t.max_pages = p->max_pages;
+    t.status = p->dev_status;
+    return t;
+}
+
+int compare_ints(const void* a, const void* b)
+{
+    const int32_t x = *static_cast<const int32_t*>(a), y = *static_cast<const int32_t*>(b);
+    return x < y ? -1 : x > y;
+}
+
+// Every page in range, every target named once and no target a source.
+int check_pairs(const int32_t* pairs, int64_t n, int64_t n_pages)
+{
+    for (int64_t i = 0; i < 2 * n; ++i)
+        if (pairs[i] < 0 || pairs[i] >= n_pages) return ATTN_CORE_ERR_INVALID_ARG;
+    if (n > n_pages) return ATTN_CORE_ERR_INVALID_ARG;
+    if (n <= 16) {
+        for (int64_t i = 0; i < n; ++i)
+            for (int64_t j = 0; j < n; ++j)
+                if (pairs[2 * i + 1] == pairs[2 * j] || (i != j && pairs[2 * i + 1] == pairs[2 * j + 1]))
+                    return ATTN_CORE_ERR_INVALID_ARG;
+        return ATTN_CORE_OK;
+    }
+    int32_t* dst = static_cast<int32_t*>(malloc((size_t)n * sizeof(int32_t)));
+    if (dst == nullptr) return ATTN_CORE_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i) dst[i] = pairs[2 * i + 1];
+    qsort(dst, (size_t)n, sizeof(int32_t), compare_ints);
+    int rc = ATTN_CORE_OK;
+    for (int64_t i = 1; i < n && !rc; ++i)
+        if (dst[i] == dst[i - 1]) rc = ATTN_CORE_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n && !rc; ++i)
+        if (bsearch(&pairs[2 * i], dst, (size_t)n, sizeof(int32_t), compare_ints)) rc = ATTN_CORE_ERR_INVALID_ARG;
+    free(dst);
+    return rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope_table* t, const void* q,
+                           const void* k, const void* v, const int64_t* strides, void* q_out, void* k_pages,
+                           void* v_pages, void* stream)
+{
+    int rc = check_paged(p);
+    if (rc) return rc;
+    if (!k || !v || !k_pages || !v_pages || (q == nullptr) != (q_out == nullptr)) return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->flags) return ATTN_CORE_ERR_INVALID_ARG;   // no wait in this kernel to time out
+    if (t != nullptr) {
+        if ((rc = check_rope_table(t))) return rc;
+        if (t->d != p->d) return ATTN_CORE_ERR_INVALID_ARG;
+    }
+    const int64_t packed[3] = {(int64_t)p->h_q * p->d, (int64_t)p->h_kv * p->d, (int64_t)p->h_kv * p->d};
+    for (int i = 0; i < 3 && strides; ++i) {
+        if (i == 0 && !q) continue;
+        if (strides[i] < 0 || strides[i] > ((int64_t)1 << 42)) return ATTN_CORE_ERR_INVALID_ARG;
+        if (strides[i] % 8) return ATTN_CORE_ERR_MISALIGNED;
+    }
+    if (!strides) strides = packed;
+    if (q && q == q_out && strides[0] != packed[0]) return ATTN_CORE_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_pages, (const void*)v_pages})
+        if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
+    if (p->n_tokens == 0) return ATTN_CORE_OK;
+    if ((rc = check_device())) return rc;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    ac::AppendArgs a{};
+    a.t = paged_tables(p);
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q_stride = q ? strides[0] : 0;
+    a.k_stride = strides[1];
+    a.v_stride = strides[2];
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_pages = static_cast<uint16_t*>(k_pages);
+    a.v_pages = static_cast<uint16_t*>(v_pages);
+    ac::RopeTable none{};            // no rotation: every unit is a copy
+    none.d = p->d;
+    none.mscale = 1.0f;
+    const ac::RopeTable& rt = t ? *reinterpret_cast<const ac::RopeTable*>(t) : none;
+    return ac::launch_append(rt, a, sms, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
+}
+
+size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p)
+{
+    return check_paged(p) ? 0 : ac::paged_ws_bytes(p->d);
+}
+
+int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = check_paged(p);
+    if (rc) return rc;
+    if (!q || !k_pages || !v_pages || !o || !lse || !workspace) return ATTN_CORE_ERR_INVALID_ARG;
+    for (const void* x : {q, k_pages, v_pages, (const void*)o, (const void*)lse})
+        if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_CORE_ERR_MISALIGNED;
+    if (workspace_bytes < ac::paged_ws_bytes(p->d)) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
+    if (p->n_tokens == 0) return ATTN_CORE_OK;
+    if ((rc = check_device())) return rc;
+    ac::PagedArgs a{};
+    a.t = paged_tables(p);
+    a.q = static_cast<const uint16_t*>(q);
+    a.k_pages = static_cast<const uint16_t*>(k_pages);
+    a.v_pages = static_cast<const uint16_t*>(v_pages);
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.d = p->d;
+    a.causal = p->causal;
+    const float scale = (p->scale > 0.0f) ? p->scale : 1.0f / sqrtf((float)p->d);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    return ac::launch_paged(a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
+}
+
+int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,
+                        const int32_t* pairs, int64_t n_pairs, void* stream)
+{
+    if (!pages || n_planes <= 0 || n_pages <= 0 || n_pages > (int64_t)INT32_MAX || page_bytes <= 0 || n_pairs < 0 ||
+        (n_pairs > 0 && !pairs))
+        return ATTN_CORE_ERR_INVALID_ARG;
+    // sizes whose products stay in range (65535: blocks in y; 2 GiB a page)
+    if (n_planes > 65535 || page_bytes > ((int64_t)1 << 31)) return ATTN_CORE_ERR_UNSUPPORTED;
+    if (!aligned16(pages) || page_bytes % 16 || plane_stride % 16) return ATTN_CORE_ERR_MISALIGNED;
+    if (n_planes > 1 && plane_stride < n_pages * page_bytes) return ATTN_CORE_ERR_INVALID_ARG;
+    int rc = check_pairs(pairs, n_pairs, n_pages);
+    if (rc) return rc;
+    if (n_pairs == 0) return ATTN_CORE_OK;
+    if ((rc = check_device())) return rc;
+    return ac::launch_page_copy(pages, n_planes, plane_stride, page_bytes, pairs, n_pairs,
+                                reinterpret_cast<cudaStream_t>(stream))
+               ? ATTN_CORE_ERR_CUDA
+               : ATTN_CORE_OK;
 }
 
 }  // extern "C"

@@ -226,6 +226,70 @@ int launch_dal_bwd(const DalArgs& a, int sms, cudaStream_t stream);
 int launch_gelu_fwd(const uint16_t* x, uint16_t* y, int64_t n, int sms, cudaStream_t stream);
 int launch_gelu_bwd(const uint16_t* x, const uint16_t* dy, uint16_t* dx, int64_t n, int sms, cudaStream_t stream);
 
+// Rotary positions (rope.cu).  The table as attn_core_rope_table holds it.
+struct RopeTable {
+    int32_t d, rot, interleaved;
+    float mscale;
+    uint64_t turns[128];
+};
+struct RopeArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    uint16_t* yq;
+    uint16_t* yk;
+    int64_t q_stride[3], k_stride[3], yq_stride[3], yk_stride[3];   // batch, head, token; elements
+    int32_t s, h_q, h_kv;
+    int32_t pos0;
+    const int32_t* positions;   // [b, s], or null
+    float sign;                 // 1 forward, -1 backward
+    int32_t tile;               // tokens per block (set by the launcher)
+};
+int launch_rope(const RopeTable& t, RopeArgs& a, int b, int sms, cudaStream_t stream);
+
+// A batch of sequences whose keys and values live in pages: device tables and
+// the sizes that bound them.  The kernels check every entry they use against
+// those sizes and report kStatusTable in the caller's status word.
+constexpr int32_t kStatusTable = 7;   // ATTN_CORE_ERR_DEVICE_TABLE
+struct PagedTables {
+    const int32_t* cu_q;        // [n_seq + 1]
+    const int32_t* kv_lens;     // [n_seq]
+    const int32_t* page_table;  // [n_seq, max_pages]
+    int32_t n_seq, n_tokens, h_q, h_kv;
+    int32_t page_size, page_shift;   // page_size == 1 << page_shift
+    int32_t n_pages, max_pages;
+    int32_t* status;            // may be null
+};
+struct AppendArgs {
+    PagedTables t;
+    const uint16_t* q;          // may be null
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_stride, k_stride, v_stride;   // elements from one token to the next
+    uint16_t* q_out;
+    uint16_t* k_pages;
+    uint16_t* v_pages;
+    int32_t tile;               // tokens per block (set by the launcher)
+};
+int launch_append(const RopeTable& t, AppendArgs& a, int sms, cudaStream_t stream);
+
+// Attention of new tokens over the pages (paged.cu).
+struct PagedArgs {
+    PagedTables t;
+    const uint16_t* q;
+    const uint16_t* k_pages;
+    const uint16_t* v_pages;
+    uint16_t* o;
+    float* lse;
+    int32_t d, causal;
+    float scale_log2;           // score scale * log2(e)
+};
+size_t paged_ws_bytes(int d);
+int launch_paged(const PagedArgs& a, cudaStream_t stream);
+
+// Page copies (pages.cu): `pairs` is a host array.
+int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,
+                     int64_t n_pairs, cudaStream_t stream);
+
 // Query-tile height of the dK/dV kernel for head dimension d (TMEM budget).
 constexpr int dkdv_query_tile(int d) { return (2 * d + 2 * 128 <= 512) ? 128 : 64; }
 // Key-block width of the dQ kernel for head dimension d (TMEM budget:

@@ -65,6 +65,7 @@ extern "C" {
 #define ATTN_CORE_ERR_WORKSPACE_TOO_SMALL 4 /* bwd workspace smaller than attn_core_bwd_workspace_bytes */
 #define ATTN_CORE_ERR_CUDA 5                /* a CUDA runtime or driver call failed */
 #define ATTN_CORE_ERR_DEVICE_TIMEOUT 6      /* a kernel wait ran past its limit (reported via dev_status) */
+#define ATTN_CORE_ERR_DEVICE_TABLE 7        /* a device table held an entry out of range (reported via dev_status) */
 
 /* flags */
 #define ATTN_CORE_FLAG_REDRAW_MASK 0x1         /* backward: the dK/dV kernel draws the dropout mask again
@@ -308,6 +309,157 @@ int attn_core_dropout_add_ln_bwd(const attn_core_dal_params* p, const void* dy, 
  * each, asynchronous on `stream`. */
 int attn_core_gelu_fwd(int64_t n, const void* x, void* y, void* stream);
 int attn_core_gelu_bwd(int64_t n, const void* x, const void* dy, void* dx, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  Pair i of a head's first rot_dim values, (x_a, x_b), is
+ * turned by the angle w = position * f_i:
+ *     y_a = m (x_a cos w - x_b sin w),   y_b = m (x_b cos w + x_a sin w),
+ * with (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.  The
+ * values from rot_dim on are copied.  A score of two rotated heads depends on
+ * the difference of their positions only.  f_i = base^(-2i / rot_dim) radians
+ * per position, then scaled for contexts longer than the trained one:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   BANDS   with n = original_len f_i / 2 pi (turns over the trained length)
+ *           and k = clamp((n - low_freq) / (high_freq - low_freq), 0, 1):
+ *           k f_i + (1 - k) f_i / factor
+ *   YARN    ("YaRN: Efficient Context Window Extension", Peng et al. 2023)
+ *           with c(n) = rot_dim ln(original_len / 2 pi n) / (2 ln base), the
+ *           pair that turns n times over the trained length,
+ *           lo = max(floor(c(beta_fast)), 0),
+ *           hi = min(ceil(c(beta_slow)), rot_dim - 1) and
+ *           k = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):
+ *           (1 - k) f_i + k f_i / factor, and m = 0.1 ln(factor) + 1
+ * m = 1 unless YARN or `mscale` sets it. */
+#define ATTN_CORE_ROPE_NONE 0
+#define ATTN_CORE_ROPE_LINEAR 1
+#define ATTN_CORE_ROPE_BANDS 2
+#define ATTN_CORE_ROPE_YARN 3
+
+typedef struct {
+    int32_t d;            /* head dimension, multiple of 8, 8 .. 512 */
+    int32_t rot_dim;      /* rotated leading part, multiple of 8, at most min(d, 256); 0 selects that */
+    int32_t interleaved;  /* 0 or 1 */
+    int32_t scaling;      /* ATTN_CORE_ROPE_* */
+    double base;          /* > 1; 0 selects 10000 */
+    double factor;        /* > 0; 0 selects 1 */
+    double original_len;  /* trained context length, > 0 for BANDS and YARN */
+    double low_freq, high_freq;     /* BANDS, low < high; both 0 select 1 and 4 */
+    double beta_fast, beta_slow;    /* YARN, slow < fast; both 0 select 32 and 1 */
+    double mscale;        /* m, > 0; 0 selects 1 (YARN: 0.1 ln(factor) + 1, at least 1) */
+} attn_core_rope_config;
+
+/* The frequencies as the kernels take them, filled by attn_core_rope_init and
+ * passed by value to each launch: turns[i] is f_i / 2 pi turns per position
+ * as a 64-bit fraction, so that position * turns[i] modulo 2^64 is the angle
+ * reduced exactly, at any position. */
+typedef struct {
+    int32_t d, rot_dim, interleaved;
+    float mscale;
+    uint64_t turns[128];
+} attn_core_rope_table;
+
+int attn_core_rope_init(const attn_core_rope_config* c, attn_core_rope_table* out);   /* pure host */
+
+/* Rotation of Q and K in one launch, over any layout whose heads are
+ * contiguous in d: element (batch, head, token, c) of a tensor is at
+ * batch * stride[0] + head * stride[1] + token * stride[2] + c.  Strides are
+ * in elements, non-negative multiples of 8; an input's may be 0 (a broadcast
+ * tensor), an output's must keep its rows apart.  [b, h, s, d] is
+ * {h s d, s d, d}; a packed [tokens, h, d] is b = 1, {0, d, h d}.  Pointers are
+ * 16-byte aligned.  An output may be its own input (same pointer and strides),
+ * otherwise it overlaps no input.  h_q or h_kv may be 0 (its pointers are then
+ * ignored); s = 0 does nothing. */
+typedef struct {
+    int32_t b, s, h_q, h_kv;
+    int64_t q_stride[3], k_stride[3];     /* inputs: batch, head, token */
+    int64_t yq_stride[3], yk_stride[3];   /* outputs */
+    int32_t pos0;                         /* position of token 0 where `positions` is NULL */
+    const int32_t* positions;             /* device int32 [b, s] (negative ones turn back), or NULL: pos0 + token */
+} attn_core_rope_params;
+
+int attn_core_rope_fwd(const attn_core_rope_params* p, const attn_core_rope_table* t, const void* q, const void* k,
+                       void* yq, void* yk, void* stream);
+
+/* Backward: dq, dk from the gradients of the rotated tensors.  The rotation is
+ * orthogonal up to m, so this is the turn by -w, times m. */
+int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_table* t, const void* dyq,
+                       const void* dyk, void* dq, void* dk, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A key/value cache in pages, and attention of new tokens over it (serving).
+ *   k_pages, v_pages : bf16 [n_pages, h_kv, page_size, d]
+ *   q, o             : bf16 [n_tokens, h_q, d]    packed new tokens
+ *   lse              : fp32 [h_q, n_tokens]
+ * Sequence i owns the new tokens cu_seqlens_q[i] .. cu_seqlens_q[i + 1] - 1 (n
+ * of them) and kv_lens[i] keys, the new tokens' own among them; key j is row
+ * j % page_size of page page_table[i * max_pages + j / page_size].  New token
+ * t has position kv_lens[i] - n + t and, under the causal mask (aligned
+ * bottom-right), sees the keys up to that position; without it, all of them.
+ * A row that sees no key (kv_lens[i] < n, or no keys at all) gets O = 0 and
+ * LSE = -inf.  Tokens from cu_seqlens_q[n_seq] on belong to no sequence: their
+ * rows are left as they were.  What pages hold past a sequence's end is never
+ * used, NaN included, nor are page_table entries past its last page.  Values
+ * of keys that are visible to some row of a 128-row tile must be finite.
+ *
+ * The three tables are in device memory and read by the kernels only, so a
+ * captured graph follows them: one capture serves every step as long as the
+ * sizes in this struct stay.  The kernels check them: an entry out of range (a
+ * page outside the cache, lengths that are negative, decrease or exceed
+ * n_tokens or max_pages * page_size) writes ATTN_CORE_ERR_DEVICE_TABLE to
+ * dev_status, touches nothing outside the tensors, and leaves that sequence's
+ * results undefined. */
+typedef struct {
+    int32_t n_seq;          /* >= 1 */
+    int32_t n_tokens;       /* rows of q and o; 0: nothing to do */
+    int32_t h_q, h_kv, d;   /* h_q % h_kv == 0, h_q / h_kv <= 128, d in {64, 96, 128, 160} */
+    int32_t page_size;      /* 16, 32, 64, 128 or 256 */
+    int32_t n_pages;        /* pages in the cache */
+    int32_t max_pages;      /* entries per sequence in page_table */
+    int32_t causal;         /* 0 or 1 */
+    float scale;            /* score scale; <= 0 selects 1/sqrtf(d) */
+    const int32_t* cu_seqlens_q;   /* device [n_seq + 1], from 0, nondecreasing */
+    const int32_t* kv_lens;        /* device [n_seq] */
+    const int32_t* page_table;     /* device [n_seq, max_pages] */
+    int32_t* dev_status;           /* as attn_core_params; may be NULL */
+    int32_t flags;                 /* 0 or ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT */
+    uint32_t wait_timeout_ms;      /* limit of each in-kernel wait; 0 selects 2000 ms */
+} attn_core_paged_params;
+
+/* Adds the new tokens to the cache, rotating Q and K on the way (`t`; NULL for
+ * no rotation, its d must equal p's): writes q_out [n_tokens, h_q, d] and the
+ * new tokens' rows of the pages, nothing else.  strides (host; NULL for packed
+ * tensors): elements from one token to the next of q, k and v, multiples of 8
+ * -- slices of a fused [tokens, (h_q + 2 h_kv) d] projection qualify.  q and
+ * q_out may both be NULL (only the cache is written), and q_out may be q if q
+ * is packed.  No two new tokens may share a cache row (a page that two
+ * sequences share is copied before either appends to it).  One kernel. */
+int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope_table* t, const void* q,
+                           const void* k, const void* v, const int64_t* strides, void* q_out, void* k_pages,
+                           void* v_pages, void* stream);
+
+/* Attention of the new tokens over the cache (which already holds their own
+ * keys and values): O and LSE.  `workspace`: caller-owned device memory of at
+ * least attn_core_paged_workspace_bytes(p) bytes, 256-byte aligned, for the
+ * partial results of rows whose keys are shared out among thread blocks; its
+ * contents on entry do not matter, and calls (or graph replays) that may overlap on the GPU need
+ * one each.  The size depends on h_q / h_kv's and the tables' values not at
+ * all: only on d.  Results do not depend on timing (no atomics): the same
+ * inputs give the same bits on the same device. */
+size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p);
+int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Copies pages inside a cache: page pairs[2i + 1] <- page pairs[2i], in every
+ * plane (one per layer and per K or V; a plane holds n_pages pages of
+ * page_bytes and starts plane_stride bytes after the one before).  Forking a
+ * sequence copies its last, partly filled page; compaction moves pages to the
+ * free places of lower number.  `pairs` is a host array, consumed by the call
+ * (a captured graph keeps the copies it was captured with).  The copies run in
+ * no order, so each target is named once and is no copy's source: anything
+ * else is refused.  page_bytes and plane_stride are multiples of 16. */
+int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,
+                        const int32_t* pairs, int64_t n_pairs, void* stream);
 
 #ifdef __cplusplus
 }
