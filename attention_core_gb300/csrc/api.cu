@@ -160,6 +160,22 @@ int encode_map_strided(CUtensorMap* m, const void* ptr, int d, int s, int64_t he
     return r == CUDA_SUCCESS ? ATTN_CORE_OK : ATTN_CORE_ERR_CUDA;
 }
 
+// 4-D map over [tokens][kv heads][group][d] bf16: box = one column chunk of the
+// `group` rows of one KV head of `tpt` tokens, swizzled as encode_map_strided's.
+int encode_map_rows4(CUtensorMap* m, const void* ptr, int d, int group, int kv_heads, int64_t tokens, int tpt)
+{
+    const int cw = (d % 64 == 0) ? 64 : 32;
+    const CUtensorMapSwizzle sw = (cw == 64) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)kv_heads, (cuuint64_t)tokens};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)group * d * 2, (cuuint64_t)kv_heads * group * d * 2};
+    cuuint32_t box[4] = {(cuuint32_t)cw, (cuuint32_t)group, 1, (cuuint32_t)tpt};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_CORE_OK : ATTN_CORE_ERR_CUDA;
+}
+
 // Where the query-side (Q, O, dO, dQ) and key-side (K, V, dK, dV) rows of one
 // launch live, and where its LSE rows go.
 struct Geometry {
@@ -1049,18 +1065,32 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
     if (workspace_bytes < ac::paged_ws_bytes(p->d)) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
     if (p->n_tokens == 0) return ATTN_CORE_OK;
     if ((rc = check_device())) return rc;
+    if ((rc = get_encoder())) return rc;
     ac::PagedArgs a{};
     a.t = paged_tables(p);
-    a.q = static_cast<const uint16_t*>(q);
-    a.k_pages = static_cast<const uint16_t*>(k_pages);
-    a.v_pages = static_cast<const uint16_t*>(v_pages);
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
+    a.ws = static_cast<uint8_t*>(workspace);
     a.d = p->d;
     a.causal = p->causal;
+    a.group = p->h_q / p->h_kv;
+    a.tpt = ac::paged_tokens_per_tile(a.group);
     const float scale = (p->scale > 0.0f) ? p->scale : 1.0f / sqrtf((float)p->d);
     a.scale_log2 = scale * 1.44269504088896340736f;
-    return ac::launch_paged(a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
+    a.timeout_ns = (uint64_t)(p->wait_timeout_ms ? p->wait_timeout_ms : 2000u) * 1000000ull;
+    a.inject_timeout = (p->flags & ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
+    if ((rc = device_sms(&a.num_sms))) return rc;
+    // Pages: rows of one KV head of one page, [n_pages * h_kv][page_size][d].
+    // Q: the group's heads of a run of tokens, [n_tokens][h_kv][group][d].
+    CUtensorMap tq, tk, tv;
+    const int box = p->page_size < kBlockRows ? p->page_size : kBlockRows;
+    const int64_t page_rows = (int64_t)p->n_pages * p->h_kv, page_elems = (int64_t)p->page_size * p->d;
+    if ((rc = encode_map_strided(&tk, k_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
+        (rc = encode_map_strided(&tv, v_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
+        (rc = encode_map_rows4(&tq, q, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)))
+        return rc;
+    return ac::launch_paged(tq, tk, tv, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA
+                                                                                  : ATTN_CORE_OK;
 }
 
 int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,

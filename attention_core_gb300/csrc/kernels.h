@@ -275,16 +275,20 @@ int launch_append(const RopeTable& t, AppendArgs& a, int sms, cudaStream_t strea
 // Attention of new tokens over the pages (paged.cu).
 struct PagedArgs {
     PagedTables t;
-    const uint16_t* q;
-    const uint16_t* k_pages;
-    const uint16_t* v_pages;
-    uint16_t* o;
-    float* lse;
+    uint16_t* o;                // bf16 [n_tokens, h_q, d]
+    float* lse;                 // [h_q, n_tokens]
+    uint8_t* ws;                // paged_ws_bytes(d)
     int32_t d, causal;
+    int32_t group, tpt;         // h_q / h_kv, and new tokens per tile of 128 rows
     float scale_log2;           // score scale * log2(e)
+    uint64_t timeout_ns;
+    int32_t inject_timeout;
+    int32_t num_sms;
 };
 size_t paged_ws_bytes(int d);
-int launch_paged(const PagedArgs& a, cudaStream_t stream);
+int paged_tokens_per_tile(int group);
+int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                 cudaStream_t stream);
 
 // Page copies (pages.cu): `pairs` is a host array.
 int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,

@@ -1,89 +1,755 @@
 // paged.cu -- attention of new tokens over a paged key/value cache on sm_103a.
 //
-// O = softmax(scale q K^T + mask) V and LSE, per (new token, query head).
-// One warp per row: lanes take a key each for the scores and a slice of d for
-// the sums, 32 keys at a time, with a running maximum and sum in fp32.
+//     O = softmax(scale q K^T + mask) V,  LSE,  per (new token, query head),
+// with K and V of a sequence in pages of 16 .. 256 keys.  One kernel for every
+// case, from one token of one sequence to chunks of thousands: the query heads
+// that share a KV head and up to 128 / group tokens form the 128 rows of a
+// tile, so a KV head's pages are read once per tile, not once per head.
+//
+// Bounds: with few rows per KV head (single tokens) the pages' bytes over HBM;
+// with many, the row work of the softmax beside the two products of each
+// 128 x 128 block.  The tile is M = 128 in both: with 8 live rows the padded
+// products still take less time (about 1000 cycles a block at d = 128) than the
+// block's 64 KB take to arrive at one SM's share of HBM (about 2700), and warps
+// without a live row skip the softmax.
+//
+// Persistent, one CTA per SM; each takes an equal share of all blocks
+// (paged_sched.cuh), cutting long tiles.  Structure (384 threads), as the
+// forward of the core:
+//   warp 0  K: lane i loads page i of a block (its page_table entry and one TMA
+//           per column chunk); lane 31 also each tile's Q
+//   warp 2  V, into its own ring; rows past the sequence's end are zeroed in
+//           shared memory, so that what the page holds there (NaN included)
+//           meets no product
+//   warp 1  issues the tcgen05 MMAs: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}
+//           with P read from TMEM
+//   warps 4-11  online softmax, one row per TMEM lane, two column halves of 64
+//           keys; for d <= 128 each half keeps its own maximum, sum and O
+//           accumulator, merged at the tile's end; for d = 160 TMEM has room
+//           for one accumulator and the halves exchange their block maxima
+// Probabilities are rounded to bf16 for the product (the row sum is taken
+// before), everything else is fp32; the running maximum moves only when it
+// grows by more than 2^8.
+//
+// A whole tile's rows go to O; a cut tile's parts go to the workspace as fp32
+// rows divided by their own sum, with their own base-2 LSE, and a second kernel
+// joins them: O = sum_p w_p O_p / sum_p w_p, w_p = 2^(lse_p - max).
 #include "kernels.h"
+#include "paged_sched.cuh"
 #include "ptx.cuh"
+#include "tile.cuh"
 
 namespace ac {
 
+namespace {
+
+constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_simple_kernel(const PagedArgs a)
+struct PagedCfg {
+    using G = TileGeom<D>;
+    static constexpr uint32_t TILE = G::template tile_bytes<128>();
+    static constexpr uint32_t CHUNK = G::template chunk_bytes<128>();
+    static constexpr int NQ = (D <= 128) ? 2 : 1;
+    static constexpr int ST = (D <= 64) ? 5 : (D <= 96 ? 3 : 2);
+    static constexpr bool SPLIT = (D <= 128);
+    static constexpr uint32_t OFF_Q = 0;
+    static constexpr uint32_t OFF_K = NQ * TILE;
+    static constexpr uint32_t OFF_V = OFF_K + ST * TILE;
+    static constexpr uint32_t OFF_BAR = OFF_V + ST * TILE;
+    static constexpr uint32_t BAR_BYTES = 512;
+    static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
+    static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
+    static constexpr uint32_t SMEM = OFF_XCH + XCH_BYTES + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory budget");
+    static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O = 256, T_O1 = 256 + D, T_X = 256 + D;
+    static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
+};
+
+struct PagedBars {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t v_tail;        // a tile's last, partial V block has landed (rows past its end still to be zeroed)
+    uint64_t s_full[2];
+    uint64_t p_full[2];     // d = 160: P of the block is in TMEM
+    uint64_t p_half[2][2];  // SPLIT: [score buffer][half] P of the half is in TMEM
+    uint64_t o_half[2];     // SPLIT: the half's P.V of the block is done
+    uint64_t o_done;        // d = 160: the block's P.V is done
+    uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
+    uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
+    uint64_t o_free;        // the tile's O has been read
+    uint64_t o_tile;        // the tile's last P.V is done
+    uint64_t drain;
+    uint64_t never;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int64_t line_units;             // T
+    int64_t start_rel;              // where this CTA's share starts: units into start_seq
+    int32_t start_seq;
+    int32_t warp_sum_pad;
+    int64_t warp_sum[kThreads / 32];
+};
+static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
+
+enum : int32_t {
+    kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
+    kSitePFull, kSiteSFull, kSiteODone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteOTile, kSiteDrain
+};
+__device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                                            uint32_t bar)
 {
-    const PagedTables& t = a.t;
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= (int64_t)t.n_tokens * t.h_q) return;
-    const int tok = (int)(row / t.h_q), head = (int)(row % t.h_q);
-    int seq = 0;
-    while (seq < t.n_seq && t.cu_q[seq + 1] <= tok) ++seq;
-    if (seq >= t.n_seq) return;
-    const int q0 = t.cu_q[seq], q1 = t.cu_q[seq + 1], kv = t.kv_lens[seq];
-    if (q0 < 0 || tok < q0 || q1 > t.n_tokens || kv < 0 || kv > (int64_t)t.max_pages * t.page_size) {
-        if (t.status) atomicCAS(t.status, 0, kStatusTable);
-        return;
-    }
-    const int64_t seen64 = a.causal ? (int64_t)kv - q1 + tok + 1 : kv;
-    const int seen = (int)(seen64 < 0 ? 0 : seen64);
-    for (int c = lane; c < D; c += 32) qs[warp][c] = __uint_as_float((uint32_t)a.q[row * D + c] << 16);
-    __syncwarp();
-    const int hk = head / (t.h_q / t.h_kv);
-    float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-    for (int j0 = 0; j0 < seen; j0 += 32) {
-        const int j = j0 + lane;
-        int64_t base = 0;
-        float x = -INFINITY;
-        if (j < seen) {
-            const int page = t.page_table[(int64_t)seq * t.max_pages + (j >> t.page_shift)];
-            if (page < 0 || page >= t.n_pages) {
-                if (t.status) atomicCAS(t.status, 0, kStatusTable);
-            } else {
-                base = (((int64_t)page * t.h_kv + hk) * t.page_size + (j & (t.page_size - 1))) * D;
-            }
-            float dot = 0.f;
-            for (int c = 0; c < D; ++c) dot += qs[warp][c] * __uint_as_float((uint32_t)a.k_pages[base + c] << 16);
-            x = dot * a.scale_log2;
-        }
-        float mx = x;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_new = fmaxf(m, mx);
-        const float f = exp2f(m - m_new);
-        const float p = exp2f(x - m_new);
-        l *= f;
-        for (int e = 0; e < D / 32; ++e) acc[e] *= f;
-        float ps = p;
-        for (int o = 16; o; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l += ps;
-        m = m_new;
-        for (int i = 0; i < 32 && j0 + i < seen; ++i) {
-            const float pi = __shfl_sync(0xffffffffu, p, i);
-            const int64_t bi = __shfl_sync(0xffffffffu, base, i);
-            for (int e = 0; e < D / 32; ++e)
-                acc[e] += pi * __uint_as_float((uint32_t)a.v_pages[bi + e * 32 + lane] << 16);
-        }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int e = 0; e < D / 32; ++e)
-        a.o[row * D + e * 32 + lane] = (uint16_t)(pack_bf16x2(acc[e] * inv, 0.f) & 0xffffu);
-    if (lane == 0)
-        a.lse[(int64_t)head * t.n_tokens + tok] = l > 0.f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
 }
 
-size_t paged_ws_bytes(int) { return 256; }
+// What the join needs to know of a cut tile, written by the CTA that has its
+// first part (slot 1 of its own two; the later parts are in slot 0 of the CTAs
+// after it).
+struct CutTile {
+    int32_t last_cta;    // 0: this CTA cut no tile at its end
+    int32_t q_tok, n_rows, head;
+};
 
-int launch_paged(const PagedArgs& a, cudaStream_t st)
+// Workspace: parts [CTA][slot] of 128 fp32 rows, their base-2 LSEs, CutTile [CTA].
+__host__ __device__ inline size_t part_row(int cta, int slot) { return ((size_t)cta * 2 + slot) * 128; }
+__host__ __device__ inline size_t ws_lse_offset(int d) { return (size_t)kPagedMaxCtas * 2 * 128 * d * sizeof(float); }
+__host__ __device__ inline size_t ws_cut_offset(int d)
 {
-    const unsigned grid = (unsigned)(((int64_t)a.t.n_tokens * a.t.h_q + 3) / 4);
+    return ws_lse_offset(d) + (size_t)kPagedMaxCtas * 2 * 128 * sizeof(float);
+}
+
+// The next segment with blocks to visit (the others only have zeros to write,
+// which is the row threads' business).
+__device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, Segment& g)
+{
+    while (w.next(t, g))
+        if (g.j1 > g.j0) return true;
+    return false;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const PagedArgs a)
+{
+    using G = TileGeom<D>;
+    using C = PagedCfg<D>;
+    constexpr int ST = C::ST;
+    const PagedTables& t = a.t;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    const uint32_t sb = raw + pad;
+    PagedBars* bars = reinterpret_cast<PagedBars*>(smem_raw + pad + C::OFF_BAR);
+    auto bar = [](uint64_t& b) { return smem_u32(&b); };
+    const uint32_t warp = warp_id(), lane = lane_id();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(bars->q_full[i]), 1);
+            mbar_init(bar(bars->q_empty[i]), 1);
+            mbar_init(bar(bars->s_full[i]), 1);
+            mbar_init(bar(bars->p_full[i]), kRowThreads);
+            mbar_init(bar(bars->xmax[i]), kRowThreads);
+            mbar_init(bar(bars->p_half[i][0]), kRowThreads / 2);
+            mbar_init(bar(bars->p_half[i][1]), kRowThreads / 2);
+            mbar_init(bar(bars->o_half[i]), 1);
+        }
+        for (int st = 0; st < ST; ++st) {
+            mbar_init(bar(bars->k_full[st]), 1);
+            mbar_init(bar(bars->k_empty[st]), 1);
+            mbar_init(bar(bars->v_full[st]), 1);
+            mbar_init(bar(bars->v_empty[st]), 1);
+        }
+        mbar_init(bar(bars->v_tail), 1);
+        mbar_init(bar(bars->o_done), 1);
+        mbar_init(bar(bars->o_free), kRowThreads);
+        mbar_init(bar(bars->o_tile), 1);
+        mbar_init(bar(bars->drain), 1);
+        mbar_init(bar(bars->lsum), kRowThreads);
+        mbar_init(bar(bars->lsum2), kRowThreads);
+        mbar_init(bar(bars->never), 1);
+        bars->abort_flag = 0;
+        bars->start_seq = -1;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+
+    // ---- this CTA's share of the line: thread i sums the units of its run of
+    // sequences, the block sums those, and the run that holds the share's first
+    // unit finds the sequence.
+    const int run = (t.n_seq + kThreads - 1) / kThreads;
+    const int s0 = (int)threadIdx.x * run < t.n_seq ? (int)threadIdx.x * run : t.n_seq;
+    const int s1 = s0 + run < t.n_seq ? s0 + run : t.n_seq;
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const SeqTable q = read_seq(t, s, a.tpt, a.causal);
+        if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
+        mine += q.s.units(q.s.tiles()) * t.h_kv;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((int)lane >= o) upto += x;
+    }
+    if (lane == 31) bars->warp_sum[warp] = upto;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t x = bars->warp_sum[w];
+        if (w < (int)warp) upto += x;
+        total += x;
+    }
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    per = per > kMinUnits ? per : kMinUnits;
+    const int64_t u0 = (int64_t)blockIdx.x * per;
+    const int64_t u1 = u0 + per < total ? u0 + per : total;
+    if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
+        int64_t rel = u0 - (upto - mine);
+        for (int s = s0; s < s1; ++s) {
+            const SeqTable q = read_seq(t, s, a.tpt, a.causal);
+            const int64_t n = q.s.units(q.s.tiles()) * t.h_kv;
+            if (rel < n) {
+                bars->start_seq = s;
+                bars->start_rel = rel;
+                break;
+            }
+            rel -= n;
+        }
+    }
+    CutTile* cut = reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D)) + blockIdx.x;
+    if (threadIdx.x == 0) cut->last_cta = 0;
+    __syncthreads();
+    const uint32_t tmem = bars->tmem_base;
+    const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
+    SegmentWalk walk;
+    walk.tpt = a.tpt;
+    walk.causal = a.causal;
+    walk.at = walk.end = 0;
+    if (u0 < u1) walk.start(t, bars->start_seq, bars->start_rel, u0, u1);
+    const int group = a.group;
+
+    bool alive = true;
+    if (a.inject_timeout) alive = wait_bounded(wc, bar(bars->never), 0, timeout_code(kSiteInject));
+
+    if (alive && (warp == 0 || warp == 2)) {
+        // ---- TMA producers.  A block's pages go to one lane each: the lane reads
+        // the page's table entry (before the wait for the ring slot, which hides
+        // it) and issues its column chunks.  A page outside the cache reads as
+        // zeros (coordinates outside the tensor map) and is reported.
+        const bool is_v = warp == 2;
+        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        uint64_t* full = is_v ? bars->v_full : bars->k_full;
+        uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+        const uint32_t ring = sb + (is_v ? C::OFF_V : C::OFF_K);
+        const int rows_pp = t.page_size < 128 ? t.page_size : 128;     // rows of a block from one page
+        int gi = 0, u = 0, tails = 0;
+        bool ok = true;
+        Segment g;
+        while (ok && next_work(walk, t, g)) {
+            if (!is_v) {
+                // the tile's Q as soon as its buffer is free
+                const int qs = u % C::NQ;
+                ok = wait_warp(wc, bar(bars->q_empty[qs]), ((u / C::NQ) & 1) ^ 1, timeout_code(kSiteQEmpty));
+                if (!ok) break;
+                if (lane == 31) {
+                    mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * G::ROWB * G::NCH);
+                    for (int ch = 0; ch < G::NCH; ++ch)
+                        tma_load_4d(sb + C::OFF_Q + qs * C::TILE + ch * C::CHUNK, &tm_q, ch * G::CW, 0, g.head, g.q_tok,
+                                    bar(bars->q_full[qs]));
+                }
+                __syncwarp();
+                ++u;
+            }
+            for (int j = g.j0; j < g.j1; ++j, ++gi) {
+                const int st = gi % ST;
+                const int rows = g.kv - j * 128 < 128 ? g.kv - j * 128 : 128;     // keys of the block
+                const int pages = (rows + rows_pp - 1) / rows_pp;
+                int page = -1, row = 0;
+                if ((int)lane < pages) {
+                    const int key = j * 128 + (int)lane * rows_pp;
+                    page = t.page_table[(int64_t)g.seq * t.max_pages + (key >> t.page_shift)];
+                    row = key & (t.page_size - 1);
+                    if (page < 0 || page >= t.n_pages) {
+                        page = -1;
+                        if (t.status) atomicCAS(t.status, 0, kStatusTable);
+                    }
+                }
+                ok = wait_warp(wc, bar(empty[st]), ((gi / ST) & 1) ^ 1,
+                               timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
+                if (!ok) break;
+                const bool tail = is_v && rows < 128;
+                const uint32_t land = bar(tail ? bars->v_tail : full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages * rows_pp) * G::ROWB * G::NCH);
+                __syncwarp();
+                if ((int)lane < pages) {
+                    const int z = page < 0 ? -1 : page * t.h_kv + g.head;
+                    const uint32_t dst = ring + st * C::TILE + (uint32_t)((int)lane * rows_pp) * G::ROWB;
+                    for (int ch = 0; ch < G::NCH; ++ch) tma_load_3d(dst + ch * C::CHUNK, tm, ch * G::CW, row, z, land);
+                }
+                __syncwarp();
+                if (tail) {
+                    ok = wait_warp(wc, land, tails & 1, timeout_code(kSiteVTail));
+                    if (!ok) break;
+                    ++tails;
+                    // rows [rows, 128) of every chunk are contiguous
+                    const uint32_t n16 = (uint32_t)(128 - rows) * (G::ROWB / 16);
+                    for (int ch = 0; ch < G::NCH; ++ch)
+                        for (uint32_t i = lane; i < n16; i += 32)
+                            st_shared_v4(ring + st * C::TILE + ch * C::CHUNK + (uint32_t)rows * G::ROWB + i * 16, 0u, 0u,
+                                         0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(full[st]));
+                }
+            }
+        }
+    } else if (alive && warp == 1) {
+        // ---- MMA issuer (the whole warp, see mma_ss): one stream over all blocks
+        // of all segments; P.V of a block goes after the next block's scores.
+        constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
+        constexpr uint32_t IDO = idesc_bf16(128, D, false, true);     // O += P V
+        struct Blk {
+            int g, u;
+            bool first, last;
+        };
+        auto issue_pv = [&](const Blk& k) -> bool {
+            if (k.first && !wait_warp(wc, bar(bars->o_free), (k.u & 1) ^ 1, timeout_code(kSiteOFree))) return false;
+            const int st = k.g % ST;
+            const uint32_t vbase = sb + C::OFF_V + st * C::TILE;
+            const uint32_t tP = tmem + ((k.g & 1) ? C::T_S1 : C::T_S0);
+            if (!wait_warp(wc, bar(bars->v_full[st]), (k.g / ST) & 1, timeout_code(kSiteVFull))) return false;
+            if constexpr (C::SPLIT) {
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_warp(wc, bar(bars->p_half[k.g & 1][h]), (k.g >> 1) & 1, timeout_code(kSitePFull)))
+                        return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + (h ? C::T_O1 : C::T_O), tP + 64 * h + 8 * kk,
+                               G::template desc_mn<128>(vbase, 4 * h + kk), IDO, (!k.first || kk > 0) ? 1u : 0u);
+                    mma_commit(bar(bars->o_half[h]));
+                }
+            } else {
+                if (!wait_warp(wc, bar(bars->p_full[k.g & 1]), (k.g >> 1) & 1, timeout_code(kSitePFull))) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tmem + C::T_O, tP + split_a_col(kk, 128), G::template desc_mn<128>(vbase, kk), IDO,
+                           (!k.first || kk > 0) ? 1u : 0u);
+                mma_commit(bar(bars->o_done));
+            }
+            mma_commit(bar(bars->v_empty[st]));
+            if (k.last) mma_commit(bar(bars->o_tile));
+            return true;
+        };
+        Blk prev{-1, 0, false, false};
+        int gi = 0;
+        bool ok = true;
+        Segment g;
+        for (int u = 0; ok && next_work(walk, t, g); ++u) {
+            const int qs = u % C::NQ;
+            // At a tile boundary the previous tile's last P.V goes first unless this
+            // tile's Q and first K block are already resident.
+            if (prev.g >= 0 && (!test_wait_warp(bar(bars->q_full[qs]), (u / C::NQ) & 1) ||
+                                !test_wait_warp(bar(bars->k_full[gi % ST]), (gi / ST) & 1))) {
+                ok = issue_pv(prev);
+                prev.g = -1;
+                if (!ok) break;
+            }
+            ok = wait_warp(wc, bar(bars->q_full[qs]), (u / C::NQ) & 1, timeout_code(kSiteQFull));
+            for (int j = g.j0; j < g.j1 && ok; ++j, ++gi) {
+                const int st = gi % ST;
+                ok = wait_warp(wc, bar(bars->k_full[st]), (gi / ST) & 1, timeout_code(kSiteKFull));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t kbase = sb + C::OFF_K + st * C::TILE;
+                const uint32_t qbase = sb + C::OFF_Q + qs * C::TILE;
+                const uint32_t tS = tmem + ((gi & 1) ? C::T_S1 : C::T_S0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tS, G::template desc_k<128>(qbase, kk), G::template desc_k<128>(kbase, kk), IDS,
+                           kk > 0 ? 1u : 0u);
+                mma_commit(bar(bars->k_empty[st]));
+                mma_commit(bar(bars->s_full[gi & 1]));
+                if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qs]));
+                if (prev.g >= 0) ok = issue_pv(prev);
+                prev = Blk{gi, u, j == g.j0, j == g.j1 - 1};
+            }
+        }
+        if (ok && prev.g >= 0) ok = issue_pv(prev);
+        // every MMA must be complete before the CTA releases TMEM
+        mma_commit(bar(bars->drain));
+        wait_warp(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
+    } else if (alive && warp >= 4) {
+        // ---- softmax / epilogue: row = TMEM lane, half = which 64 keys of a block
+        const RowThread rt = row_thread();
+        const int h = rt.half, r = rt.row;
+        const uint32_t lane_off = rt.lane_off;
+        const uint32_t tX = tmem + C::T_X + lane_off;
+        float2* xch = reinterpret_cast<float2*>(smem_raw + pad + C::OFF_XCH);
+        const int r_tok = r / group, r_head = r % group;       // row r: token r_tok of the tile, head r_head of the group
+        int pv_done = 0, g0 = 0, u = 0;
+        bool ok = true;
+        Segment g;
+        while (ok && walk.next(t, g)) {
+            const int nk = g.j1 - g.j0;
+            const bool live = r_tok < g.n_tok && r < a.tpt * group;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int head = g.head * group + r_head;
+            const int tok = g.q_tok + (live ? r_tok : 0);
+            uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D;
+            float* lrow = a.lse + (size_t)head * t.n_tokens + tok;
+            if (nk == 0) {                                     // no key for any row of the tile
+                if (live) {
+                    for (int c = h; c < D / 8; c += 2) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (h == 0) *lrow = -INFINITY;
+                }
+                continue;
+            }
+            // keys that this row sees
+            int lim = g.kv;
+            if (a.causal) {
+                const int64_t seen = g.first_pos + r_tok + 1;
+                lim = seen < g.kv ? (int)(seen > 0 ? seen : 0) : g.kv;
+            }
+            const uint32_t tO = tmem + C::T_O + lane_off;
+            const uint32_t tO1 = tmem + C::T_O1 + lane_off;
+            const uint32_t tOh = (C::SPLIT && h) ? tO1 : tO;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < nk; ++j) {
+                const int gi = g0 + j;
+                const uint32_t tS = tmem + ((gi & 1) ? C::T_S1 : C::T_S0) + lane_off + 64 * h;
+                ok = __all_sync(0xffffffffu,
+                                wait_bounded(wc, bar(bars->s_full[gi & 1]), (gi >> 1) & 1, timeout_code(kSiteSFull)));
+                if (!ok) break;
+                if (!warp_live) {                              // no row of this warp is used: only keep step
+                    if constexpr (!C::SPLIT) {
+                        ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[gi & 1]), (gi >> 1) & 1,
+                                                                 timeout_code(kSiteXmax)));
+                        if (!ok) break;
+                    }
+                    mbar_arrive(bar(C::SPLIT ? bars->p_half[gi & 1][h] : bars->p_full[gi & 1]));
+                    continue;
+                }
+                tc_fence_after();
+                float x[64];
+                {
+                    uint32_t rr[64];
+                    tmem_ld64(tS, rr);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(rr[e]);
+                }
+                const int left = lim - ((g.j0 + j) * 128 + 64 * h);    // visible keys from this half's first on
+                if (left < 64) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= left) x[c] = -INFINITY;
+                }
+                float mx = fmax3(x[0], x[1], x[2]);
+#pragma unroll
+                for (int c = 3; c < 63; c += 2) mx = fmax3(mx, x[c], x[c + 1]);
+                mx = fmaxf(mx, x[63]);
+                if constexpr (!C::SPLIT) {
+                    tmem_st1(tX + (gi & 1) * 2 + h, __float_as_uint(mx));
+                    tmem_st_wait();
+                    tc_fence_before();
+                    ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[gi & 1]), (gi >> 1) & 1,
+                                                             timeout_code(kSiteXmax)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    mx = fmaxf(mx, __uint_as_float(tmem_ld1(tX + (gi & 1) * 2 + (h ^ 1))));
+                }
+                const float m_new = fmaxf(m_run, mx * a.scale_log2);
+                if (__any_sync(0xffffffffu, m_new > m_run + 8.0f)) {
+                    if (j > 0) {
+                        // the accumulator's last P.V (block j - 1) must be done
+                        ok = __all_sync(0xffffffffu,
+                                        wait_bounded(wc, bar(C::SPLIT ? bars->o_half[h] : bars->o_done),
+                                                     (pv_done + j - 1) & 1, timeout_code(kSiteODone)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        // a row that has seen no key yet keeps its zeros
+                        const float f = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
+                        l_run *= f;
+                        const uint64_t f2 = f2_pack(f, f);
+                        constexpr int c_step = C::SPLIT ? 1 : 2;
+#pragma unroll 1
+                        for (int c32 = C::SPLIT ? 0 : h; c32 < D / 32; c32 += c_step) {
+                            uint32_t rr[32];
+                            tmem_ld32(tOh + c32 * 32, rr);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint64_t o2 =
+                                    f2_mul(f2_pack(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), f2);
+                                float lo, hi;
+                                f2_unpack(o2, lo, hi);
+                                rr[2 * e] = __float_as_uint(lo);
+                                rr[2 * e + 1] = __float_as_uint(hi);
+                            }
+                            tmem_st32(tOh + c32 * 32, rr);
+                        }
+                        tmem_st_wait();
+                    }
+                    m_run = m_new;
+                }
+                // a row (or half) that has seen no key: every p is 0, not NaN
+                const float m_ref = m_run == -INFINITY ? 0.f : m_run;
+                const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+                const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
+                uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                uint32_t pw[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float lo, hi;
+                    f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc2, nm2), lo, hi);
+                    lo = ex2_approx(lo);
+                    hi = ex2_approx(hi);
+                    acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(lo, hi));
+                    pw[e] = pack_bf16x2(lo, hi);
+                }
+                {
+                    float lo, hi;
+                    f2_unpack(f2_add(acc2[0], acc2[1]), lo, hi);
+                    l_run += lo + hi;
+                }
+                tmem_st32(tS, pw);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar(C::SPLIT ? bars->p_half[gi & 1][h] : bars->p_full[gi & 1]));
+            }
+            if (!ok) break;
+            // Final row statistics: O = a0 O_0 + a1 O_1 (SPLIT), O = a0 O (else); a
+            // row that saw no key has l = 0 and gets zeros.
+            float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
+            if constexpr (C::SPLIT) {
+                if (h == 1) xch[r] = make_float2(m_run, l_run);
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), u & 1, timeout_code(kSiteLsum)));
+                if (!ok) break;
+                if (h == 0) {
+                    const float2 o1 = xch[r];
+                    const float m = fmaxf(m_run, o1.x);
+                    const float m_ref = (m == -INFINITY) ? 0.f : m;
+                    const float f0 = ex2_approx(m_run - m_ref), f1 = ex2_approx(o1.x - m_ref);
+                    const float l_tot = l_run * f0 + o1.y * f1;
+                    const float inv = l_tot > 0.f ? 1.0f / l_tot : 0.f;
+                    a0 = f0 * inv;
+                    a1 = f1 * inv;
+                    lse2 = l_tot > 0.f ? m_ref + log2f(l_tot) : -INFINITY;
+                    xch[r] = make_float2(a0, a1);
+                }
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum2), u & 1, timeout_code(kSiteLsum)));
+                if (!ok) break;
+                if (h == 1) {
+                    const float2 f = xch[r];
+                    a0 = f.x;
+                    a1 = f.y;
+                }
+            } else {
+                tmem_st1(tX + 4 + h, __float_as_uint(l_run));
+                tmem_st_wait();
+                tc_fence_before();
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), u & 1, timeout_code(kSiteLsum)));
+                if (!ok) break;
+                tc_fence_after();
+                const float l_tot = l_run + __uint_as_float(tmem_ld1(tX + 4 + (h ^ 1)));
+                a0 = l_tot > 0.f ? 1.0f / l_tot : 0.f;
+                lse2 = l_tot > 0.f ? m_run + log2f(l_tot) : -INFINITY;
+            }
+            ok = __all_sync(0xffffffffu, wait_bounded(wc, bar(bars->o_tile), u & 1, timeout_code(kSiteOTile)));
+            if (!ok) break;
+            tc_fence_after();
+            if (warp_live) {
+                const size_t prow = part_row(blockIdx.x, g.from_start ? 1 : 0) + r;
+                float* part = reinterpret_cast<float*>(a.ws) + prow * D;
+                if (live && h == 0) {
+                    if (g.whole)
+                        *lrow = lse2 * 0.693147180559945309f;
+                    else
+                        reinterpret_cast<float*>(a.ws + ws_lse_offset(D))[prow] = lse2;
+                }
+                // The TMEM loads are warp-collective; only the stores are guarded.
+#pragma unroll 1
+                for (int c32 = h; c32 < D / 32; c32 += 2) {
+                    uint32_t rr[32];
+                    tmem_ld32(tO + c32 * 32, rr);
+                    float f[32];
+                    if constexpr (C::SPLIT) {
+                        uint32_t r1[32];
+                        tmem_ld32(tO1 + c32 * 32, r1);
+                        // a half without a visible key has an accumulator of zeros (p = 0)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            f[e] = __uint_as_float(rr[e]) * a0 + __uint_as_float(r1[e]) * a1;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(rr[e]) * a0;
+                    }
+                    if (live && g.whole) {
+#pragma unroll
+                        for (int u4 = 0; u4 < 4; ++u4)
+                            reinterpret_cast<uint4*>(orow)[c32 * 4 + u4] =
+                                make_uint4(pack_bf16x2(f[8 * u4], f[8 * u4 + 1]), pack_bf16x2(f[8 * u4 + 2], f[8 * u4 + 3]),
+                                           pack_bf16x2(f[8 * u4 + 4], f[8 * u4 + 5]),
+                                           pack_bf16x2(f[8 * u4 + 6], f[8 * u4 + 7]));
+                    } else if (live) {
+#pragma unroll
+                        for (int u4 = 0; u4 < 8; ++u4)
+                            reinterpret_cast<float4*>(part)[c32 * 8 + u4] =
+                                make_float4(f[4 * u4], f[4 * u4 + 1], f[4 * u4 + 2], f[4 * u4 + 3]);
+                    }
+                }
+                if (!g.whole && g.from_start && h == 0 && r == 0) {
+                    cut->q_tok = g.q_tok;
+                    cut->n_rows = g.n_tok * group;
+                    cut->head = g.head;
+                    cut->last_cta = (int32_t)((g.tile_end - 1) / per);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(bars->o_free));
+            pv_done += nk;
+            g0 += nk;
+            ++u;
+        }
+    }
+
+    __syncthreads();
+    if (bars->abort_flag) {
+        // Let any copy or MMA issued before the abort land before TMEM and
+        // shared memory are released.
+        for (int k = 0; k < 20; ++k) __nanosleep(50000);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the tiles that were cut: block (c, y) takes every gridDim.y-th
+// row of the tile that CTA c cut at its end, a warp per row, lanes over d.  The parts'
+// weights are formed by lanes over the parts.
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
+{
+    const PagedTables& t = a.t;
+    const CutTile cut = reinterpret_cast<const CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x];
+    if (cut.last_cta == 0) return;
+    __shared__ float weight[4][kPagedMaxCtas];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = cut.last_cta - (int)blockIdx.x + 1;
+    const float* lse = reinterpret_cast<const float*>(a.ws + ws_lse_offset(D));
+    const float* rows = reinterpret_cast<const float*>(a.ws);
+    auto row_of = [&](int p, int r) { return part_row((int)blockIdx.x + p, p == 0 ? 1 : 0) + r; };
+    for (int r = (int)blockIdx.y * 4 + warp; r < cut.n_rows; r += 4 * (int)gridDim.y) {
+        float mx = -INFINITY;
+        for (int p = lane; p < parts; p += 32) {
+            const float x = lse[row_of(p, r)];
+            weight[warp][p] = x;
+            mx = fmaxf(mx, x);
+        }
+#pragma unroll
+        for (int o = 16; o; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_ref = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        for (int p = lane; p < parts; p += 32) {
+            const float w = exp2f(weight[warp][p] - m_ref);
+            weight[warp][p] = w;
+            sum += w;
+        }
+#pragma unroll
+        for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        __syncwarp();
+        float acc[D / 32] = {};
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+            const float w = weight[warp][p];
+            const float* src = rows + row_of(p, r) * D + lane;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] += w * src[e * 32];
+        }
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        const int tok = cut.q_tok + r / a.group, head = cut.head * a.group + r % a.group;
+        uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D + lane;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) orow[e * 32] = (uint16_t)(pack_bf16x2(acc[e] * inv, 0.f) & 0xffffu);
+        if (lane == 0)
+            a.lse[(size_t)head * t.n_tokens + tok] =
+                sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+        __syncwarp();
+    }
+}
+
+size_t paged_ws_bytes(int d)
+{
+    const size_t b = ws_cut_offset(d) + kPagedMaxCtas * sizeof(CutTile);
+    return (b + 255) & ~(size_t)255;
+}
+
+int paged_tokens_per_tile(int group) { return 128 / group; }
+
+namespace {
+
+template <int D>
+int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                   cudaStream_t st)
+{
+    constexpr uint32_t smem = PagedCfg<D>::SMEM;
+    auto kern = paged_attn_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return (int)e;
+    // The most units that the tables can ask for bounds the grid (short batches
+    // need few CTAs), and the most blocks of a tile tells whether any can be cut.
+    const int64_t blocks = ((int64_t)a.t.max_pages * a.t.page_size + 127) / 128;
+    const int64_t tiles = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt + a.t.n_seq;
+    const int64_t want = (tiles * a.t.h_kv * blocks + kMinUnits - 1) / kMinUnits;
+    int grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
+    if (want < grid) grid = (int)want;
+    kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
+    if (grid > 1 && blocks > kSnap) {
+        const int64_t rows = (int64_t)a.tpt * a.group < (int64_t)a.t.n_tokens * a.group ? (int64_t)a.tpt * a.group
+                                                                                      : (int64_t)a.t.n_tokens * a.group;
+        const unsigned y = rows > 32 ? 8u : (unsigned)((rows + 3) / 4);
+        paged_join_kernel<D><<<dim3((unsigned)grid, y), 128, 0, st>>>(a);
+        e = cudaGetLastError();
+    }
+    return (int)e;
+}
+
+}  // namespace
+
+int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                 cudaStream_t st)
+{
     switch (a.d) {
-        case 64: paged_simple_kernel<64><<<grid, 128, 0, st>>>(a); break;
-        case 96: paged_simple_kernel<96><<<grid, 128, 0, st>>>(a); break;
-        case 128: paged_simple_kernel<128><<<grid, 128, 0, st>>>(a); break;
-        case 160: paged_simple_kernel<160><<<grid, 128, 0, st>>>(a); break;
+        case 64: return launch_paged_t<64>(tq, tk, tv, a, st);
+        case 96: return launch_paged_t<96>(tq, tk, tv, a, st);
+        case 128: return launch_paged_t<128>(tq, tk, tv, a, st);
+        case 160: return launch_paged_t<160>(tq, tk, tv, a, st);
         default: return (int)cudaErrorInvalidValue;
     }
-    return (int)cudaGetLastError();
 }
 
 }  // namespace ac

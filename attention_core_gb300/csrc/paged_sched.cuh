@@ -1,0 +1,192 @@
+// paged_sched.cuh -- work split of the attention over a paged cache.
+//
+// A tile is up to 128 rows -- `tpt` new tokens times the `group` query heads of
+// one KV head -- of one sequence, and its work is the blocks of 128 keys that
+// its last row sees (one unit at least: a tile that sees no key still has zeros
+// to write).  All tiles, in the order (sequence, KV head, row tile), form one
+// line of T units, and CTA c takes the units [c * per, (c + 1) * per), per =
+// ceil(T / grid): every CTA gets the same number of blocks whatever the lengths
+// are, and a tile is cut only where a CTA's share ends.  The parts of a cut tile
+// are joined by a second kernel.  Tiles of at most kSnap blocks are not cut:
+// the CTA whose share holds a tile's first unit takes all of it (cutting one
+// costs more, in the join, than the imbalance of a few blocks).
+//
+// Lengths are device data, so every CTA finds its share by itself: a block-wide
+// sum over the sequences' units (closed form under the causal mask), then a walk
+// from its first unit on.
+#pragma once
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace ac {
+
+constexpr int kSnap = 4;        // tiles of at most this many blocks stay whole
+constexpr int kMinUnits = 2;    // least share of a CTA
+
+// sum over i = 0 .. n - 1 of floor((a i + b) / m); a, b >= 0, m > 0
+__host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+{
+    int64_t s = 0;
+    while (n > 0) {
+        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const int64_t top = a * n + b;
+        n = top / m;
+        b = top % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+        if (m == 0) break;
+    }
+    return s;
+}
+
+// One sequence's shape: nq new tokens, kv keys, tiles of tpt tokens.
+struct SeqShape {
+    int nq, kv, tpt, causal;
+    __host__ __device__ int tiles() const { return (int)(((int64_t)nq + tpt - 1) / tpt); }
+    // blocks of 128 keys that tile m sees: those of its last row
+    __host__ __device__ int blocks(int m) const
+    {
+        int64_t last = kv;
+        if (causal) {
+            const int64_t end = (int64_t)kv - nq + (int64_t)(m + 1) * tpt;
+            last = end < kv ? end : kv;
+        }
+        return last <= 0 ? 0 : (int)((last + 127) / 128);
+    }
+    __host__ __device__ int cost(int m) const
+    {
+        const int n = blocks(m);
+        return n > 0 ? n : 1;
+    }
+    // units of the tiles 0 .. m - 1
+    __host__ __device__ int64_t units(int m) const
+    {
+        if (m <= 0) return 0;
+        if (kv <= 0) return m;
+        if (!causal) return (int64_t)m * cost(0);
+        const int64_t e = (int64_t)kv - nq;                  // keys before the first new token
+        const int last = tiles() - 1;                        // sees kv keys, however many rows it has
+        int64_t z = e < 0 ? -e / tpt : 0;                    // tiles that see nothing: one unit each
+        if (z > m) z = m;
+        const int64_t plain = (m < last ? m : last) - z;     // tiles that see e + (i + 1) tpt keys
+        int64_t s = z;
+        if (plain > 0) s += floor_sum(plain, 128, tpt, e + (z + 1) * tpt + 127);
+        if (m > last) s += cost(last);
+        return s;
+    }
+};
+
+// A sequence as the tables give it, made safe: lengths that do not fit the
+// tensors make it empty (`bad`).
+struct SeqTable {
+    int q0;
+    SeqShape s;
+    bool bad;
+};
+__host__ __device__ inline SeqTable read_seq(const PagedTables& t, int seq, int tpt, int causal)
+{
+    SeqTable r;
+    const int q0 = t.cu_q[seq], q1 = t.cu_q[seq + 1], kv = t.kv_lens[seq];
+    r.bad = q0 < 0 || q1 < q0 || q1 > t.n_tokens || kv < 0 || kv > (int64_t)t.max_pages * t.page_size;
+    r.q0 = q0;
+    r.s = SeqShape{r.bad ? 0 : q1 - q0, r.bad ? 0 : kv, tpt, causal};
+    return r;
+}
+
+// A piece of one tile: blocks [j0, j1) of it.
+struct Segment {
+    int seq, head, m;      // sequence, KV head, row tile
+    int q_tok, n_tok;      // first token (row of q) and tokens of the tile
+    int kv;                // keys of the sequence
+    int64_t first_pos;     // position of the tile's first token
+    int j0, j1;            // blocks of this piece; both 0: the tile sees no key
+    bool whole;            // the whole tile
+    bool from_start;       // the tile's first unit is in it
+    int64_t tile_end;      // unit after the tile's last
+};
+
+// Walks a CTA's share of the line.  `at` is the unit at which the next segment
+// starts; the CTA's share ends at `end`.
+struct SegmentWalk {
+    int tpt, causal;
+    int64_t at, end;
+    int seq, head, m, b;   // where `at` is: block b of row tile m
+    SeqTable cur;
+
+    __host__ __device__ void load(const PagedTables& t) { cur = read_seq(t, seq, tpt, causal); }
+
+    // Unit `at` lies `rel` units into sequence s.
+    __host__ __device__ void start(const PagedTables& t, int s, int64_t rel, int64_t at_, int64_t end_)
+    {
+        at = at_;
+        end = end_;
+        seq = s;
+        load(t);
+        const int tiles = cur.s.tiles();
+        const int64_t per_head = cur.s.units(tiles);
+        head = (int)(rel / per_head);
+        const int64_t r = rel % per_head;
+        int lo = 0, hi = tiles;                              // last m with units(m) <= r
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (cur.s.units(mid) <= r)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        m = lo;
+        b = (int)(r - cur.s.units(m));
+        const int n = cur.s.cost(m);
+        if (b > 0 && n <= kSnap) {                           // another CTA has all of this tile
+            at += n - b;
+            b = n;
+        }
+    }
+
+    __host__ __device__ bool next(const PagedTables& t, Segment& g)
+    {
+        if (at >= end) return false;
+        int n = cur.s.cost(m);
+        if (b >= n) {
+            b = 0;
+            if (++m >= cur.s.tiles()) {
+                m = 0;
+                if (++head >= t.h_kv) {
+                    head = 0;
+                    do {
+                        if (++seq >= t.n_seq) {              // only past the line's end
+                            at = end;
+                            return false;
+                        }
+                        load(t);
+                    } while (cur.s.nq <= 0);
+                }
+            }
+            n = cur.s.cost(m);
+        }
+        const int64_t left = end - at;
+        const int take = (n <= kSnap || left > n - b) ? n - b : (int)left;
+        g.seq = seq;
+        g.head = head;
+        g.m = m;
+        g.q_tok = cur.q0 + m * tpt;
+        g.n_tok = cur.s.nq - m * tpt < tpt ? cur.s.nq - m * tpt : tpt;
+        g.kv = cur.s.kv;
+        g.first_pos = (int64_t)cur.s.kv - cur.s.nq + (int64_t)m * tpt;
+        const bool sees = cur.s.blocks(m) > 0;
+        g.j0 = sees ? b : 0;
+        g.j1 = sees ? b + take : 0;
+        g.whole = take == n;
+        g.from_start = b == 0;
+        g.tile_end = at + (n - b);
+        at += take;
+        b += take;
+        return true;
+    }
+};
+
+}  // namespace ac

@@ -301,6 +301,18 @@ def test_captured_graph_follows_the_tables():
     p.kv_lens.copy_(full)
 
 
+def test_wait_that_runs_out_is_reported():
+    """The test hook: every thread waits on a barrier that nothing completes,
+    gives up after the limit and leaves; the next call is sound."""
+    p = Paged([1, 3], [500, 40], 4, 2, 128, 16, seed=13)
+    ac.paged_fwd(p.batch(flags=ac.FLAG_TEST_WAIT_TIMEOUT, wait_timeout_ms=20), p.q, p.k_pages, p.v_pages)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) & 0xff == ac.ERR_DEVICE_TIMEOUT
+    p.status.zero_()
+    o, lse = _run(p)
+    check_attention(o, lse, attend(p), p)
+
+
 def test_two_streams_with_a_batch_each():
     ps = [Paged([1, 40], [6000, 300], 8, 2, 128, 64, seed=s) for s in (20, 21)]
     streams = [torch.cuda.Stream() for _ in ps]
