@@ -361,6 +361,14 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _raw_stream(device: int) -> int:
+    """The current stream's handle without the Stream object around it (0.1
+    against 3 us on a Grace host: a short call's time)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _params_from(q, k, causal, p_drop, seed, offset, scale, **kw) -> Params:
     b, h_q, s, d = q.shape
     return Params(b=b, h_q=h_q, h_kv=k.shape[1], s=s, d=d, causal=causal, p_drop=p_drop,
@@ -611,13 +619,24 @@ def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: i
                                               n_pairs, stream or None)
 
 
-def _on_device(*tensors) -> None:
-    """The library launches on the current device: every tensor lives there."""
+def _device() -> int:
     import torch
-    dev = torch.cuda.current_device()
+    return torch.cuda.current_device()
+
+
+def _need(t, name, dtype, shape, device: int) -> None:
+    """A contiguous tensor of this type and shape on the current device, where
+    the library launches; _check says what else it is."""
+    if not (t.__class__.__name__ == "Tensor" and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        _check(t, name, dtype, shape)
+        _on_device(device, t)
+
+
+def _on_device(device: int, *tensors) -> None:
     for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+        if t is not None and t.get_device() != device:      # -1 off the GPU
+            raise ValueError(f"tensors must be on the current device (cuda:{device}), got {t.device}")
 
 
 def _rope_view(x, name, d):
@@ -638,44 +657,68 @@ def _rope_view(x, name, d):
     return b, h, s, (tb if b > 1 else 0, th if h > 1 else 0, ts if s > 1 else 0)
 
 
-def _rope(call, what, q, k, table, positions, pos0, out_q, out_k):
-    import torch
-    d = table.d
+# The argument structure of a rotation follows from its tensors' shapes and
+# strides alone: made once for each and copied (building it costs more than the
+# launch).
+_ROPE_PARAMS: dict = {}
+
+
+def _rope_params(q, k, out_q, out_k, d):
     p = _CRopeParams()
-    ptr = [0, 0, 0, 0]
-    outs = [out_q, out_k]
     lead = None
-    for i, (x, y, name) in enumerate(((q, out_q, "q"), (k, out_k, "k"))):
+    for x, y, name in ((q, out_q, "q"), (k, out_k, "k")):
         if x is None:
             continue
         b, h, s, st = _rope_view(x, name, d)
         if lead not in (None, (b, s, x.dim())):
             raise ValueError(f"q and k must have the same batch and tokens, got {tuple(q.shape)}, {tuple(k.shape)}")
         lead = (b, s, x.dim())
-        if y is None:
-            outs[i] = y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if y is None:           # allocated like x, contiguous
+            yst = (h * s * d, s * d, d) if x.dim() == 4 else (0, d, h * d)
         elif y.shape != x.shape:
             raise ValueError(f"out_{name} must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
-        yst = _rope_view(y, "out_" + name, d)[3]
-        if i == 0:
-            p.h_q, p.q_stride[:], p.yq_stride[:] = h, st, yst
         else:
-            p.h_kv, p.k_stride[:], p.yk_stride[:] = h, st, yst
-        ptr[i], ptr[i + 2] = x.data_ptr(), y.data_ptr()
+            yst = _rope_view(y, "out_" + name, d)[3]
+        setattr(p, "h_" + ("q" if name == "q" else "kv"), h)
+        getattr(p, name + "_stride")[:] = st
+        getattr(p, "y" + name + "_stride")[:] = yst
     if lead is None:
         raise ValueError("q or k must be given")
-    p.b, p.s, p.pos0 = lead[0], lead[1], int(pos0)
-    if positions is not None:
-        if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
-                or positions.numel() != p.b * p.s:
+    p.b, p.s = lead[:2]
+    return p
+
+
+def _rope(call, what, q, k, table, positions, pos0, out_q, out_k):
+    import torch
+    dev = _device()
+    _on_device(dev, q, k, out_q, out_k, positions)
+    key = (table.d, *[None if x is None else (x.shape, x.stride(), x.dtype) for x in (q, k, out_q, out_k)])
+    known = _ROPE_PARAMS.get(key)
+    if known is None:
+        known = _rope_params(q, k, out_q, out_k, table.d)
+        if len(_ROPE_PARAMS) >= 256:
+            _ROPE_PARAMS.clear()
+        _ROPE_PARAMS[key] = known
+    p = _CRopeParams.from_buffer_copy(known)
+    if positions is None:
+        p.pos0 = int(pos0)
+    else:
+        if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.numel() != p.b * p.s:
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor of {p.b * p.s} values")
         p.positions = positions.data_ptr()
-    _on_device(q, k, outs[0], outs[1], positions)
-    if p.b * p.s:
-        rc = call(p, table, *ptr, _stream())
-        if rc != OK:
-            raise AttnCoreError(rc, what)
-    return outs[0], outs[1]
+    xq = xk = yq = yk = 0
+    if q is not None:
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        xq, yq = q.data_ptr(), out_q.data_ptr()
+    if k is not None:
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        xk, yk = k.data_ptr(), out_k.data_ptr()
+    rc = call(p, table, xq, xk, yq, yk, _raw_stream(dev)) if p.s else OK
+    if rc != OK:
+        raise AttnCoreError(rc, what)
+    return out_q, out_k
 
 
 def rope_fwd(q, k, table: RopeTable, *, positions=None, pos0: int = 0, out_q=None, out_k=None):
@@ -747,21 +790,23 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     ``table`` at their positions (None: as they are), and rotate q
     [n_tokens, h_q, d] (or None).  Returns q's rotation, packed."""
     import torch
+    dev, bf16 = _device(), torch.bfloat16
     strides = [0, _token_stride(k, "k", batch._kv_shape), _token_stride(v, "v", batch._kv_shape)]
-    _check(k_pages, "k_pages", torch.bfloat16, batch._page_shape)
-    _check(v_pages, "v_pages", torch.bfloat16, batch._page_shape)
+    _need(k_pages, "k_pages", bf16, batch._page_shape, dev)
+    _need(v_pages, "v_pages", bf16, batch._page_shape, dev)
     if q is not None:
         strides[0] = _token_stride(q, "q", batch._q_shape)
         if out_q is None:
-            out_q = torch.empty(batch._q_shape, dtype=torch.bfloat16, device=q.device)
-        _check(out_q, "out_q", torch.bfloat16, batch._q_shape)
+            out_q = torch.empty(batch._q_shape, dtype=bf16, device=q.device)
+        else:
+            _need(out_q, "out_q", bf16, batch._q_shape, dev)
     elif out_q is not None:
         raise ValueError("out_q without q")
-    _on_device(q, k, v, k_pages, v_pages, out_q, batch.tables[0])
+    _on_device(dev, q, k, v, batch.workspace)
     if batch.params.n_tokens:
         rc = attn_core_paged_append(batch.params, table, q.data_ptr() if q is not None else 0, k.data_ptr(),
                                     v.data_ptr(), strides, out_q.data_ptr() if q is not None else 0,
-                                    k_pages.data_ptr(), v_pages.data_ptr(), _stream())
+                                    k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_append")
     return out_q
@@ -772,21 +817,22 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
     (which already holds their keys and values).  Returns (O like q, LSE fp32
     [h_q, n_tokens])."""
     import torch
-    _check(q, "q", torch.bfloat16, batch._q_shape)
-    _check(k_pages, "k_pages", torch.bfloat16, batch._page_shape)
-    _check(v_pages, "v_pages", torch.bfloat16, batch._page_shape)
+    dev, bf16 = _device(), torch.bfloat16
+    _need(q, "q", bf16, batch._q_shape, dev)
+    _need(k_pages, "k_pages", bf16, batch._page_shape, dev)
+    _need(v_pages, "v_pages", bf16, batch._page_shape, dev)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check(out, "out", torch.bfloat16, batch._q_shape)
+        _need(out, "out", bf16, batch._q_shape, dev)
     if lse is None:
         lse = torch.empty(batch._lse_shape, dtype=torch.float32, device=q.device)
     else:
-        _check(lse, "lse", torch.float32, batch._lse_shape)
-    _on_device(q, k_pages, v_pages, out, lse, batch.workspace)
+        _need(lse, "lse", torch.float32, batch._lse_shape, dev)
+    _on_device(dev, batch.workspace)
     if batch.params.n_tokens:
         rc = attn_core_paged_fwd(batch.params, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), *batch._ws, _stream())
+                                 lse.data_ptr(), *batch._ws, _raw_stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_fwd")
     return out, lse
@@ -806,23 +852,27 @@ def page_copy(pages, pairs) -> None:
         if pairs.is_cuda:
             raise ValueError("pairs must be in host memory")
         pairs = pairs.numpy()
-    wide = np.asarray(pairs)
-    if wide.size and wide.dtype.kind not in "iu":
-        raise ValueError("pairs must be integers")
-    if wide.size and (wide.ndim != 2 or wide.shape[1] != 2):
-        raise ValueError(f"pairs must be [n, 2], got {wide.shape}")
-    arr = np.ascontiguousarray(wide, dtype=np.int32)
-    if arr.dtype != wide.dtype and not np.array_equal(arr, wide):
-        raise ValueError("pairs must fit 32 bits")
-    _on_device(pages)
-    planes = pages.shape[0] if pages.dim() == 5 else 1
-    n_pages = pages.shape[-4]
+    arr = pairs
+    if not (isinstance(arr, np.ndarray) and arr.dtype == np.int32 and arr.ndim == 2 and arr.shape[1] == 2
+            and arr.flags.c_contiguous):
+        wide = np.asarray(pairs)
+        if wide.size and wide.dtype.kind not in "iu":
+            raise ValueError("pairs must be integers")
+        if wide.size and (wide.ndim != 2 or wide.shape[1] != 2):
+            raise ValueError(f"pairs must be [n, 2], got {wide.shape}")
+        arr = np.ascontiguousarray(wide, dtype=np.int32)
+        if not np.array_equal(arr, wide):
+            raise ValueError("pairs must fit 32 bits")
+    dev = _device()
+    _on_device(dev, pages)
+    shape = pages.shape
+    planes, n_pages = (shape[0] if len(shape) == 5 else 1), shape[-4]
     if pages.numel() == 0:
         if arr.size:
             raise ValueError("no pages to copy")
         return
-    page_bytes = pages.numel() // (planes * n_pages) * pages.element_size()
+    page_bytes = shape[-3] * shape[-2] * shape[-1] * pages.element_size()
     rc = attn_core_page_copy(pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes, arr.ctypes.data,
-                             arr.shape[0] if arr.size else 0, _stream())
+                             len(arr) if arr.size else 0, _raw_stream(dev))
     if rc != OK:
         raise AttnCoreError(rc, "attn_core_page_copy")

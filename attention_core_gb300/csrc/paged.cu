@@ -34,6 +34,8 @@
 // A whole tile's rows go to O; a cut tile's parts go to the workspace as fp32
 // rows divided by their own sum, with their own base-2 LSE, and a second kernel
 // joins them: O = sum_p w_p O_p / sum_p w_p, w_p = 2^(lse_p - max).
+#include <stddef.h>
+
 #include "kernels.h"
 #include "paged_sched.cuh"
 #include "ptx.cuh"
@@ -50,14 +52,16 @@ struct PagedCfg {
     using G = TileGeom<D>;
     static constexpr uint32_t TILE = G::template tile_bytes<128>();
     static constexpr uint32_t CHUNK = G::template chunk_bytes<128>();
-    static constexpr int NQ = (D <= 128) ? 2 : 1;
-    static constexpr int ST = (D <= 64) ? 5 : (D <= 96 ? 3 : 2);
+    // One Q buffer (the next tile's Q loads behind this tile's last softmax and
+    // epilogue) leaves the most room for keys and values in flight.
+    static constexpr int NQ = (D <= 64) ? 2 : 1;
+    static constexpr int ST = (D <= 64) ? 6 : (D <= 96 ? 4 : (D <= 128 ? 3 : 2));
     static constexpr bool SPLIT = (D <= 128);
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = NQ * TILE;
     static constexpr uint32_t OFF_V = OFF_K + ST * TILE;
     static constexpr uint32_t OFF_BAR = OFF_V + ST * TILE;
-    static constexpr uint32_t BAR_BYTES = 512;
+    static constexpr uint32_t BAR_BYTES = 640;
     static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
     static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
     static constexpr uint32_t SMEM = OFF_XCH + XCH_BYTES + 1024;
@@ -68,27 +72,32 @@ struct PagedCfg {
 
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
-    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
     uint64_t v_tail;        // a tile's last, partial V block has landed (rows past its end still to be zeroed)
     uint64_t s_full[2];
-    uint64_t p_full[2];     // d = 160: P of the block is in TMEM
-    uint64_t p_half[2][2];  // SPLIT: [score buffer][half] P of the half is in TMEM
     uint64_t o_half[2];     // SPLIT: the half's P.V of the block is done
     uint64_t o_done;        // d = 160: the block's P.V is done
-    uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
-    uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
-    uint64_t o_free;        // the tile's O has been read
     uint64_t o_tile;        // the tile's last P.V is done
     uint64_t drain;
     uint64_t never;
+    // completed by the row threads of one half
+    uint64_t p_half[2][2];  // SPLIT: [score buffer][half] P of the half is in TMEM
+    // completed by all row threads
+    uint64_t p_full[2];     // d = 160: P of the block is in TMEM
+    uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
+    uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
+    uint64_t o_free;        // the tile's O has been read
     uint32_t tmem_base;
     int32_t abort_flag;
-    int64_t line_units;             // T
-    int64_t start_rel;              // where this CTA's share starts: units into start_seq
-    int32_t start_seq;
-    int32_t warp_sum_pad;
     int64_t warp_sum[kThreads / 32];
+    // where this CTA's share starts
+    int64_t start_rel;      // units into the KV head
+    int32_t start_seq, start_head;
+    SeqTable start_table;
 };
+constexpr int kBarsOnce = offsetof(PagedBars, p_half) / 8;     // one arrival (a commit or a producer)
+constexpr int kBarsHalf = offsetof(PagedBars, p_full) / 8;     // kRowThreads / 2
+constexpr int kBarsAll = offsetof(PagedBars, tmem_base) / 8;   // kRowThreads
 static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
@@ -152,33 +161,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
     const uint32_t warp = warp_id(), lane = lane_id();
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(bars->q_full[i]), 1);
-            mbar_init(bar(bars->q_empty[i]), 1);
-            mbar_init(bar(bars->s_full[i]), 1);
-            mbar_init(bar(bars->p_full[i]), kRowThreads);
-            mbar_init(bar(bars->xmax[i]), kRowThreads);
-            mbar_init(bar(bars->p_half[i][0]), kRowThreads / 2);
-            mbar_init(bar(bars->p_half[i][1]), kRowThreads / 2);
-            mbar_init(bar(bars->o_half[i]), 1);
+    // Set-up, spread over the warps: warp 3 the barriers, warp 1 TMEM, warp 0 the
+    // descriptors, and from warp 4 on the lengths.
+    if (warp == 3) {
+        uint64_t* all = reinterpret_cast<uint64_t*>(bars);
+        for (int i = lane; i < kBarsAll; i += 32)
+            mbar_init(bar(all[i]), i < kBarsOnce ? 1 : (i < kBarsHalf ? kRowThreads / 2 : kRowThreads));
+        if (lane == 0) {
+            bars->abort_flag = 0;
+            reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
         }
-        for (int st = 0; st < ST; ++st) {
-            mbar_init(bar(bars->k_full[st]), 1);
-            mbar_init(bar(bars->k_empty[st]), 1);
-            mbar_init(bar(bars->v_full[st]), 1);
-            mbar_init(bar(bars->v_empty[st]), 1);
-        }
-        mbar_init(bar(bars->v_tail), 1);
-        mbar_init(bar(bars->o_done), 1);
-        mbar_init(bar(bars->o_free), kRowThreads);
-        mbar_init(bar(bars->o_tile), 1);
-        mbar_init(bar(bars->drain), 1);
-        mbar_init(bar(bars->lsum), kRowThreads);
-        mbar_init(bar(bars->lsum2), kRowThreads);
-        mbar_init(bar(bars->never), 1);
-        bars->abort_flag = 0;
-        bars->start_seq = -1;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -191,17 +183,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tmem_relinquish();
     }
 
-    // ---- this CTA's share of the line: thread i sums the units of its run of
+    // ---- this CTA's share of the line: every thread sums the units of its run of
     // sequences, the block sums those, and the run that holds the share's first
     // unit finds the sequence.
+    const int order = ((int)threadIdx.x + kThreads - 128) % kThreads;     // warp 4 first
     const int run = (t.n_seq + kThreads - 1) / kThreads;
-    const int s0 = (int)threadIdx.x * run < t.n_seq ? (int)threadIdx.x * run : t.n_seq;
+    const int s0 = order * run < t.n_seq ? order * run : t.n_seq;
     const int s1 = s0 + run < t.n_seq ? s0 + run : t.n_seq;
-    int64_t mine = 0;
+    int64_t mine = 0, per_head = 0;
+    SeqTable table{};
     for (int s = s0; s < s1; ++s) {
-        const SeqTable q = read_seq(t, s, a.tpt, a.causal);
-        if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
-        mine += q.s.units(q.s.tiles()) * t.h_kv;
+        table = read_seq(t, s, a.tpt, a.causal);
+        if (table.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
+        per_head = table.s.units(table.s.tiles());
+        mine += per_head * t.h_kv;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -209,7 +204,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
         if ((int)lane >= o) upto += x;
     }
-    if (lane == 31) bars->warp_sum[warp] = upto;
+    if (lane == 31) bars->warp_sum[order / 32] = upto;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -217,28 +212,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         const int64_t x = bars->warp_sum[w];
-        if (w < (int)warp) upto += x;
+        if (w < order / 32) upto += x;
         total += x;
     }
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t per = quot(total + gridDim.x - 1, gridDim.x);
     per = per > kMinUnits ? per : kMinUnits;
     const int64_t u0 = (int64_t)blockIdx.x * per;
     const int64_t u1 = u0 + per < total ? u0 + per : total;
     if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
         int64_t rel = u0 - (upto - mine);
-        for (int s = s0; s < s1; ++s) {
-            const SeqTable q = read_seq(t, s, a.tpt, a.causal);
-            const int64_t n = q.s.units(q.s.tiles()) * t.h_kv;
-            if (rel < n) {
-                bars->start_seq = s;
-                bars->start_rel = rel;
-                break;
-            }
-            rel -= n;
+        int s = s0;
+        for (; run > 1; ++s) {                       // with one sequence a thread it is at hand
+            table = read_seq(t, s, a.tpt, a.causal);
+            per_head = table.s.units(table.s.tiles());
+            if (rel < per_head * t.h_kv) break;
+            rel -= per_head * t.h_kv;
         }
+        const int head = (int)quot(rel, per_head);
+        bars->start_seq = s;
+        bars->start_head = head;
+        bars->start_rel = rel - head * per_head;
+        bars->start_table = table;
     }
-    CutTile* cut = reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D)) + blockIdx.x;
-    if (threadIdx.x == 0) cut->last_cta = 0;
     __syncthreads();
     const uint32_t tmem = bars->tmem_base;
     const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
@@ -246,17 +241,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     walk.tpt = a.tpt;
     walk.causal = a.causal;
     walk.at = walk.end = 0;
-    if (u0 < u1) walk.start(t, bars->start_seq, bars->start_rel, u0, u1);
+    if (u0 < u1)
+        walk.start(bars->start_seq, bars->start_table, bars->start_head, bars->start_rel, u0, u1);
     const int group = a.group;
 
     bool alive = true;
     if (a.inject_timeout) alive = wait_bounded(wc, bar(bars->never), 0, timeout_code(kSiteInject));
 
     if (alive && (warp == 0 || warp == 2)) {
-        // ---- TMA producers.  A block's pages go to one lane each: the lane reads
-        // the page's table entry (before the wait for the ring slot, which hides
-        // it) and issues its column chunks.  A page outside the cache reads as
-        // zeros (coordinates outside the tensor map) and is reported.
+        // ---- TMA producers.  The page_table entries of a tile come 32 at a time, one
+        // a lane, the next 32 on their way; a block's pages go to one lane each, which
+        // issues the page's column chunks.  A page outside the cache reads as zeros
+        // (coordinates outside the tensor map) and is reported.
         const bool is_v = warp == 2;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
         uint64_t* full = is_v ? bars->v_full : bars->k_full;
@@ -267,6 +263,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bool ok = true;
         Segment g;
         while (ok && next_work(walk, t, g)) {
+            const int32_t* entries = t.page_table + (int64_t)g.seq * t.max_pages;
+            const int n_entries = (g.kv + t.page_size - 1) >> t.page_shift;
+            auto entry = [&](int i) {
+                if (i >= n_entries) return -1;
+                const int page = entries[i];
+                if (page >= 0 && page < t.n_pages) return page;
+                if (t.status) atomicCAS(t.status, 0, kStatusTable);
+                return -1;
+            };
+            int window = ((g.j0 * 128) >> t.page_shift) & ~31;             // first entry of the 32 at hand
+            int page_now = entry(window + (int)lane), page_next = entry(window + 32 + (int)lane);
             if (!is_v) {
                 // the tile's Q as soon as its buffer is free
                 const int qs = u % C::NQ;
@@ -285,16 +292,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const int st = gi % ST;
                 const int rows = g.kv - j * 128 < 128 ? g.kv - j * 128 : 128;     // keys of the block
                 const int pages = (rows + rows_pp - 1) / rows_pp;
-                int page = -1, row = 0;
-                if ((int)lane < pages) {
-                    const int key = j * 128 + (int)lane * rows_pp;
-                    page = t.page_table[(int64_t)g.seq * t.max_pages + (key >> t.page_shift)];
-                    row = key & (t.page_size - 1);
-                    if (page < 0 || page >= t.n_pages) {
-                        page = -1;
-                        if (t.status) atomicCAS(t.status, 0, kStatusTable);
-                    }
+                const int first = (j * 128) >> t.page_shift;                      // a block's entries share a window
+                if (first >= window + 32) {
+                    window += 32;
+                    page_now = page_next;
+                    page_next = entry(window + 32 + (int)lane);
                 }
+                const int page = __shfl_sync(0xffffffffu, page_now, (first - window + (int)lane) & 31);
+                const int row = (j * 128 + (int)lane * rows_pp) & (t.page_size - 1);
                 ok = wait_warp(wc, bar(empty[st]), ((gi / ST) & 1) ^ 1,
                                timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
                 if (!ok) break;
@@ -620,6 +625,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
                 }
                 if (!g.whole && g.from_start && h == 0 && r == 0) {
+                    CutTile* cut = reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D)) + blockIdx.x;
                     cut->q_tok = g.q_tok;
                     cut->n_rows = g.n_tok * group;
                     cut->head = g.head;

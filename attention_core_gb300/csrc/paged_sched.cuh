@@ -24,21 +24,30 @@ namespace ac {
 constexpr int kSnap = 4;        // tiles of at most this many blocks stay whole
 constexpr int kMinUnits = 2;    // least share of a CTA
 
+// a / b; lengths are 31-bit numbers, so the quotients nearly always fit the
+// 32-bit divide, which takes a fraction of the 64-bit one's time
+__host__ __device__ inline int64_t quot(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+    return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // sum over i = 0 .. n - 1 of floor((a i + b) / m); a, b >= 0, m > 0
 __host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
 {
     int64_t s = 0;
     while (n > 0) {
-        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
+        const int64_t qa = quot(a, m), qb = quot(b, m);
+        s += (n - 1) * n / 2 * qa + n * qb;
+        a -= qa * m;
+        b -= qb * m;
+        if (a == 0) break;
         const int64_t top = a * n + b;
-        n = top / m;
-        b = top % m;
+        n = quot(top, m);
+        b = top - n * m;
         const int64_t t = m;
         m = a;
         a = t;
-        if (m == 0) break;
     }
     return s;
 }
@@ -46,7 +55,7 @@ __host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 // One sequence's shape: nq new tokens, kv keys, tiles of tpt tokens.
 struct SeqShape {
     int nq, kv, tpt, causal;
-    __host__ __device__ int tiles() const { return (int)(((int64_t)nq + tpt - 1) / tpt); }
+    __host__ __device__ int tiles() const { return (int)quot((int64_t)nq + tpt - 1, tpt); }
     // blocks of 128 keys that tile m sees: those of its last row
     __host__ __device__ int blocks(int m) const
     {
@@ -70,7 +79,7 @@ struct SeqShape {
         if (!causal) return (int64_t)m * cost(0);
         const int64_t e = (int64_t)kv - nq;                  // keys before the first new token
         const int last = tiles() - 1;                        // sees kv keys, however many rows it has
-        int64_t z = e < 0 ? -e / tpt : 0;                    // tiles that see nothing: one unit each
+        int64_t z = e < 0 ? quot(-e, tpt) : 0;                    // tiles that see nothing: one unit each
         if (z > m) z = m;
         const int64_t plain = (m < last ? m : last) - z;     // tiles that see e + (i + 1) tpt keys
         int64_t s = z;
@@ -79,6 +88,27 @@ struct SeqShape {
         return s;
     }
 };
+
+// The last row tile of a head that starts at or before unit r of it.  On the
+// device a whole warp calls this with one r: each round its lanes test 32
+// candidates.
+__host__ __device__ inline int find_tile(const SeqShape& s, int64_t r)
+{
+    int lo = 0, hi = s.tiles();
+    while (hi - lo > 1) {
+#ifdef __CUDA_ARCH__
+        const int step = (hi - lo + 31) / 32;
+        const int m = lo + (int)(threadIdx.x & 31) * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, m < hi && s.units(m) <= r);
+        lo += (31 - __clz(le)) * step;                       // lane 0's test holds
+        hi = lo + step < hi ? lo + step : hi;
+#else
+        const int m = lo + (hi - lo) / 2;
+        (s.units(m) <= r ? lo : hi) = m;
+#endif
+    }
+    return lo;
+}
 
 // A sequence as the tables give it, made safe: lengths that do not fit the
 // tensors make it empty (`bad`).
@@ -119,26 +149,16 @@ struct SegmentWalk {
 
     __host__ __device__ void load(const PagedTables& t) { cur = read_seq(t, seq, tpt, causal); }
 
-    // Unit `at` lies `rel` units into sequence s.
-    __host__ __device__ void start(const PagedTables& t, int s, int64_t rel, int64_t at_, int64_t end_)
+    // Unit `at_` lies r units into KV head h of sequence sq.  (Whole warps, see
+    // find_tile.)
+    __host__ __device__ void start(int sq, const SeqTable& table, int h, int64_t r, int64_t at_, int64_t end_)
     {
         at = at_;
         end = end_;
-        seq = s;
-        load(t);
-        const int tiles = cur.s.tiles();
-        const int64_t per_head = cur.s.units(tiles);
-        head = (int)(rel / per_head);
-        const int64_t r = rel % per_head;
-        int lo = 0, hi = tiles;                              // last m with units(m) <= r
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            if (cur.s.units(mid) <= r)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        m = lo;
+        seq = sq;
+        cur = table;
+        head = h;
+        m = find_tile(cur.s, r);
         b = (int)(r - cur.s.units(m));
         const int n = cur.s.cost(m);
         if (b > 0 && n <= kSnap) {                           // another CTA has all of this tile
