@@ -70,20 +70,17 @@ struct PagedCfg {
     static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
 };
 
+// Barriers of block g's ring slot st = g % ST serve every role that waits for the
+// same event, so the issuing warp commits twice per block: s_full (S_g is in TMEM;
+// K's slot is free) and pv_done (O has block g; V's slot and P are free).
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
-    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t k_full[6], v_full[6], s_full[6], pv_done[6];
     uint64_t v_tail;        // a tile's last, partial V block has landed (rows past its end still to be zeroed)
-    uint64_t s_full[2];
-    uint64_t o_half[2];     // SPLIT: the half's P.V of the block is done
-    uint64_t o_done;        // d = 160: the block's P.V is done
-    uint64_t o_tile;        // the tile's last P.V is done
     uint64_t drain;
     uint64_t never;
-    // completed by the row threads of one half
-    uint64_t p_half[2][2];  // SPLIT: [score buffer][half] P of the half is in TMEM
     // completed by all row threads
-    uint64_t p_full[2];     // d = 160: P of the block is in TMEM
+    uint64_t p_full[2];     // P of the block is in TMEM
     uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
     uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
     uint64_t o_free;        // the tile's O has been read
@@ -95,14 +92,13 @@ struct PagedBars {
     int32_t start_seq, start_head;
     SeqTable start_table;
 };
-constexpr int kBarsOnce = offsetof(PagedBars, p_half) / 8;     // one arrival (a commit or a producer)
-constexpr int kBarsHalf = offsetof(PagedBars, p_full) / 8;     // kRowThreads / 2
+constexpr int kBarsOnce = offsetof(PagedBars, p_full) / 8;     // one arrival (a commit or a producer)
 constexpr int kBarsAll = offsetof(PagedBars, tmem_base) / 8;   // kRowThreads
 static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
     kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
-    kSitePFull, kSiteSFull, kSiteODone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteOTile, kSiteDrain
+    kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -131,6 +127,20 @@ __host__ __device__ inline size_t ws_cut_offset(int d)
 {
     return ws_lse_offset(d) + (size_t)kPagedMaxCtas * 2 * 128 * sizeof(float);
 }
+
+// Position in a ring of N slots: the slot, and the parity of its current use.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void advance()
+    {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The next segment with blocks to visit (the others only have zeros to write,
 // which is the row threads' business).
@@ -166,7 +176,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (warp == 3) {
         uint64_t* all = reinterpret_cast<uint64_t*>(bars);
         for (int i = lane; i < kBarsAll; i += 32)
-            mbar_init(bar(all[i]), i < kBarsOnce ? 1 : (i < kBarsHalf ? kRowThreads / 2 : kRowThreads));
+            mbar_init(bar(all[i]), i < kBarsOnce ? 1 : kRowThreads);
         if (lane == 0) {
             bars->abort_flag = 0;
             reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
@@ -256,10 +266,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const bool is_v = warp == 2;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
         uint64_t* full = is_v ? bars->v_full : bars->k_full;
-        uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+        uint64_t* empty = is_v ? bars->pv_done : bars->s_full;
         const uint32_t ring = sb + (is_v ? C::OFF_V : C::OFF_K);
         const int rows_pp = t.page_size < 128 ? t.page_size : 128;     // rows of a block from one page
-        int gi = 0, u = 0, tails = 0;
+        Ring<ST> rg;
+        Ring<C::NQ> qr;
+        int tails = 0;
         bool ok = true;
         Segment g;
         while (ok && next_work(walk, t, g)) {
@@ -276,8 +288,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             int page_now = entry(window + (int)lane), page_next = entry(window + 32 + (int)lane);
             if (!is_v) {
                 // the tile's Q as soon as its buffer is free
-                const int qs = u % C::NQ;
-                ok = wait_warp(wc, bar(bars->q_empty[qs]), ((u / C::NQ) & 1) ^ 1, timeout_code(kSiteQEmpty));
+                const int qs = qr.slot;
+                ok = wait_warp(wc, bar(bars->q_empty[qs]), qr.phase ^ 1, timeout_code(kSiteQEmpty));
                 if (!ok) break;
                 if (lane == 31) {
                     mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * G::ROWB * G::NCH);
@@ -286,10 +298,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                     bar(bars->q_full[qs]));
                 }
                 __syncwarp();
-                ++u;
+                qr.advance();
             }
-            for (int j = g.j0; j < g.j1; ++j, ++gi) {
-                const int st = gi % ST;
+            for (int j = g.j0; j < g.j1; ++j, rg.advance()) {
+                const int st = rg.slot;
                 const int rows = g.kv - j * 128 < 128 ? g.kv - j * 128 : 128;     // keys of the block
                 const int pages = (rows + rows_pp - 1) / rows_pp;
                 const int first = (j * 128) >> t.page_shift;                      // a block's entries share a window
@@ -300,8 +312,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 const int page = __shfl_sync(0xffffffffu, page_now, (first - window + (int)lane) & 31);
                 const int row = (j * 128 + (int)lane * rows_pp) & (t.page_size - 1);
-                ok = wait_warp(wc, bar(empty[st]), ((gi / ST) & 1) ^ 1,
-                               timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
+                ok = wait_warp(wc, bar(empty[st]), rg.phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
                 if (!ok) break;
                 const bool tail = is_v && rows < 128;
                 const uint32_t land = bar(tail ? bars->v_tail : full[st]);
@@ -331,78 +342,77 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
     } else if (alive && warp == 1) {
         // ---- MMA issuer (the whole warp, see mma_ss): one stream over all blocks
-        // of all segments; P.V of a block goes after the next block's scores.
+        // of all segments; P.V of a block goes after the next block's scores.  The
+        // products are ordered by their issue, so S of block g + 1 may overwrite the
+        // buffer that P.V of block g - 1 reads.
         constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
         constexpr uint32_t IDO = idesc_bf16(128, D, false, true);     // O += P V
-        struct Blk {
-            int g, u;
-            bool first, last;
-        };
-        auto issue_pv = [&](const Blk& k) -> bool {
-            if (k.first && !wait_warp(wc, bar(bars->o_free), (k.u & 1) ^ 1, timeout_code(kSiteOFree))) return false;
-            const int st = k.g % ST;
-            const uint32_t vbase = sb + C::OFF_V + st * C::TILE;
-            const uint32_t tP = tmem + ((k.g & 1) ? C::T_S1 : C::T_S0);
-            if (!wait_warp(wc, bar(bars->v_full[st]), (k.g / ST) & 1, timeout_code(kSiteVFull))) return false;
+        Ring<ST> rs, rv;            // the next block's slot for S, and for P.V
+        Ring<2> bs, bv;             // their score buffers
+        Ring<C::NQ> qr;
+        uint32_t o_phase = 1;       // o_free: the first tile finds O free
+        bool pending = false;       // a block has its S but not its P.V
+        bool v_first = false;       // it is its tile's first
+        auto issue_pv = [&]() -> bool {
+            if (v_first) {
+                if (!wait_warp(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
+                o_phase ^= 1;
+            }
+            const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
+            const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
+            if (!wait_warp(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull))) return false;
+            if (!wait_warp(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull))) return false;
+            tc_fence_after();
             if constexpr (C::SPLIT) {
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait_warp(wc, bar(bars->p_half[k.g & 1][h]), (k.g >> 1) & 1, timeout_code(kSitePFull)))
-                        return false;
-                    tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + (h ? C::T_O1 : C::T_O), tP + 64 * h + 8 * kk,
-                               G::template desc_mn<128>(vbase, 4 * h + kk), IDO, (!k.first || kk > 0) ? 1u : 0u);
-                    mma_commit(bar(bars->o_half[h]));
-                }
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tmem + (kk >= 4 ? C::T_O1 : C::T_O), tP + (kk >= 4 ? 64 : 0) + 8 * (kk & 3),
+                           G::template desc_mn<128>(vbase, kk), IDO, (!v_first || (kk & 3) > 0) ? 1u : 0u);
             } else {
-                if (!wait_warp(wc, bar(bars->p_full[k.g & 1]), (k.g >> 1) & 1, timeout_code(kSitePFull))) return false;
-                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ts(tmem + C::T_O, tP + split_a_col(kk, 128), G::template desc_mn<128>(vbase, kk), IDO,
-                           (!k.first || kk > 0) ? 1u : 0u);
-                mma_commit(bar(bars->o_done));
+                           (!v_first || kk > 0) ? 1u : 0u);
             }
-            mma_commit(bar(bars->v_empty[st]));
-            if (k.last) mma_commit(bar(bars->o_tile));
+            mma_commit(bar(bars->pv_done[rv.slot]));
+            rv.advance();
+            bv.advance();
+            pending = false;
             return true;
         };
-        Blk prev{-1, 0, false, false};
-        int gi = 0;
         bool ok = true;
         Segment g;
-        for (int u = 0; ok && next_work(walk, t, g); ++u) {
-            const int qs = u % C::NQ;
+        while (ok && next_work(walk, t, g)) {
             // At a tile boundary the previous tile's last P.V goes first unless this
             // tile's Q and first K block are already resident.
-            if (prev.g >= 0 && (!test_wait_warp(bar(bars->q_full[qs]), (u / C::NQ) & 1) ||
-                                !test_wait_warp(bar(bars->k_full[gi % ST]), (gi / ST) & 1))) {
-                ok = issue_pv(prev);
-                prev.g = -1;
+            if (pending && (!test_wait_warp(bar(bars->q_full[qr.slot]), qr.phase) ||
+                            !test_wait_warp(bar(bars->k_full[rs.slot]), rs.phase))) {
+                ok = issue_pv();
                 if (!ok) break;
             }
-            ok = wait_warp(wc, bar(bars->q_full[qs]), (u / C::NQ) & 1, timeout_code(kSiteQFull));
-            for (int j = g.j0; j < g.j1 && ok; ++j, ++gi) {
-                const int st = gi % ST;
-                ok = wait_warp(wc, bar(bars->k_full[st]), (gi / ST) & 1, timeout_code(kSiteKFull));
+            ok = wait_warp(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
+            const uint32_t qbase = sb + C::OFF_Q + qr.slot * C::TILE;
+            for (int j = g.j0; j < g.j1 && ok; ++j) {
+                ok = wait_warp(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t kbase = sb + C::OFF_K + st * C::TILE;
-                const uint32_t qbase = sb + C::OFF_Q + qs * C::TILE;
-                const uint32_t tS = tmem + ((gi & 1) ? C::T_S1 : C::T_S0);
+                const uint32_t kbase = sb + C::OFF_K + rs.slot * C::TILE;
+                const uint32_t tS = tmem + (bs.slot ? C::T_S1 : C::T_S0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss(tS, G::template desc_k<128>(qbase, kk), G::template desc_k<128>(kbase, kk), IDS,
                            kk > 0 ? 1u : 0u);
-                mma_commit(bar(bars->k_empty[st]));
-                mma_commit(bar(bars->s_full[gi & 1]));
-                if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qs]));
-                if (prev.g >= 0) ok = issue_pv(prev);
-                prev = Blk{gi, u, j == g.j0, j == g.j1 - 1};
+                mma_commit(bar(bars->s_full[rs.slot]));
+                if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qr.slot]));
+                rs.advance();
+                bs.advance();
+                if (pending) ok = issue_pv();
+                pending = true;
+                v_first = j == g.j0;
             }
+            qr.advance();
         }
-        if (ok && prev.g >= 0) ok = issue_pv(prev);
+        if (ok && pending) ok = issue_pv();
         // every MMA must be complete before the CTA releases TMEM
         mma_commit(bar(bars->drain));
         wait_warp(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
@@ -414,7 +424,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t tX = tmem + C::T_X + lane_off;
         float2* xch = reinterpret_cast<float2*>(smem_raw + pad + C::OFF_XCH);
         const int r_tok = r / group, r_head = r % group;       // row r: token r_tok of the tile, head r_head of the group
-        int pv_done = 0, g0 = 0, u = 0;
+        Ring<ST> rg;                // this block's slot
+        Ring<2> bs;                 // and score buffer
+        uint32_t tile_phase = 0;
         bool ok = true;
         Segment g;
         while (ok && walk.next(t, g)) {
@@ -442,19 +454,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const uint32_t tO1 = tmem + C::T_O1 + lane_off;
             const uint32_t tOh = (C::SPLIT && h) ? tO1 : tO;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int j = 0; j < nk; ++j) {
-                const int gi = g0 + j;
-                const uint32_t tS = tmem + ((gi & 1) ? C::T_S1 : C::T_S0) + lane_off + 64 * h;
-                ok = __all_sync(0xffffffffu,
-                                wait_bounded(wc, bar(bars->s_full[gi & 1]), (gi >> 1) & 1, timeout_code(kSiteSFull)));
+            Ring<ST> before = rg;                              // the block before this one
+            for (int j = 0; j < nk; ++j, before = rg, rg.advance(), bs.advance()) {
+                const uint32_t tS = tmem + (bs.slot ? C::T_S1 : C::T_S0) + lane_off + 64 * h;
+                ok = wait_warp(wc, bar(bars->s_full[rg.slot]), rg.phase, timeout_code(kSiteSFull));
                 if (!ok) break;
                 if (!warp_live) {                              // no row of this warp is used: only keep step
                     if constexpr (!C::SPLIT) {
-                        ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[gi & 1]), (gi >> 1) & 1,
+                        ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[bs.slot]), bs.phase,
                                                                  timeout_code(kSiteXmax)));
                         if (!ok) break;
                     }
-                    mbar_arrive(bar(C::SPLIT ? bars->p_half[gi & 1][h] : bars->p_full[gi & 1]));
+                    mbar_arrive(bar(bars->p_full[bs.slot]));
                     continue;
                 }
                 tc_fence_after();
@@ -476,22 +487,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int c = 3; c < 63; c += 2) mx = fmax3(mx, x[c], x[c + 1]);
                 mx = fmaxf(mx, x[63]);
                 if constexpr (!C::SPLIT) {
-                    tmem_st1(tX + (gi & 1) * 2 + h, __float_as_uint(mx));
+                    tmem_st1(tX + bs.slot * 2 + h, __float_as_uint(mx));
                     tmem_st_wait();
                     tc_fence_before();
-                    ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[gi & 1]), (gi >> 1) & 1,
+                    ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[bs.slot]), bs.phase,
                                                              timeout_code(kSiteXmax)));
                     if (!ok) break;
                     tc_fence_after();
-                    mx = fmaxf(mx, __uint_as_float(tmem_ld1(tX + (gi & 1) * 2 + (h ^ 1))));
+                    mx = fmaxf(mx, __uint_as_float(tmem_ld1(tX + bs.slot * 2 + (h ^ 1))));
                 }
                 const float m_new = fmaxf(m_run, mx * a.scale_log2);
                 if (__any_sync(0xffffffffu, m_new > m_run + 8.0f)) {
                     if (j > 0) {
                         // the accumulator's last P.V (block j - 1) must be done
-                        ok = __all_sync(0xffffffffu,
-                                        wait_bounded(wc, bar(C::SPLIT ? bars->o_half[h] : bars->o_done),
-                                                     (pv_done + j - 1) & 1, timeout_code(kSiteODone)));
+                        ok = wait_warp(wc, bar(bars->pv_done[before.slot]), before.phase, timeout_code(kSitePvDone));
                         if (!ok) break;
                         tc_fence_after();
                         // a row that has seen no key yet keeps its zeros
@@ -541,7 +550,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tmem_st32(tS, pw);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(C::SPLIT ? bars->p_half[gi & 1][h] : bars->p_full[gi & 1]));
+                mbar_arrive(bar(bars->p_full[bs.slot]));
             }
             if (!ok) break;
             // Final row statistics: O = a0 O_0 + a1 O_1 (SPLIT), O = a0 O (else); a
@@ -549,7 +558,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
             if constexpr (C::SPLIT) {
                 if (h == 1) xch[r] = make_float2(m_run, l_run);
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), u & 1, timeout_code(kSiteLsum)));
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum)));
                 if (!ok) break;
                 if (h == 0) {
                     const float2 o1 = xch[r];
@@ -563,7 +572,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     lse2 = l_tot > 0.f ? m_ref + log2f(l_tot) : -INFINITY;
                     xch[r] = make_float2(a0, a1);
                 }
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum2), u & 1, timeout_code(kSiteLsum)));
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum2), tile_phase, timeout_code(kSiteLsum)));
                 if (!ok) break;
                 if (h == 1) {
                     const float2 f = xch[r];
@@ -574,14 +583,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tmem_st1(tX + 4 + h, __float_as_uint(l_run));
                 tmem_st_wait();
                 tc_fence_before();
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), u & 1, timeout_code(kSiteLsum)));
+                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum)));
                 if (!ok) break;
                 tc_fence_after();
                 const float l_tot = l_run + __uint_as_float(tmem_ld1(tX + 4 + (h ^ 1)));
                 a0 = l_tot > 0.f ? 1.0f / l_tot : 0.f;
                 lse2 = l_tot > 0.f ? m_run + log2f(l_tot) : -INFINITY;
             }
-            ok = __all_sync(0xffffffffu, wait_bounded(wc, bar(bars->o_tile), u & 1, timeout_code(kSiteOTile)));
+            ok = wait_warp(wc, bar(bars->pv_done[before.slot]), before.phase, timeout_code(kSitePvDone));
             if (!ok) break;
             tc_fence_after();
             if (warp_live) {
@@ -634,9 +643,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             tc_fence_before();
             mbar_arrive(bar(bars->o_free));
-            pv_done += nk;
-            g0 += nk;
-            ++u;
+            tile_phase ^= 1;
         }
     }
 
