@@ -102,6 +102,22 @@ enum : int32_t {
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
+// A whole warp's bounded wait, in few instructions where the phase is complete
+// already: the issuing warp's loop has to stay small (its instructions are
+// fetched between those of the row warps), so the waiting itself is out of line.
+// Not for the row warps, whose registers a call would spill.
+static __device__ __noinline__ bool wait_longer(volatile int* abort_flag, int32_t* status, uint64_t timeout_ns,
+                                                uint32_t bar, uint32_t parity, int32_t code)
+{
+    const WaitCtx w{abort_flag, status, timeout_ns};
+    return __all_sync(0xffffffffu, wait_bounded<true>(w, bar, parity, code));
+}
+__device__ __forceinline__ bool wait_w(const WaitCtx& w, uint32_t bar, uint32_t parity, int32_t code)
+{
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return wait_longer(w.abort_flag, w.status, w.timeout_ns, bar, parity, code);
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
                                             uint32_t bar)
 {
@@ -289,7 +305,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (!is_v) {
                 // the tile's Q as soon as its buffer is free
                 const int qs = qr.slot;
-                ok = wait_warp(wc, bar(bars->q_empty[qs]), qr.phase ^ 1, timeout_code(kSiteQEmpty));
+                ok = wait_w(wc, bar(bars->q_empty[qs]), qr.phase ^ 1, timeout_code(kSiteQEmpty));
                 if (!ok) break;
                 if (lane == 31) {
                     mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * G::ROWB * G::NCH);
@@ -312,7 +328,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 const int page = __shfl_sync(0xffffffffu, page_now, (first - window + (int)lane) & 31);
                 const int row = (j * 128 + (int)lane * rows_pp) & (t.page_size - 1);
-                ok = wait_warp(wc, bar(empty[st]), rg.phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
+                ok = wait_w(wc, bar(empty[st]), rg.phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
                 if (!ok) break;
                 const bool tail = is_v && rows < 128;
                 const uint32_t land = bar(tail ? bars->v_tail : full[st]);
@@ -325,7 +341,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 __syncwarp();
                 if (tail) {
-                    ok = wait_warp(wc, land, tails & 1, timeout_code(kSiteVTail));
+                    ok = wait_w(wc, land, tails & 1, timeout_code(kSiteVTail));
                     if (!ok) break;
                     ++tails;
                     // rows [rows, 128) of every chunk are contiguous
@@ -355,13 +371,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bool v_first = false;       // it is its tile's first
         auto issue_pv = [&]() -> bool {
             if (v_first) {
-                if (!wait_warp(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
+                if (!wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
                 o_phase ^= 1;
             }
             const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
             const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
-            if (!wait_warp(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull))) return false;
-            if (!wait_warp(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull))) return false;
+            if (!wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull))) return false;
+            if (!wait_w(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull))) return false;
             tc_fence_after();
             if constexpr (C::SPLIT) {
 #pragma unroll
@@ -390,10 +406,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 ok = issue_pv();
                 if (!ok) break;
             }
-            ok = wait_warp(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
+            ok = wait_w(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
             const uint32_t qbase = sb + C::OFF_Q + qr.slot * C::TILE;
             for (int j = g.j0; j < g.j1 && ok; ++j) {
-                ok = wait_warp(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull));
+                ok = wait_w(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t kbase = sb + C::OFF_K + rs.slot * C::TILE;
@@ -415,7 +431,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (ok && pending) ok = issue_pv();
         // every MMA must be complete before the CTA releases TMEM
         mma_commit(bar(bars->drain));
-        wait_warp(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
+        wait_w(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
     } else if (alive && warp >= 4) {
         // ---- softmax / epilogue: row = TMEM lane, half = which 64 keys of a block
         const RowThread rt = row_thread();
@@ -461,8 +477,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (!ok) break;
                 if (!warp_live) {                              // no row of this warp is used: only keep step
                     if constexpr (!C::SPLIT) {
-                        ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[bs.slot]), bs.phase,
-                                                                 timeout_code(kSiteXmax)));
+                        mbar_arrive(bar(bars->xmax[bs.slot]));
+                        ok = wait_warp(wc, bar(bars->xmax[bs.slot]), bs.phase, timeout_code(kSiteXmax));
                         if (!ok) break;
                     }
                     mbar_arrive(bar(bars->p_full[bs.slot]));
@@ -490,8 +506,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     tmem_st1(tX + bs.slot * 2 + h, __float_as_uint(mx));
                     tmem_st_wait();
                     tc_fence_before();
-                    ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->xmax[bs.slot]), bs.phase,
-                                                             timeout_code(kSiteXmax)));
+                    mbar_arrive(bar(bars->xmax[bs.slot]));
+                    ok = wait_warp(wc, bar(bars->xmax[bs.slot]), bs.phase, timeout_code(kSiteXmax));
                     if (!ok) break;
                     tc_fence_after();
                     mx = fmaxf(mx, __uint_as_float(tmem_ld1(tX + bs.slot * 2 + (h ^ 1))));
@@ -558,7 +574,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
             if constexpr (C::SPLIT) {
                 if (h == 1) xch[r] = make_float2(m_run, l_run);
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum)));
+                mbar_arrive(bar(bars->lsum));
+                ok = wait_warp(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum));
                 if (!ok) break;
                 if (h == 0) {
                     const float2 o1 = xch[r];
@@ -572,7 +589,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     lse2 = l_tot > 0.f ? m_ref + log2f(l_tot) : -INFINITY;
                     xch[r] = make_float2(a0, a1);
                 }
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum2), tile_phase, timeout_code(kSiteLsum)));
+                mbar_arrive(bar(bars->lsum2));
+                ok = wait_warp(wc, bar(bars->lsum2), tile_phase, timeout_code(kSiteLsum));
                 if (!ok) break;
                 if (h == 1) {
                     const float2 f = xch[r];
@@ -583,7 +601,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tmem_st1(tX + 4 + h, __float_as_uint(l_run));
                 tmem_st_wait();
                 tc_fence_before();
-                ok = __all_sync(0xffffffffu, row_barrier(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum)));
+                mbar_arrive(bar(bars->lsum));
+                ok = wait_warp(wc, bar(bars->lsum), tile_phase, timeout_code(kSiteLsum));
                 if (!ok) break;
                 tc_fence_after();
                 const float l_tot = l_run + __uint_as_float(tmem_ld1(tX + 4 + (h ^ 1)));
