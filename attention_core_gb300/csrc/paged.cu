@@ -21,8 +21,8 @@
 //   warp 2  V, into its own ring; rows past the sequence's end are zeroed in
 //           shared memory, so that what the page holds there (NaN included)
 //           meets no product
-//   warp 1  issues the tcgen05 MMAs: S_j = Q K_j^T, then O += P_{j-1} V_{j-1}
-//           with P read from TMEM
+//   warp 1  issues S_j = Q K_j^T (tcgen05) into one of two TMEM score buffers
+//   warp 3  issues O += P_j V_j with P read from TMEM
 //   warps 4-11  online softmax, one row per TMEM lane, two column halves of 64
 //           keys; for d <= 128 each half keeps its own maximum, sum and O
 //           accumulator, merged at the tile's end; for d = 160 TMEM has room
@@ -71,13 +71,14 @@ struct PagedCfg {
 };
 
 // Barriers of block g's ring slot st = g % ST serve every role that waits for the
-// same event, so the issuing warp commits twice per block: s_full (S_g is in TMEM;
-// K's slot is free) and pv_done (O has block g; V's slot and P are free).
+// same event, so each product is committed once: s_full (S_g is in TMEM; K's slot is free) and
+// pv_done (O has block g; V's slot and the score buffer with P are free).
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[6], v_full[6], s_full[6], pv_done[6];
+    uint64_t pv_issued[2];  // the P.V that reads the score buffer has been issued
     uint64_t v_tail;        // a tile's last, partial V block has landed (rows past its end still to be zeroed)
-    uint64_t drain;
+    uint64_t drain[2];      // every product of an issuing warp is done (before TMEM is released)
     uint64_t never;
     // completed by all row threads
     uint64_t p_full[2];     // P of the block is in TMEM
@@ -98,7 +99,7 @@ static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
     kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
-    kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteDrain
+    kSitePFull, kSiteSFull, kSitePvDone, kSitePvIssued, kSiteXmax, kSiteOFree, kSiteLsum, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -357,59 +358,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
         }
     } else if (alive && warp == 1) {
-        // ---- MMA issuer (the whole warp, see mma_ss): one stream over all blocks
-        // of all segments; P.V of a block goes after the next block's scores.  The
-        // products are ordered by their issue, so S of block g + 1 may overwrite the
-        // buffer that P.V of block g - 1 reads.
-        constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
-        constexpr uint32_t IDO = idesc_bf16(128, D, false, true);     // O += P V
-        Ring<ST> rs, rv;            // the next block's slot for S, and for P.V
-        Ring<2> bs, bv;             // their score buffers
+        // ---- S = Q K^T of every block (the whole warp issues, see mma_ss).  A score
+        // buffer holds S, then P, until its P.V has read it; the tensor pipe takes
+        // products in the order in which they are issued, so it is enough that the
+        // other warp has issued that P.V (the fences on both sides of the barrier
+        // carry the order from warp to warp).
+        constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);
+        Ring<ST> rs;
+        Ring<2> bs;
         Ring<C::NQ> qr;
-        uint32_t o_phase = 1;       // o_free: the first tile finds O free
-        bool pending = false;       // a block has its S but not its P.V
-        bool v_first = false;       // it is its tile's first
-        auto issue_pv = [&]() -> bool {
-            if (v_first) {
-                if (!wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
-                o_phase ^= 1;
-            }
-            const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
-            const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
-            if (!wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull))) return false;
-            if (!wait_w(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull))) return false;
-            tc_fence_after();
-            if constexpr (C::SPLIT) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + (kk >= 4 ? C::T_O1 : C::T_O), tP + (kk >= 4 ? 64 : 0) + 8 * (kk & 3),
-                           G::template desc_mn<128>(vbase, kk), IDO, (!v_first || (kk & 3) > 0) ? 1u : 0u);
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + C::T_O, tP + split_a_col(kk, 128), G::template desc_mn<128>(vbase, kk), IDO,
-                           (!v_first || kk > 0) ? 1u : 0u);
-            }
-            mma_commit(bar(bars->pv_done[rv.slot]));
-            rv.advance();
-            bv.advance();
-            pending = false;
-            return true;
-        };
         bool ok = true;
         Segment g;
         while (ok && next_work(walk, t, g)) {
-            // At a tile boundary the previous tile's last P.V goes first unless this
-            // tile's Q and first K block are already resident.
-            if (pending && (!test_wait_warp(bar(bars->q_full[qr.slot]), qr.phase) ||
-                            !test_wait_warp(bar(bars->k_full[rs.slot]), rs.phase))) {
-                ok = issue_pv();
-                if (!ok) break;
-            }
             ok = wait_w(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
             const uint32_t qbase = sb + C::OFF_Q + qr.slot * C::TILE;
             for (int j = g.j0; j < g.j1 && ok; ++j) {
-                ok = wait_w(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull));
+                ok = wait_w(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull)) &&
+                     wait_w(wc, bar(bars->pv_issued[bs.slot]), bs.phase ^ 1, timeout_code(kSitePvIssued));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t kbase = sb + C::OFF_K + rs.slot * C::TILE;
@@ -422,16 +387,52 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qr.slot]));
                 rs.advance();
                 bs.advance();
-                if (pending) ok = issue_pv();
-                pending = true;
-                v_first = j == g.j0;
             }
             qr.advance();
         }
-        if (ok && pending) ok = issue_pv();
         // every MMA must be complete before the CTA releases TMEM
-        mma_commit(bar(bars->drain));
-        wait_w(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
+        mma_commit(bar(bars->drain[0]));
+        wait_w(wc, bar(bars->drain[0]), 0, timeout_code(kSiteDrain));
+    } else if (alive && warp == 3) {
+        // ---- O += P V of every block, from a warp (and SM sub-partition) of its own: one
+        // warp issuing both products was what bounded compute-heavy batches (1870
+        // cycles a block at d = 128 where the products take 1040).
+        constexpr uint32_t IDO = idesc_bf16(128, D, false, true);
+        Ring<ST> rv;
+        Ring<2> bv;
+        uint32_t o_phase = 1;       // o_free: the first tile finds O free
+        bool ok = true;
+        Segment g;
+        while (ok && next_work(walk, t, g)) {
+            ok = wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree));
+            o_phase ^= 1;
+            for (int j = g.j0; j < g.j1 && ok; ++j) {
+                ok = wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull)) &&
+                     wait_w(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
+                const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
+                const uint32_t more = j > g.j0 ? 1u : 0u;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    if constexpr (C::SPLIT)
+                        mma_ts(tmem + (kk >= 4 ? C::T_O1 : C::T_O), tP + (kk >= 4 ? 64 : 0) + 8 * (kk & 3),
+                               G::template desc_mn<128>(vbase, kk), IDO, (kk & 3) > 0 ? 1u : more);
+                    else
+                        mma_ts(tmem + C::T_O, tP + split_a_col(kk, 128), G::template desc_mn<128>(vbase, kk), IDO,
+                               kk > 0 ? 1u : more);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bars->pv_issued[bv.slot]));
+                mma_commit(bar(bars->pv_done[rv.slot]));
+                rv.advance();
+                bv.advance();
+            }
+        }
+        mma_commit(bar(bars->drain[1]));
+        wait_w(wc, bar(bars->drain[1]), 0, timeout_code(kSiteDrain));
     } else if (alive && warp >= 4) {
         // ---- softmax / epilogue: row = TMEM lane, half = which 64 keys of a block
         const RowThread rt = row_thread();
