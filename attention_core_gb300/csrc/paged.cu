@@ -81,7 +81,7 @@ struct PagedBars {
     uint64_t drain[2];      // every product of an issuing warp is done (before TMEM is released)
     uint64_t never;
     // completed by all row threads
-    uint64_t p_full[2];     // P of the block is in TMEM
+    uint64_t p_full[2][2];  // [part][score buffer] P of the part (32 keys of each half) is in TMEM
     uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
     uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
     uint64_t o_free;        // the tile's O has been read
@@ -407,22 +407,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             ok = wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree));
             o_phase ^= 1;
             for (int j = g.j0; j < g.j1 && ok; ++j) {
-                ok = wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull)) &&
-                     wait_w(wc, bar(bars->p_full[bv.slot]), bv.phase, timeout_code(kSitePFull));
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
                 const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
                 const uint32_t more = j > g.j0 ? 1u : 0u;
+                ok = wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull));
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    if constexpr (C::SPLIT)
-                        mma_ts(tmem + (kk >= 4 ? C::T_O1 : C::T_O), tP + (kk >= 4 ? 64 : 0) + 8 * (kk & 3),
-                               G::template desc_mn<128>(vbase, kk), IDO, (kk & 3) > 0 ? 1u : more);
-                    else
-                        mma_ts(tmem + C::T_O, tP + split_a_col(kk, 128), G::template desc_mn<128>(vbase, kk), IDO,
-                               kk > 0 ? 1u : more);
+                for (int part = 0; part < 2 && ok; ++part) {
+                    ok = wait_w(wc, bar(bars->p_full[part][bv.slot]), bv.phase, timeout_code(kSitePFull));
+                    if (!ok) break;
+                    tc_fence_after();
+                    // key slices of 16: 0, 1 | 2, 3 of half 0, and of half 1
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = 4 * (i / 2) + 2 * part + (i & 1);
+                        const bool fresh = C::SPLIT ? (kk & 3) == 0 : kk == 0;     // the accumulator's first slice
+                        mma_ts(tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O), tP + split_a_col(kk, 128),
+                               G::template desc_mn<128>(vbase, kk), IDO, fresh ? more : 1u);
+                    }
                 }
+                if (!ok) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bars->pv_issued[bv.slot]));
@@ -482,7 +485,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         ok = wait_warp(wc, bar(bars->xmax[bs.slot]), bs.phase, timeout_code(kSiteXmax));
                         if (!ok) break;
                     }
-                    mbar_arrive(bar(bars->p_full[bs.slot]));
+                    mbar_arrive(bar(bars->p_full[0][bs.slot]));
+                    mbar_arrive(bar(bars->p_full[1][bs.slot]));
                     continue;
                 }
                 tc_fence_after();
@@ -499,10 +503,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     for (int c = 0; c < 64; ++c)
                         if (c >= left) x[c] = -INFINITY;
                 }
-                float mx = fmax3(x[0], x[1], x[2]);
+                float mx4[4];                                  // four chains: one would be 32 steps long
 #pragma unroll
-                for (int c = 3; c < 63; c += 2) mx = fmax3(mx, x[c], x[c + 1]);
-                mx = fmaxf(mx, x[63]);
+                for (int k = 0; k < 4; ++k) {
+                    mx4[k] = fmaxf(x[16 * k], x[16 * k + 1]);
+#pragma unroll
+                    for (int c = 2; c < 16; c += 2) mx4[k] = fmax3(mx4[k], x[16 * k + c], x[16 * k + c + 1]);
+                }
+                float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                 if constexpr (!C::SPLIT) {
                     tmem_st1(tX + bs.slot * 2 + h, __float_as_uint(mx));
                     tmem_st_wait();
@@ -549,25 +557,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
                 const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
                 uint64_t acc2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                uint32_t pw[32];
+                // P goes out in two parts of 32 keys a half, so that the first part's
+                // products run while the second is formed.
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float lo, hi;
-                    f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc2, nm2), lo, hi);
-                    lo = ex2_approx(lo);
-                    hi = ex2_approx(hi);
-                    acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(lo, hi));
-                    pw[e] = pack_bf16x2(lo, hi);
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float lo, hi;
+                        f2_unpack(f2_fma(f2_pack(x[32 * part + 2 * e], x[32 * part + 2 * e + 1]), sc2, nm2), lo, hi);
+                        lo = ex2_approx(lo);
+                        hi = ex2_approx(hi);
+                        acc2[e & 1] = f2_add(acc2[e & 1], f2_pack(lo, hi));
+                        pw[e] = pack_bf16x2(lo, hi);
+                    }
+                    tmem_st16(tS + 16 * part, pw);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(bar(bars->p_full[part][bs.slot]));
                 }
                 {
                     float lo, hi;
                     f2_unpack(f2_add(acc2[0], acc2[1]), lo, hi);
                     l_run += lo + hi;
                 }
-                tmem_st32(tS, pw);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(bar(bars->p_full[bs.slot]));
             }
             if (!ok) break;
             // Final row statistics: O = a0 O_0 + a1 O_1 (SPLIT), O = a0 O (else); a
