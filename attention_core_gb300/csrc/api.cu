@@ -1082,14 +1082,16 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
     if ((rc = device_sms(&a.num_sms))) return rc;
     // Pages: rows of one KV head of one page, [n_pages * h_kv][page_size][d].
     // Q: the group's heads of a run of tokens, [n_tokens][h_kv][group][d].
-    CUtensorMap tq, tk, tv;
+    // O as Q.
+    CUtensorMap tq, tk, tv, to;
     const int box = p->page_size < kBlockRows ? p->page_size : kBlockRows;
     const int64_t page_rows = (int64_t)p->n_pages * p->h_kv, page_elems = (int64_t)p->page_size * p->d;
     if ((rc = encode_map_strided(&tk, k_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
         (rc = encode_map_strided(&tv, v_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
-        (rc = encode_map_rows4(&tq, q, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)))
+        (rc = encode_map_rows4(&tq, q, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)) ||
+        (rc = encode_map_rows4(&to, o, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)))
         return rc;
-    return ac::launch_paged(tq, tk, tv, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA
+    return ac::launch_paged(tq, tk, tv, to, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA
                                                                                   : ATTN_CORE_OK;
 }
 

@@ -287,8 +287,8 @@ struct PagedArgs {
 };
 size_t paged_ws_bytes(int d);
 int paged_tokens_per_tile(int group);
-int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
-                 cudaStream_t stream);
+int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                 const PagedArgs& a, cudaStream_t stream);
 
 // Page copies (pages.cu): `pairs` is a host array.
 int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,

@@ -53,14 +53,18 @@ struct PagedCfg {
     static constexpr uint32_t TILE = G::template tile_bytes<128>();
     static constexpr uint32_t CHUNK = G::template chunk_bytes<128>();
     // One Q buffer (the next tile's Q loads behind this tile's last softmax and
-    // epilogue) leaves the most room for keys and values in flight.
+    // epilogue), K and V rings, and for d <= 128 a stage through which a full
+    // tile's O leaves by TMA.
     static constexpr int NQ = (D <= 64) ? 2 : 1;
-    static constexpr int ST = (D <= 64) ? 6 : (D <= 96 ? 4 : (D <= 128 ? 3 : 2));
+    static constexpr int SK = (D <= 64) ? 6 : (D <= 96 ? 4 : (D <= 128 ? 3 : 2));
+    static constexpr int SV = (D <= 64) ? 5 : (D <= 96 ? 3 : 2);
+    static constexpr bool STAGE_O = D <= 128;
     static constexpr bool SPLIT = (D <= 128);
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = NQ * TILE;
-    static constexpr uint32_t OFF_V = OFF_K + ST * TILE;
-    static constexpr uint32_t OFF_BAR = OFF_V + ST * TILE;
+    static constexpr uint32_t OFF_V = OFF_K + SK * TILE;
+    static constexpr uint32_t OFF_OST = OFF_V + SV * TILE;
+    static constexpr uint32_t OFF_BAR = OFF_OST + (STAGE_O ? TILE : 0);
     static constexpr uint32_t BAR_BYTES = 640;
     static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
     static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
@@ -70,7 +74,7 @@ struct PagedCfg {
     static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
 };
 
-// Barriers of block g's ring slot st = g % ST serve every role that waits for the
+// Barriers of block g's ring slots (g % SK for K, g % SV for V) serve every role that waits for the
 // same event, so each product is committed once: s_full (S_g is in TMEM; K's slot is free) and
 // pv_done (O has block g; V's slot and the score buffer with P are free).
 struct PagedBars {
@@ -85,13 +89,11 @@ struct PagedBars {
     uint64_t xmax[2];       // d = 160: row-max exchange between the column halves
     uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
     uint64_t o_free;        // the tile's O has been read
+    uint64_t ost_full;      // a full tile's O is in the stage
     uint32_t tmem_base;
     int32_t abort_flag;
     int64_t warp_sum[kThreads / 32];
-    // where this CTA's share starts
-    int64_t start_rel;      // units into the KV head
-    int32_t start_seq, start_head;
-    SeqTable start_table;
+    SegmentWalk walk;       // where this CTA's share starts
 };
 constexpr int kBarsOnce = offsetof(PagedBars, p_full) / 8;     // one arrival (a commit or a producer)
 constexpr int kBarsAll = offsetof(PagedBars, tmem_base) / 8;   // kRowThreads
@@ -99,7 +101,7 @@ static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
     kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
-    kSitePFull, kSiteSFull, kSitePvDone, kSitePvIssued, kSiteXmax, kSiteOFree, kSiteLsum, kSiteDrain
+    kSitePFull, kSiteSFull, kSitePvDone, kSitePvIssued, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -126,6 +128,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, uint32_t src, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+        ::"l"(reinterpret_cast<uint64_t>(tm)), "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
 
@@ -173,11 +183,10 @@ __device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const PagedArgs a)
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PagedArgs a)
 {
     using G = TileGeom<D>;
     using C = PagedCfg<D>;
-    constexpr int ST = C::ST;
     const PagedTables& t = a.t;
 
     extern __shared__ uint8_t smem_raw[];
@@ -246,31 +255,39 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     per = per > kMinUnits ? per : kMinUnits;
     const int64_t u0 = (int64_t)blockIdx.x * per;
     const int64_t u1 = u0 + per < total ? u0 + per : total;
-    if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
+    const bool found = u0 < u1 && u0 >= upto - mine && u0 < upto;
+    const uint32_t who = __ballot_sync(0xffffffffu, found);
+    if (who) {
+        // the warp that holds the first unit finds its tile, all lanes together
         int64_t rel = u0 - (upto - mine);
         int s = s0;
-        for (; run > 1; ++s) {                       // with one sequence a thread it is at hand
+        for (; found && run > 1; ++s) {              // with one sequence a thread it is at hand
             table = read_seq(t, s, a.tpt, a.causal);
             per_head = table.s.units(table.s.tiles());
             if (rel < per_head * t.h_kv) break;
             rel -= per_head * t.h_kv;
         }
+        const int src = __ffs(who) - 1;
+        s = __shfl_sync(0xffffffffu, s, src);
+        rel = __shfl_sync(0xffffffffu, rel, src);
+        per_head = __shfl_sync(0xffffffffu, per_head, src);
+        table = read_seq(t, s, a.tpt, a.causal);
         const int head = (int)quot(rel, per_head);
-        bars->start_seq = s;
-        bars->start_head = head;
-        bars->start_rel = rel - head * per_head;
-        bars->start_table = table;
+        SegmentWalk w;
+        w.tpt = a.tpt;
+        w.causal = a.causal;
+        w.start(s, table, head, rel - head * per_head, u0, u1);
+        if (lane == 0) bars->walk = w;
     }
+    if (threadIdx.x == 0 && u0 >= u1) bars->walk.at = bars->walk.end = 0;
     __syncthreads();
     const uint32_t tmem = bars->tmem_base;
     const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
-    SegmentWalk walk;
-    walk.tpt = a.tpt;
-    walk.causal = a.causal;
-    walk.at = walk.end = 0;
-    if (u0 < u1)
-        walk.start(bars->start_seq, bars->start_table, bars->start_head, bars->start_rel, u0, u1);
+    SegmentWalk walk = bars->walk;
     const int group = a.group;
+
+    // the join may take its place on the chip (it waits for this grid's end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true;
     if (a.inject_timeout) alive = wait_bounded(wc, bar(bars->never), 0, timeout_code(kSiteInject));
@@ -286,23 +303,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         uint64_t* empty = is_v ? bars->pv_done : bars->s_full;
         const uint32_t ring = sb + (is_v ? C::OFF_V : C::OFF_K);
         const int rows_pp = t.page_size < 128 ? t.page_size : 128;     // rows of a block from one page
-        Ring<ST> rg;
+        const int n_slots = is_v ? C::SV : C::SK;
+        int slot = 0;
+        uint32_t phase = 0;
         Ring<C::NQ> qr;
         int tails = 0;
         bool ok = true;
         Segment g;
         while (ok && next_work(walk, t, g)) {
-            const int32_t* entries = t.page_table + (int64_t)g.seq * t.max_pages;
-            const int n_entries = (g.kv + t.page_size - 1) >> t.page_shift;
-            auto entry = [&](int i) {
-                if (i >= n_entries) return -1;
-                const int page = entries[i];
-                if (page >= 0 && page < t.n_pages) return page;
-                if (t.status) atomicCAS(t.status, 0, kStatusTable);
-                return -1;
-            };
-            int window = ((g.j0 * 128) >> t.page_shift) & ~31;             // first entry of the 32 at hand
-            int page_now = entry(window + (int)lane), page_next = entry(window + 32 + (int)lane);
             if (!is_v) {
                 // the tile's Q as soon as its buffer is free
                 const int qs = qr.slot;
@@ -317,8 +325,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 __syncwarp();
                 qr.advance();
             }
-            for (int j = g.j0; j < g.j1; ++j, rg.advance()) {
-                const int st = rg.slot;
+            const int32_t* entries = t.page_table + (int64_t)g.seq * t.max_pages;
+            const int n_entries = (g.kv + t.page_size - 1) >> t.page_shift;
+            auto entry = [&](int i) { return i < n_entries ? entries[i] : -1; };
+            int window = ((g.j0 * 128) >> t.page_shift) & ~31;             // first entry of the 32 at hand
+            int page_now = entry(window + (int)lane), page_next = entry(window + 32 + (int)lane);
+            for (int j = g.j0; j < g.j1; ++j) {
+                const int st = slot;
                 const int rows = g.kv - j * 128 < 128 ? g.kv - j * 128 : 128;     // keys of the block
                 const int pages = (rows + rows_pp - 1) / rows_pp;
                 const int first = (j * 128) >> t.page_shift;                      // a block's entries share a window
@@ -329,14 +342,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 const int page = __shfl_sync(0xffffffffu, page_now, (first - window + (int)lane) & 31);
                 const int row = (j * 128 + (int)lane * rows_pp) & (t.page_size - 1);
-                ok = wait_w(wc, bar(empty[st]), rg.phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
+                ok = wait_w(wc, bar(empty[st]), phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
                 if (!ok) break;
+                if (++slot == n_slots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
                 const bool tail = is_v && rows < 128;
                 const uint32_t land = bar(tail ? bars->v_tail : full[st]);
                 if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages * rows_pp) * G::ROWB * G::NCH);
                 __syncwarp();
                 if ((int)lane < pages) {
-                    const int z = page < 0 ? -1 : page * t.h_kv + g.head;
+                    int z = page * t.h_kv + g.head;
+                    if (page < 0 || page >= t.n_pages) {
+                        z = -1;
+                        if (t.status) atomicCAS(t.status, 0, kStatusTable);
+                    }
                     const uint32_t dst = ring + st * C::TILE + (uint32_t)((int)lane * rows_pp) * G::ROWB;
                     for (int ch = 0; ch < G::NCH; ++ch) tma_load_3d(dst + ch * C::CHUNK, tm, ch * G::CW, row, z, land);
                 }
@@ -364,7 +385,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // other warp has issued that P.V (the fences on both sides of the barrier
         // carry the order from warp to warp).
         constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);
-        Ring<ST> rs;
+        Ring<C::SK> rs;
         Ring<2> bs;
         Ring<C::NQ> qr;
         bool ok = true;
@@ -398,7 +419,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // warp issuing both products was what bounded compute-heavy batches (1870
         // cycles a block at d = 128 where the products take 1040).
         constexpr uint32_t IDO = idesc_bf16(128, D, false, true);
-        Ring<ST> rv;
+        Ring<C::SV> rv;
         Ring<2> bv;
         uint32_t o_phase = 1;       // o_free: the first tile finds O free
         bool ok = true;
@@ -444,9 +465,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t tX = tmem + C::T_X + lane_off;
         float2* xch = reinterpret_cast<float2*>(smem_raw + pad + C::OFF_XCH);
         const int r_tok = r / group, r_head = r % group;       // row r: token r_tok of the tile, head r_head of the group
-        Ring<ST> rg;                // this block's slot
-        Ring<2> bs;                 // and score buffer
-        uint32_t tile_phase = 0;
+        Ring<C::SK> rg;             // this block's slot of K
+        Ring<C::SV> rv;             // and of V
+        Ring<2> bs;                 // and its score buffer
+        uint32_t tile_phase = 0, stage_phase = 0;
         bool ok = true;
         Segment g;
         while (ok && walk.next(t, g)) {
@@ -474,8 +496,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const uint32_t tO1 = tmem + C::T_O1 + lane_off;
             const uint32_t tOh = (C::SPLIT && h) ? tO1 : tO;
             float m_run = -INFINITY, l_run = 0.f;
-            Ring<ST> before = rg;                              // the block before this one
-            for (int j = 0; j < nk; ++j, before = rg, rg.advance(), bs.advance()) {
+            Ring<C::SV> before = rv;                           // the block before this one
+            for (int j = 0; j < nk; ++j, before = rv, rv.advance(), rg.advance(), bs.advance()) {
                 const uint32_t tS = tmem + (bs.slot ? C::T_S1 : C::T_S0) + lane_off + 64 * h;
                 ok = wait_warp(wc, bar(bars->s_full[rg.slot]), rg.phase, timeout_code(kSiteSFull));
                 if (!ok) break;
@@ -586,6 +608,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // Final row statistics: O = a0 O_0 + a1 O_1 (SPLIT), O = a0 O (else); a
             // row that saw no key has l = 0 and gets zeros.
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
+            // a full tile's O leaves through the stage: free once its last store has read it
+            const bool staged = C::STAGE_O && g.whole && g.n_tok == a.tpt;
+            if (staged && h == 0 && r == 0) bulk_wait_read0();
             if constexpr (C::SPLIT) {
                 if (h == 1) xch[r] = make_float2(m_run, l_run);
                 mbar_arrive(bar(bars->lsum));
@@ -652,7 +677,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(rr[e]) * a0;
                     }
-                    if (live && g.whole) {
+                    if (staged) {
+#pragma unroll
+                        for (int u4 = 0; u4 < 4; ++u4)
+                            st_shared_v4(sb + C::OFF_OST + G::template unit_offset<128>(r, c32 * 32 + 8 * u4),
+                                         pack_bf16x2(f[8 * u4], f[8 * u4 + 1]), pack_bf16x2(f[8 * u4 + 2], f[8 * u4 + 3]),
+                                         pack_bf16x2(f[8 * u4 + 4], f[8 * u4 + 5]),
+                                         pack_bf16x2(f[8 * u4 + 6], f[8 * u4 + 7]));
+                    } else if (live && g.whole) {
 #pragma unroll
                         for (int u4 = 0; u4 < 4; ++u4)
                             reinterpret_cast<uint4*>(orow)[c32 * 4 + u4] =
@@ -677,7 +709,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             tc_fence_before();
             mbar_arrive(bar(bars->o_free));
             tile_phase ^= 1;
+            if (staged) {
+                fence_proxy_async_smem();
+                mbar_arrive(bar(bars->ost_full));
+                if (warp == 4) {
+                    ok = wait_warp(wc, bar(bars->ost_full), stage_phase, timeout_code(kSiteStage));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        for (int ch = 0; ch < G::NCH; ++ch)
+                            tma_store_4d(&tm_o, sb + C::OFF_OST + ch * C::CHUNK, ch * G::CW, 0, g.head, g.q_tok);
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                }
+                stage_phase ^= 1;
+            }
         }
+        // the last O store must have read the stage before the CTA exits
+        if (h == 0 && r == 0) bulk_wait_read0();
     }
 
     __syncthreads();
@@ -693,58 +742,61 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
 }
 
-// Joins the parts of the tiles that were cut: block (c, y) takes every gridDim.y-th
-// row of the tile that CTA c cut at its end, a warp per row, lanes over d.  The parts'
-// weights are formed by lanes over the parts.
+// Joins the parts of the tiles that were cut: block (c, y) takes rows 4y .. 4y + 3 of
+// the tile that CTA c cut at its end, a warp per row.  Lanes over the parts form the
+// weights, lanes over d (16 bytes each) the sums; up to eight parts' loads are in
+// flight.  Launched while the attention kernel still runs, it waits for its end.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedTables& t = a.t;
     const CutTile cut = reinterpret_cast<const CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x];
-    if (cut.last_cta == 0) return;
-    __shared__ float weight[4][kPagedMaxCtas];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = (int)blockIdx.y * 4 + warp;
+    if (cut.last_cta == 0 || r >= cut.n_rows) return;
+    __shared__ float weight[4][kPagedMaxCtas];
     const int parts = cut.last_cta - (int)blockIdx.x + 1;
     const float* lse = reinterpret_cast<const float*>(a.ws + ws_lse_offset(D));
     const float* rows = reinterpret_cast<const float*>(a.ws);
-    auto row_of = [&](int p, int r) { return part_row((int)blockIdx.x + p, p == 0 ? 1 : 0) + r; };
-    for (int r = (int)blockIdx.y * 4 + warp; r < cut.n_rows; r += 4 * (int)gridDim.y) {
-        float mx = -INFINITY;
-        for (int p = lane; p < parts; p += 32) {
-            const float x = lse[row_of(p, r)];
-            weight[warp][p] = x;
-            mx = fmaxf(mx, x);
-        }
+    auto row_of = [&](int p) { return part_row((int)blockIdx.x + p, p == 0 ? 1 : 0) + r; };
+    float mx = -INFINITY;
+    for (int p = lane; p < parts; p += 32) {
+        const float x = lse[row_of(p)];
+        weight[warp][p] = x;
+        mx = fmaxf(mx, x);
+    }
 #pragma unroll
-        for (int o = 16; o; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_ref = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
-        for (int p = lane; p < parts; p += 32) {
-            const float w = exp2f(weight[warp][p] - m_ref);
-            weight[warp][p] = w;
-            sum += w;
-        }
+    for (int o = 16; o; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float m_ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    for (int p = lane; p < parts; p += 32) {
+        const float w = exp2f(weight[warp][p] - m_ref);
+        weight[warp][p] = w;
+        sum += w;
+    }
 #pragma unroll
-        for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncwarp();
-        float acc[D / 32] = {};
-#pragma unroll 4
+    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const int tok = cut.q_tok + r / a.group, head = cut.head * a.group + r % a.group;
+    uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D;
+    for (int c = lane * 4; c < D; c += 128) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int p = 0; p < parts; ++p) {
             const float w = weight[warp][p];
-            const float* src = rows + row_of(p, r) * D + lane;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] += w * src[e * 32];
+            const float4 x = *reinterpret_cast<const float4*>(rows + row_of(p) * D + c);
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
         }
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        const int tok = cut.q_tok + r / a.group, head = cut.head * a.group + r % a.group;
-        uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D + lane;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) orow[e * 32] = (uint16_t)(pack_bf16x2(acc[e] * inv, 0.f) & 0xffffu);
-        if (lane == 0)
-            a.lse[(size_t)head * t.n_tokens + tok] =
-                sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945309f : -INFINITY;
-        __syncwarp();
+        *reinterpret_cast<uint2*>(orow + c) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     }
+    if (lane == 0)
+        a.lse[(size_t)head * t.n_tokens + tok] = sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945309f : -INFINITY;
 }
 
 size_t paged_ws_bytes(int d)
@@ -758,7 +810,7 @@ int paged_tokens_per_tile(int group) { return 128 / group; }
 namespace {
 
 template <int D>
-int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, const PagedArgs& a,
                    cudaStream_t st)
 {
     constexpr uint32_t smem = PagedCfg<D>::SMEM;
@@ -772,28 +824,35 @@ int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     const int64_t want = (tiles * a.t.h_kv * blocks + kMinUnits - 1) / kMinUnits;
     int grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
     if (want < grid) grid = (int)want;
-    kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, a);
+    kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, to, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
     if (grid > 1 && blocks > kSnap) {
         const int64_t rows = (int64_t)a.tpt * a.group < (int64_t)a.t.n_tokens * a.group ? (int64_t)a.tpt * a.group
                                                                                       : (int64_t)a.t.n_tokens * a.group;
-        const unsigned y = rows > 32 ? 8u : (unsigned)((rows + 3) / 4);
-        paged_join_kernel<D><<<dim3((unsigned)grid, y), 128, 0, st>>>(a);
-        e = cudaGetLastError();
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + 3) / 4));
+        cfg.blockDim = dim3(128);
+        cfg.stream = st;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
     }
     return (int)e;
 }
 
 }  // namespace
 
-int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, const PagedArgs& a,
                  cudaStream_t st)
 {
     switch (a.d) {
-        case 64: return launch_paged_t<64>(tq, tk, tv, a, st);
-        case 96: return launch_paged_t<96>(tq, tk, tv, a, st);
-        case 128: return launch_paged_t<128>(tq, tk, tv, a, st);
-        case 160: return launch_paged_t<160>(tq, tk, tv, a, st);
+        case 64: return launch_paged_t<64>(tq, tk, tv, to, a, st);
+        case 96: return launch_paged_t<96>(tq, tk, tv, to, a, st);
+        case 128: return launch_paged_t<128>(tq, tk, tv, to, a, st);
+        case 160: return launch_paged_t<160>(tq, tk, tv, to, a, st);
         default: return (int)cudaErrorInvalidValue;
     }
 }
