@@ -945,6 +945,11 @@ int check_paged(const attn_core_paged_params* p)
         (int64_t)p->max_pages * ps >= (int64_t)INT32_MAX - 2 * kBlockRows ||
         (int64_t)p->n_tokens * p->h_q >= (int64_t)INT32_MAX)
         return ATTN_CORE_ERR_INVALID_ARG;
+    // the units of work of one KV head (paged_sched.cuh)
+    const int64_t tpt = ac::paged_tokens_per_tile(p->h_q / p->h_kv);
+    if ((p->n_tokens + tpt - 1) / tpt * (((int64_t)p->max_pages * ps + kBlockRows - 1) / kBlockRows) >=
+        (int64_t)INT32_MAX || p->n_tokens >= INT32_MAX - 2 * kBlockRows)
+        return ATTN_CORE_ERR_UNSUPPORTED;
     for (const void* t : {(const void*)p->cu_seqlens_q, (const void*)p->kv_lens, (const void*)p->page_table})
         if (reinterpret_cast<uintptr_t>(t) & 3u) return ATTN_CORE_ERR_MISALIGNED;
     return ATTN_CORE_OK;

@@ -16,8 +16,7 @@
 // Persistent, one CTA per SM; each takes an equal share of all blocks
 // (paged_sched.cuh), cutting long tiles.  Structure (384 threads), as the
 // forward of the core:
-//   warp 0  K: lane i loads page i of a block (its page_table entry and one TMA
-//           per column chunk); lane 31 also each tile's Q
+//   warp 0  K, by TMA: one box per page and column chunk; and each tile's Q
 //   warp 2  V, into its own ring; rows past the sequence's end are zeroed in
 //           shared memory, so that what the page holds there (NaN included)
 //           meets no product
@@ -35,6 +34,8 @@
 // rows divided by their own sum, with their own base-2 LSE, and a second kernel
 // joins them: O = sum_p w_p O_p / sum_p w_p, w_p = 2^(lse_p - max).
 #include <stddef.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged_sched.cuh"
@@ -118,19 +119,34 @@ static __device__ __noinline__ bool wait_longer(volatile int* abort_flag, int32_
 __device__ __forceinline__ bool wait_w(const WaitCtx& w, uint32_t bar, uint32_t parity, int32_t code)
 {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-    return wait_longer(w.abort_flag, w.status, w.timeout_ns, bar, parity, code);
+    return __all_sync(0xffffffffu, wait_longer(w.abort_flag, w.status, w.timeout_ns, bar, parity, code));
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
-                                            uint32_t bar)
+// TMA loads issued by whole warps: called converged by all 32 lanes, elect.sync
+// picks the one that issues.  The operands stay in warp-uniform code: 15 to 28
+// cycles a load, against 53 when a lane per page issues its own and 65 from
+// inside an `if (lane == 0)` (16 loads of 2 KB from one warp).
+__device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_warp(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                                                 uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
-
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, uint32_t src, int x, int y, int z, int w)
 {
     asm volatile(
@@ -169,13 +185,33 @@ struct Ring {
     }
 };
 
-// The next segment with blocks to visit (the others only have zeros to write,
-// which is the row threads' business).
-__device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, Segment& g)
+// A value that all lanes of a warp hold alike, in a form that the compiler knows to
+// be warp-uniform.  The producing and issuing warps' operands (descriptors,
+// coordinates, barriers) then live in uniform registers; from ordinary ones each
+// TMA load or product pays for moving its operands over (88 cycles a load, 40 a
+// product, against 28 and 23).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The next segment with blocks to visit, for the producing and issuing warps (the
+// other segments only have zeros to write, which is the row threads' business).
+struct Work {
+    int seq, head, q_tok, kv, j0, j1;
+};
+__device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, Work& k)
 {
-    while (w.next(t, g))
-        if (g.j1 > g.j0) return true;
-    return false;
+    Segment g;
+    bool more;
+    do {
+        more = w.next(t, g);
+    } while (more && g.j1 <= g.j0);
+    if (!__all_sync(0xffffffffu, more)) return false;
+    k.seq = uniform(g.seq);
+    k.head = uniform(g.head);
+    k.q_tok = uniform(g.q_tok);
+    k.kv = uniform(g.kv);
+    k.j0 = uniform(g.j0);
+    k.j1 = uniform(g.j1);
+    return true;
 }
 
 }  // namespace
@@ -195,7 +231,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t sb = raw + pad;
     PagedBars* bars = reinterpret_cast<PagedBars*>(smem_raw + pad + C::OFF_BAR);
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
-    const uint32_t warp = warp_id(), lane = lane_id();
+    const uint32_t warp = (uint32_t)uniform((int)warp_id()), lane = lane_id();
 
     // Set-up, spread over the warps: warp 3 the barriers, warp 1 TMEM, warp 0 the
     // descriptors, and from warp 4 on the lengths.
@@ -226,13 +262,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int run = (t.n_seq + kThreads - 1) / kThreads;
     const int s0 = order * run < t.n_seq ? order * run : t.n_seq;
     const int s1 = s0 + run < t.n_seq ? s0 + run : t.n_seq;
-    int64_t mine = 0, per_head = 0;
+    int64_t mine = 0;
+    int per_head = 0;
     SeqTable table{};
     for (int s = s0; s < s1; ++s) {
         table = read_seq(t, s, a.tpt, a.causal);
         if (table.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
         per_head = table.s.units(table.s.tiles());
-        mine += per_head * t.h_kv;
+        mine += (int64_t)per_head * t.h_kv;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -264,8 +301,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (; found && run > 1; ++s) {              // with one sequence a thread it is at hand
             table = read_seq(t, s, a.tpt, a.causal);
             per_head = table.s.units(table.s.tiles());
-            if (rel < per_head * t.h_kv) break;
-            rel -= per_head * t.h_kv;
+            if (rel < (int64_t)per_head * t.h_kv) break;
+            rel -= (int64_t)per_head * t.h_kv;
         }
         const int src = __ffs(who) - 1;
         s = __shfl_sync(0xffffffffu, s, src);
@@ -276,12 +313,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         SegmentWalk w;
         w.tpt = a.tpt;
         w.causal = a.causal;
-        w.start(s, table, head, rel - head * per_head, u0, u1);
+        w.start(s, table, head, (int)(rel - (int64_t)head * per_head), u0, u1);
         if (lane == 0) bars->walk = w;
     }
     if (threadIdx.x == 0 && u0 >= u1) bars->walk.at = bars->walk.end = 0;
     __syncthreads();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = (uint32_t)uniform((int)bars->tmem_base);
     const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
     SegmentWalk walk = bars->walk;
     const int group = a.group;
@@ -290,39 +327,34 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true;
-    if (a.inject_timeout) alive = wait_bounded(wc, bar(bars->never), 0, timeout_code(kSiteInject));
+    if (a.inject_timeout) alive = wait_warp(wc, bar(bars->never), 0, timeout_code(kSiteInject));
 
-    if (alive && (warp == 0 || warp == 2)) {
-        // ---- TMA producers.  The page_table entries of a tile come 32 at a time, one
-        // a lane, the next 32 on their way; a block's pages go to one lane each, which
-        // issues the page's column chunks.  A page outside the cache reads as zeros
-        // (coordinates outside the tensor map) and is reported.
-        const bool is_v = warp == 2;
-        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-        uint64_t* full = is_v ? bars->v_full : bars->k_full;
-        uint64_t* empty = is_v ? bars->pv_done : bars->s_full;
-        const uint32_t ring = sb + (is_v ? C::OFF_V : C::OFF_K);
-        const int rows_pp = t.page_size < 128 ? t.page_size : 128;     // rows of a block from one page
-        const int n_slots = is_v ? C::SV : C::SK;
+    // ---- TMA producers.  The page_table entries of a tile come 32 at a time, one a
+    // lane, the next 32 on their way.  A page outside the cache reads as zeros
+    // (coordinates outside the tensor map) and is reported.
+    auto produce = [&](auto which, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, uint32_t ring) {
+        constexpr bool is_v = decltype(which)::value;
+        constexpr int n_slots = is_v ? C::SV : C::SK;
+        const int rows_shift = t.page_shift < 7 ? t.page_shift : 7;    // rows of a block from one page
         int slot = 0;
         uint32_t phase = 0;
         Ring<C::NQ> qr;
         int tails = 0;
         bool ok = true;
-        Segment g;
+        Work g;
         while (ok && next_work(walk, t, g)) {
-            if (!is_v) {
+            if constexpr (!is_v) {
                 // the tile's Q as soon as its buffer is free
                 const int qs = qr.slot;
                 ok = wait_w(wc, bar(bars->q_empty[qs]), qr.phase ^ 1, timeout_code(kSiteQEmpty));
                 if (!ok) break;
-                if (lane == 31) {
+                if (lane == 0)
                     mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * G::ROWB * G::NCH);
-                    for (int ch = 0; ch < G::NCH; ++ch)
-                        tma_load_4d(sb + C::OFF_Q + qs * C::TILE + ch * C::CHUNK, &tm_q, ch * G::CW, 0, g.head, g.q_tok,
-                                    bar(bars->q_full[qs]));
-                }
                 __syncwarp();
+#pragma unroll
+                for (int ch = 0; ch < G::NCH; ++ch)
+                    tma_load_4d_warp(sb + C::OFF_Q + qs * C::TILE + ch * C::CHUNK, &tm_q, ch * G::CW, 0, g.head, g.q_tok,
+                                     bar(bars->q_full[qs]));
                 qr.advance();
             }
             const int32_t* entries = t.page_table + (int64_t)g.seq * t.max_pages;
@@ -333,15 +365,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int j = g.j0; j < g.j1; ++j) {
                 const int st = slot;
                 const int rows = g.kv - j * 128 < 128 ? g.kv - j * 128 : 128;     // keys of the block
-                const int pages = (rows + rows_pp - 1) / rows_pp;
+                const int pages = (rows + (1 << rows_shift) - 1) >> rows_shift;
                 const int first = (j * 128) >> t.page_shift;                      // a block's entries share a window
                 if (first >= window + 32) {
                     window += 32;
                     page_now = page_next;
                     page_next = entry(window + 32 + (int)lane);
                 }
-                const int page = __shfl_sync(0xffffffffu, page_now, (first - window + (int)lane) & 31);
-                const int row = (j * 128 + (int)lane * rows_pp) & (t.page_size - 1);
                 ok = wait_w(wc, bar(empty[st]), phase ^ 1, timeout_code(is_v ? kSiteVEmpty : kSiteKEmpty));
                 if (!ok) break;
                 if (++slot == n_slots) {
@@ -350,18 +380,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 const bool tail = is_v && rows < 128;
                 const uint32_t land = bar(tail ? bars->v_tail : full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages * rows_pp) * G::ROWB * G::NCH);
+                if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages << rows_shift) * G::ROWB * G::NCH);
                 __syncwarp();
-                if ((int)lane < pages) {
+#pragma unroll 2
+                for (int p = 0; p < pages; ++p) {
+                    const int page = __shfl_sync(0xffffffffu, page_now, first - window + p);
                     int z = page * t.h_kv + g.head;
                     if (page < 0 || page >= t.n_pages) {
                         z = -1;
-                        if (t.status) atomicCAS(t.status, 0, kStatusTable);
+                        if (lane == 0 && t.status) atomicCAS(t.status, 0, kStatusTable);
+                        __syncwarp();
                     }
-                    const uint32_t dst = ring + st * C::TILE + (uint32_t)((int)lane * rows_pp) * G::ROWB;
-                    for (int ch = 0; ch < G::NCH; ++ch) tma_load_3d(dst + ch * C::CHUNK, tm, ch * G::CW, row, z, land);
+                    const int row = (j * 128 + (p << rows_shift)) & (t.page_size - 1);
+                    const uint32_t dst = ring + st * C::TILE + (uint32_t)(p << rows_shift) * G::ROWB;
+#pragma unroll
+                    for (int ch = 0; ch < G::NCH; ++ch)
+                        tma_load_3d_warp(dst + ch * C::CHUNK, tm, ch * G::CW, row, z, land);
                 }
-                __syncwarp();
                 if (tail) {
                     ok = wait_w(wc, land, tails & 1, timeout_code(kSiteVTail));
                     if (!ok) break;
@@ -378,6 +413,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
             }
         }
+    };
+    if (alive && warp == 0) {
+        produce(std::false_type{}, &tm_k, bars->k_full, bars->s_full, sb + C::OFF_K);
+    } else if (alive && warp == 2) {
+        produce(std::true_type{}, &tm_v, bars->v_full, bars->pv_done, sb + C::OFF_V);
     } else if (alive && warp == 1) {
         // ---- S = Q K^T of every block (the whole warp issues, see mma_ss).  A score
         // buffer holds S, then P, until its P.V has read it; the tensor pipe takes
@@ -389,7 +429,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         Ring<2> bs;
         Ring<C::NQ> qr;
         bool ok = true;
-        Segment g;
+        Work g;
         while (ok && next_work(walk, t, g)) {
             ok = wait_w(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
             const uint32_t qbase = sb + C::OFF_Q + qr.slot * C::TILE;
@@ -423,7 +463,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         Ring<2> bv;
         uint32_t o_phase = 1;       // o_free: the first tile finds O free
         bool ok = true;
-        Segment g;
+        Work g;
         while (ok && next_work(walk, t, g)) {
             ok = wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree));
             o_phase ^= 1;
@@ -489,8 +529,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // keys that this row sees
             int lim = g.kv;
             if (a.causal) {
-                const int64_t seen = g.first_pos + r_tok + 1;
-                lim = seen < g.kv ? (int)(seen > 0 ? seen : 0) : g.kv;
+                const int seen = g.first_pos + r_tok + 1;
+                lim = seen < g.kv ? (seen > 0 ? seen : 0) : g.kv;
             }
             const uint32_t tO = tmem + C::T_O + lane_off;
             const uint32_t tO1 = tmem + C::T_O1 + lane_off;

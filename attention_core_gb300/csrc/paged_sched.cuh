@@ -24,47 +24,50 @@ namespace ac {
 constexpr int kSnap = 4;        // tiles of at most this many blocks stay whole
 constexpr int kMinUnits = 2;    // least share of a CTA
 
-// a / b; lengths are 31-bit numbers, so the quotients nearly always fit the
-// 32-bit divide, which takes a fraction of the 64-bit one's time
+// a / b in the 32-bit divide where both fit (nearly always), which takes a
+// fraction of the 64-bit one's time
 __host__ __device__ inline int64_t quot(int64_t a, int64_t b)
 {
     if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
     return (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// sum over i = 0 .. n - 1 of floor((a i + b) / m); a, b >= 0, m > 0
-__host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+// sum over i = 0 .. n - 1 of floor((a i + b) / m), m > 0, where the sum and
+// a n + b fit 32 bits (no partial sum is larger)
+__host__ __device__ inline uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
 {
-    int64_t s = 0;
+    uint32_t s = 0;
     while (n > 0) {
-        const int64_t qa = quot(a, m), qb = quot(b, m);
-        s += (n - 1) * n / 2 * qa + n * qb;
+        const uint32_t qa = a / m, qb = b / m;
+        if (qa) s += (n - 1) * n / 2 * qa;
+        s += n * qb;
         a -= qa * m;
         b -= qb * m;
         if (a == 0) break;
-        const int64_t top = a * n + b;
-        n = quot(top, m);
+        const uint32_t top = a * n + b;
+        n = top / m;
         b = top - n * m;
-        const int64_t t = m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
     return s;
 }
 
-// One sequence's shape: nq new tokens, kv keys, tiles of tpt tokens.
+// One sequence's shape: nq new tokens, kv keys (both below 2^31 - 256), tiles of
+// tpt tokens.  The units of one KV head fit 31 bits (the caller sees to it).
 struct SeqShape {
     int nq, kv, tpt, causal;
-    __host__ __device__ int tiles() const { return (int)quot((int64_t)nq + tpt - 1, tpt); }
+    __host__ __device__ int tiles() const { return (int)(((uint32_t)nq + tpt - 1) / (uint32_t)tpt); }
     // blocks of 128 keys that tile m sees: those of its last row
     __host__ __device__ int blocks(int m) const
     {
-        int64_t last = kv;
+        int last = kv;
         if (causal) {
-            const int64_t end = (int64_t)kv - nq + (int64_t)(m + 1) * tpt;
+            const int end = kv - nq + (m + 1) * tpt;
             last = end < kv ? end : kv;
         }
-        return last <= 0 ? 0 : (int)((last + 127) / 128);
+        return last <= 0 ? 0 : (int)(((uint32_t)last + 127) / 128);
     }
     __host__ __device__ int cost(int m) const
     {
@@ -72,27 +75,36 @@ struct SeqShape {
         return n > 0 ? n : 1;
     }
     // units of the tiles 0 .. m - 1
-    __host__ __device__ int64_t units(int m) const
-    {
-        if (m <= 0) return 0;
-        if (kv <= 0) return m;
-        if (!causal) return (int64_t)m * cost(0);
-        const int64_t e = (int64_t)kv - nq;                  // keys before the first new token
-        const int last = tiles() - 1;                        // sees kv keys, however many rows it has
-        int64_t z = e < 0 ? quot(-e, tpt) : 0;                    // tiles that see nothing: one unit each
-        if (z > m) z = m;
-        const int64_t plain = (m < last ? m : last) - z;     // tiles that see e + (i + 1) tpt keys
-        int64_t s = z;
-        if (plain > 0) s += floor_sum(plain, 128, tpt, e + (z + 1) * tpt + 127);
-        if (m > last) s += cost(last);
-        return s;
-    }
+    __host__ __device__ int units(int m) const;
 };
+
+// One copy, by value: instructions are fetched cold at a kernel's start, and
+// inlining this at each use made them the largest part of it.
+#ifdef __CUDA_ARCH__
+__noinline__
+#endif
+__host__ __device__ inline int units_before(int m, int nq, int kv, int tpt, int causal)
+{
+    const SeqShape q{nq, kv, tpt, causal};
+    if (m <= 0) return 0;
+    if (kv <= 0) return m;
+    if (!causal) return m * q.cost(0);
+    const int e = kv - nq;                                   // keys before the first new token
+    const int last = q.tiles() - 1;                          // sees kv keys, however many rows it has
+    int z = e < 0 ? (int)((uint32_t)-e / (uint32_t)tpt) : 0; // tiles that see nothing: one unit each
+    if (z > m) z = m;
+    const int plain = (m < last ? m : last) - z;             // tiles that see e + (i + 1) tpt keys
+    uint32_t s = z;
+    if (plain > 0) s += floor_sum(plain, 128, tpt, e + (z + 1) * tpt + 127);
+    if (m > last) s += q.cost(last);
+    return (int)s;
+}
+__host__ __device__ inline int SeqShape::units(int m) const { return units_before(m, nq, kv, tpt, causal); }
 
 // The last row tile of a head that starts at or before unit r of it.  On the
 // device a whole warp calls this with one r: each round its lanes test 32
 // candidates.
-__host__ __device__ inline int find_tile(const SeqShape& s, int64_t r)
+__host__ __device__ inline int find_tile(const SeqShape& s, int r)
 {
     int lo = 0, hi = s.tiles();
     while (hi - lo > 1) {
@@ -132,7 +144,7 @@ struct Segment {
     int seq, head, m;      // sequence, KV head, row tile
     int q_tok, n_tok;      // first token (row of q) and tokens of the tile
     int kv;                // keys of the sequence
-    int64_t first_pos;     // position of the tile's first token
+    int first_pos;         // position of the tile's first token (negative: no key for it)
     int j0, j1;            // blocks of this piece; both 0: the tile sees no key
     bool whole;            // the whole tile
     bool from_start;       // the tile's first unit is in it
@@ -151,7 +163,7 @@ struct SegmentWalk {
 
     // Unit `at_` lies r units into KV head h of sequence sq.  (Whole warps, see
     // find_tile.)
-    __host__ __device__ void start(int sq, const SeqTable& table, int h, int64_t r, int64_t at_, int64_t end_)
+    __host__ __device__ void start(int sq, const SeqTable& table, int h, int r, int64_t at_, int64_t end_)
     {
         at = at_;
         end = end_;
@@ -159,7 +171,7 @@ struct SegmentWalk {
         cur = table;
         head = h;
         m = find_tile(cur.s, r);
-        b = (int)(r - cur.s.units(m));
+        b = r - cur.s.units(m);
         const int n = cur.s.cost(m);
         if (b > 0 && n <= kSnap) {                           // another CTA has all of this tile
             at += n - b;
@@ -196,7 +208,7 @@ struct SegmentWalk {
         g.q_tok = cur.q0 + m * tpt;
         g.n_tok = cur.s.nq - m * tpt < tpt ? cur.s.nq - m * tpt : tpt;
         g.kv = cur.s.kv;
-        g.first_pos = (int64_t)cur.s.kv - cur.s.nq + (int64_t)m * tpt;
+        g.first_pos = cur.s.kv - cur.s.nq + m * tpt;
         const bool sees = cur.s.blocks(m) > 0;
         g.j0 = sees ? b : 0;
         g.j1 = sees ? b + take : 0;

@@ -408,7 +408,10 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
  * page outside the cache, lengths that are negative, decrease or exceed
  * n_tokens or max_pages * page_size) writes ATTN_CORE_ERR_DEVICE_TABLE to
  * dev_status, touches nothing outside the tensors, and leaves that sequence's
- * results undefined. */
+ * results undefined.
+ *
+ * One limit on sizes: ceil(n_tokens / floor(128 / group)) * ceil(max_pages *
+ * page_size / 128) < 2^31, group = h_q / h_kv (ATTN_CORE_ERR_UNSUPPORTED). */
 typedef struct {
     int32_t n_seq;          /* >= 1 */
     int32_t n_tokens;       /* rows of q and o; 0: nothing to do */
