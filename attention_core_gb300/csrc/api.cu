@@ -160,20 +160,35 @@ int encode_map_strided(CUtensorMap* m, const void* ptr, int d, int s, int64_t he
     return r == CUDA_SUCCESS ? ATTN_CORE_OK : ATTN_CORE_ERR_CUDA;
 }
 
-// 4-D map over [tokens][kv heads][group][d] bf16: box = one column chunk of the
-// `group` rows of one KV head of `tpt` tokens, swizzled as encode_map_strided's.
-int encode_map_rows4(CUtensorMap* m, const void* ptr, int d, int group, int kv_heads, int64_t tokens, int tpt)
+int encode_map(CUtensorMap* m, const void* ptr, int cw, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box)
 {
-    const int cw = (d % 64 == 0) ? 64 : 32;
     const CUtensorMapSwizzle sw = (cw == 64) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)kv_heads, (cuuint64_t)tokens};
-    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)group * d * 2, (cuuint64_t)kv_heads * group * d * 2};
-    cuuint32_t box[4] = {(cuuint32_t)cw, (cuuint32_t)group, 1, (cuuint32_t)tpt};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides,
+                          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_CORE_OK : ATTN_CORE_ERR_CUDA;
+}
+
+// 4-D map over packed rows [tokens][kv heads][group][d] bf16: box = cw columns of the
+// `group` rows of one KV head of `tpt` tokens.
+int encode_map_tokens(CUtensorMap* m, const void* ptr, int cw, int d, int group, int kv_heads, int64_t tokens, int tpt)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)kv_heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)group * d * 2, (cuuint64_t)kv_heads * group * d * 2};
+    const cuuint32_t box[4] = {(cuuint32_t)cw, (cuuint32_t)group, 1, (cuuint32_t)tpt};
+    return encode_map(m, ptr, cw, 4, dims, strides, box);
+}
+
+// 3-D map over pages [page and KV head][page_size][d] bf16: box = cw columns of up to
+// 128 rows of one page.
+int encode_map_pages(CUtensorMap* m, const void* ptr, int cw, int d, int page_size, int64_t pages)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)page_size * d * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)cw, (cuuint32_t)(page_size < kBlockRows ? page_size : kBlockRows), 1};
+    return encode_map(m, ptr, cw, 3, dims, strides, box);
 }
 
 // Where the query-side (Q, O, dO, dQ) and key-side (K, V, dK, dV) rows of one
@@ -1085,19 +1100,17 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
     a.timeout_ns = (uint64_t)(p->wait_timeout_ms ? p->wait_timeout_ms : 2000u) * 1000000ull;
     a.inject_timeout = (p->flags & ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
     if ((rc = device_sms(&a.num_sms))) return rc;
-    // Pages: rows of one KV head of one page, [n_pages * h_kv][page_size][d].
-    // Q: the group's heads of a run of tokens, [n_tokens][h_kv][group][d].
-    // O as Q.
-    CUtensorMap tq, tk, tv, to;
-    const int box = p->page_size < kBlockRows ? p->page_size : kBlockRows;
-    const int64_t page_rows = (int64_t)p->n_pages * p->h_kv, page_elems = (int64_t)p->page_size * p->d;
-    if ((rc = encode_map_strided(&tk, k_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
-        (rc = encode_map_strided(&tv, v_pages, p->d, p->page_size, page_rows, p->d, page_elems, box)) ||
-        (rc = encode_map_rows4(&tq, q, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)) ||
-        (rc = encode_map_rows4(&to, o, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)))
-        return rc;
-    return ac::launch_paged(tq, tk, tv, to, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA
-                                                                                  : ATTN_CORE_OK;
+    ac::PagedMaps m;
+    for (int i = 0; i < (p->d % 64 ? 2 : 1); ++i) {
+        const int cw = i ? 32 : 64;
+        const int64_t pages = (int64_t)p->n_pages * p->h_kv;
+        if ((rc = encode_map_tokens(&m.q[i], q, cw, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)) ||
+            (rc = encode_map_pages(&m.k[i], k_pages, cw, p->d, p->page_size, pages)) ||
+            (rc = encode_map_pages(&m.v[i], v_pages, cw, p->d, p->page_size, pages)))
+            return rc;
+    }
+    if ((rc = encode_map_tokens(&m.o, o, p->d % 64 ? 32 : 64, p->d, a.group, p->h_kv, p->n_tokens, a.tpt))) return rc;
+    return ac::launch_paged(m, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
 }
 
 int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,

@@ -287,8 +287,12 @@ struct PagedArgs {
 };
 size_t paged_ws_bytes(int d);
 int paged_tokens_per_tile(int group);
-int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                 const PagedArgs& a, cudaStream_t stream);
+// Tensor maps: [0] column chunks of 64 with the 128-byte swizzle, [1] of 32 with
+// the 64-byte swizzle (d % 64 != 0 only); O as the core's maps.
+struct PagedMaps {
+    CUtensorMap q[2], k[2], v[2], o;
+};
+int launch_paged(const PagedMaps& maps, const PagedArgs& a, cudaStream_t stream);
 
 // Page copies (pages.cu): `pairs` is a host array.
 int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,

@@ -48,10 +48,44 @@ namespace {
 
 constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
 
+// Layout of a [128 x D] tile of Q, K or V: column chunks of 64 with the 128-byte
+// swizzle, then, for D = 96 and 160, one of 32 with the 64-byte swizzle.  (Chunks
+// of 32 throughout, as the core's tiles have, cost 5 TMA boxes a page instead of
+// 3 at D = 160, and small boxes bound the loads: about 40 cycles each.)
+template <int D>
+struct PagedGeom {
+    static constexpr int WIDE = D / 64;                       // chunks of 64 columns
+    static constexpr bool NARROW = D % 64 != 0;               // and one of 32
+    static constexpr int CHUNKS = WIDE + (NARROW ? 1 : 0);
+    static constexpr uint32_t TILE = 128u * D * 2;
+    static constexpr uint32_t WIDE_BYTES = 128 * 128, OFF_NARROW = WIDE * WIDE_BYTES;
+    static_assert(D % 32 == 0 && (!NARROW || D % 64 == 32), "head dimension");
+    __host__ __device__ static constexpr bool narrow(int ch) { return ch >= WIDE; }
+    __host__ __device__ static constexpr uint32_t offset(int ch) { return (uint32_t)ch * WIDE_BYTES; }
+    __host__ __device__ static constexpr uint32_t row_bytes(int ch) { return narrow(ch) ? 64 : 128; }
+    // K-major operand: the 16-wide slice kk of the head dimension
+    __device__ static __forceinline__ uint64_t desc_k(uint32_t base, int kk)
+    {
+        if (kk < 4 * WIDE)
+            return desc_plus(smem_desc(base, 16, 1024, 2u), ((kk / 4) * WIDE_BYTES + (kk % 4) * 32) >> 4);
+        return desc_plus(smem_desc(base + OFF_NARROW, 16, 512, 4u), ((kk - 4 * WIDE) * 32) >> 4);
+    }
+    // MN-major operand: rows [16 kk, 16 kk + 16) as the reduction slice, the wide
+    // columns (or the narrow chunk's) as N
+    __device__ static __forceinline__ uint64_t desc_wide(uint32_t base, int kk)
+    {
+        return desc_plus(smem_desc(base, WIDE_BYTES, 1024, 2u), (uint32_t)(kk * 16 * 128) >> 4);
+    }
+    __device__ static __forceinline__ uint64_t desc_narrow(uint32_t base, int kk)
+    {
+        return desc_plus(smem_desc(base + OFF_NARROW, 128 * 64, 512, 4u), (uint32_t)(kk * 16 * 64) >> 4);
+    }
+};
+
 template <int D>
 struct PagedCfg {
-    using G = TileGeom<D>;
-    static constexpr uint32_t TILE = G::template tile_bytes<128>();
+    using G = TileGeom<D>;                                    // the O stage
+    static constexpr uint32_t TILE = PagedGeom<D>::TILE;
     static constexpr uint32_t CHUNK = G::template chunk_bytes<128>();
     // One Q buffer (the next tile's Q loads behind this tile's last softmax and
     // epilogue), K and V rings, and for d <= 128 a stage through which a full
@@ -218,10 +252,10 @@ __device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, 
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PagedArgs a)
+paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 {
     using G = TileGeom<D>;
+    using P = PagedGeom<D>;
     using C = PagedCfg<D>;
     const PagedTables& t = a.t;
 
@@ -246,9 +280,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
+        for (int i = 0; i < (P::NARROW ? 2 : 1); ++i) {
+            tma_prefetch_desc(&maps.q[i]);
+            tma_prefetch_desc(&maps.k[i]);
+            tma_prefetch_desc(&maps.v[i]);
+        }
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
@@ -349,12 +385,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 ok = wait_w(wc, bar(bars->q_empty[qs]), qr.phase ^ 1, timeout_code(kSiteQEmpty));
                 if (!ok) break;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * G::ROWB * G::NCH);
+                    mbar_arrive_expect_tx(bar(bars->q_full[qs]), (uint32_t)(a.tpt * group) * (D * 2));
                 __syncwarp();
 #pragma unroll
-                for (int ch = 0; ch < G::NCH; ++ch)
-                    tma_load_4d_warp(sb + C::OFF_Q + qs * C::TILE + ch * C::CHUNK, &tm_q, ch * G::CW, 0, g.head, g.q_tok,
-                                     bar(bars->q_full[qs]));
+                for (int ch = 0; ch < P::CHUNKS; ++ch)
+                    tma_load_4d_warp(sb + C::OFF_Q + qs * C::TILE + P::offset(ch), &maps.q[P::narrow(ch)], ch * 64, 0,
+                                     g.head, g.q_tok, bar(bars->q_full[qs]));
                 qr.advance();
             }
             const int32_t* entries = t.page_table + (int64_t)g.seq * t.max_pages;
@@ -380,7 +416,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 const bool tail = is_v && rows < 128;
                 const uint32_t land = bar(tail ? bars->v_tail : full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages << rows_shift) * G::ROWB * G::NCH);
+                if (lane == 0) mbar_arrive_expect_tx(land, (uint32_t)(pages << rows_shift) * (D * 2));
                 __syncwarp();
 #pragma unroll 2
                 for (int p = 0; p < pages; ++p) {
@@ -392,21 +428,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         __syncwarp();
                     }
                     const int row = (j * 128 + (p << rows_shift)) & (t.page_size - 1);
-                    const uint32_t dst = ring + st * C::TILE + (uint32_t)(p << rows_shift) * G::ROWB;
+                    const uint32_t dst = ring + st * C::TILE;
 #pragma unroll
-                    for (int ch = 0; ch < G::NCH; ++ch)
-                        tma_load_3d_warp(dst + ch * C::CHUNK, tm, ch * G::CW, row, z, land);
+                    for (int ch = 0; ch < P::CHUNKS; ++ch)
+                        tma_load_3d_warp(dst + P::offset(ch) + (uint32_t)(p << rows_shift) * P::row_bytes(ch),
+                                         &tm[P::narrow(ch)], ch * 64, row, z, land);
                 }
                 if (tail) {
                     ok = wait_w(wc, land, tails & 1, timeout_code(kSiteVTail));
                     if (!ok) break;
                     ++tails;
                     // rows [rows, 128) of every chunk are contiguous
-                    const uint32_t n16 = (uint32_t)(128 - rows) * (G::ROWB / 16);
-                    for (int ch = 0; ch < G::NCH; ++ch)
-                        for (uint32_t i = lane; i < n16; i += 32)
-                            st_shared_v4(ring + st * C::TILE + ch * C::CHUNK + (uint32_t)rows * G::ROWB + i * 16, 0u, 0u,
-                                         0u, 0u);
+                    for (int ch = 0; ch < P::CHUNKS; ++ch) {
+                        const uint32_t n16 = (uint32_t)(128 - rows) * (P::row_bytes(ch) / 16);
+                        const uint32_t first = ring + st * C::TILE + P::offset(ch) + (uint32_t)rows * P::row_bytes(ch);
+                        for (uint32_t i = lane; i < n16; i += 32) st_shared_v4(first + i * 16, 0u, 0u, 0u, 0u);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(full[st]));
@@ -415,9 +452,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
     };
     if (alive && warp == 0) {
-        produce(std::false_type{}, &tm_k, bars->k_full, bars->s_full, sb + C::OFF_K);
+        produce(std::false_type{}, maps.k, bars->k_full, bars->s_full, sb + C::OFF_K);
     } else if (alive && warp == 2) {
-        produce(std::true_type{}, &tm_v, bars->v_full, bars->pv_done, sb + C::OFF_V);
+        produce(std::true_type{}, maps.v, bars->v_full, bars->pv_done, sb + C::OFF_V);
     } else if (alive && warp == 1) {
         // ---- S = Q K^T of every block (the whole warp issues, see mma_ss).  A score
         // buffer holds S, then P, until its P.V has read it; the tensor pipe takes
@@ -442,8 +479,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const uint32_t tS = tmem + (bs.slot ? C::T_S1 : C::T_S0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tS, G::template desc_k<128>(qbase, kk), G::template desc_k<128>(kbase, kk), IDS,
-                           kk > 0 ? 1u : 0u);
+                    mma_ss(tS, P::desc_k(qbase, kk), P::desc_k(kbase, kk), IDS, kk > 0 ? 1u : 0u);
                 mma_commit(bar(bars->s_full[rs.slot]));
                 if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qr.slot]));
                 rs.advance();
@@ -458,7 +494,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // ---- O += P V of every block, from a warp (and SM sub-partition) of its own: one
         // warp issuing both products was what bounded compute-heavy batches (1870
         // cycles a block at d = 128 where the products take 1040).
-        constexpr uint32_t IDO = idesc_bf16(128, D, false, true);
+        constexpr uint32_t IDO = idesc_bf16(128, P::WIDE * 64, false, true);
+        constexpr uint32_t IDN = idesc_bf16(128, 32, false, true);
         Ring<C::SV> rv;
         Ring<2> bv;
         uint32_t o_phase = 1;       // o_free: the first tile finds O free
@@ -482,8 +519,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     for (int i = 0; i < 4; ++i) {
                         const int kk = 4 * (i / 2) + 2 * part + (i & 1);
                         const bool fresh = C::SPLIT ? (kk & 3) == 0 : kk == 0;     // the accumulator's first slice
-                        mma_ts(tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O), tP + split_a_col(kk, 128),
-                               G::template desc_mn<128>(vbase, kk), IDO, fresh ? more : 1u);
+                        const uint32_t tO = tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O);
+                        const uint32_t tA = tP + split_a_col(kk, 128);
+                        mma_ts(tO, tA, P::desc_wide(vbase, kk), IDO, fresh ? more : 1u);
+                        if constexpr (P::NARROW)
+                            mma_ts(tO + P::WIDE * 64, tA, P::desc_narrow(vbase, kk), IDN, fresh ? more : 1u);
                     }
                 }
                 if (!ok) break;
@@ -757,7 +797,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     if (!ok) break;
                     if (lane == 0) {
                         for (int ch = 0; ch < G::NCH; ++ch)
-                            tma_store_4d(&tm_o, sb + C::OFF_OST + ch * C::CHUNK, ch * G::CW, 0, g.head, g.q_tok);
+                            tma_store_4d(&maps.o, sb + C::OFF_OST + ch * C::CHUNK, ch * G::CW, 0, g.head, g.q_tok);
                         bulk_commit();
                     }
                     __syncwarp();
@@ -850,8 +890,7 @@ int paged_tokens_per_tile(int group) { return 128 / group; }
 namespace {
 
 template <int D>
-int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, const PagedArgs& a,
-                   cudaStream_t st)
+int launch_paged_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t st)
 {
     constexpr uint32_t smem = PagedCfg<D>::SMEM;
     auto kern = paged_attn_kernel<D>;
@@ -864,7 +903,7 @@ int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     const int64_t want = (tiles * a.t.h_kv * blocks + kMinUnits - 1) / kMinUnits;
     int grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
     if (want < grid) grid = (int)want;
-    kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, to, a);
+    kern<<<grid, kThreads, smem, st>>>(m, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
     if (grid > 1 && blocks > kSnap) {
         const int64_t rows = (int64_t)a.tpt * a.group < (int64_t)a.t.n_tokens * a.group ? (int64_t)a.tpt * a.group
@@ -885,14 +924,13 @@ int launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 
 }  // namespace
 
-int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, const PagedArgs& a,
-                 cudaStream_t st)
+int launch_paged(const PagedMaps& m, const PagedArgs& a, cudaStream_t st)
 {
     switch (a.d) {
-        case 64: return launch_paged_t<64>(tq, tk, tv, to, a, st);
-        case 96: return launch_paged_t<96>(tq, tk, tv, to, a, st);
-        case 128: return launch_paged_t<128>(tq, tk, tv, to, a, st);
-        case 160: return launch_paged_t<160>(tq, tk, tv, to, a, st);
+        case 64: return launch_paged_t<64>(m, a, st);
+        case 96: return launch_paged_t<96>(m, a, st);
+        case 128: return launch_paged_t<128>(m, a, st);
+        case 160: return launch_paged_t<160>(m, a, st);
         default: return (int)cudaErrorInvalidValue;
     }
 }
