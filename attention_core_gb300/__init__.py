@@ -163,6 +163,9 @@ class DalParams:
 
 
 _lib = None
+# The short calls' entry points once more, with plain addresses and integers for
+# arguments: converting structures costs a few microseconds of the host's time.
+_FAST: dict = {}
 
 
 def load_library(path: str = LIB_PATH):
@@ -224,6 +227,13 @@ def load_library(path: str = LIB_PATH):
     lib.attn_core_page_copy.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp,
                                         ctypes.c_int64, vp]
     lib.attn_core_page_copy.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    for name, argtypes in (("attn_core_rope_fwd", [vp] * 7), ("attn_core_rope_bwd", [vp] * 7),
+                           ("attn_core_paged_append", [vp] * 10), ("attn_core_paged_fwd", [vp] * 7 + [ctypes.c_size_t, vp]),
+                           ("attn_core_page_copy", [vp, i64, i64, i64, i64, vp, i64, vp])):
+        f = lib[name]
+        f.argtypes, f.restype = argtypes, ctypes.c_int
+        _FAST[name] = f
     _lib = lib
     return lib
 
@@ -627,8 +637,11 @@ def _device() -> int:
 def _need(t, name, dtype, shape, device: int) -> None:
     """A contiguous tensor of this type and shape on the current device, where
     the library launches; _check says what else it is."""
-    if not (t.__class__.__name__ == "Tensor" and t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
+    try:
+        good = t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
         _check(t, name, dtype, shape)
         _on_device(device, t)
 
@@ -688,13 +701,17 @@ def _rope_params(q, k, out_q, out_k, d):
     return p
 
 
-def _rope(call, what, q, k, table, positions, pos0, out_q, out_k):
+def _rope(what, q, k, table, positions, pos0, out_q, out_k):
     import torch
     dev = _device()
-    _on_device(dev, q, k, out_q, out_k, positions)
-    key = (table.d, *[None if x is None else (x.shape, x.stride(), x.dtype) for x in (q, k, out_q, out_k)])
+    key = (table.d,
+           None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()),
+           None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
+           None if out_q is None else (out_q.shape, out_q.stride(), out_q.dtype, out_q.get_device()),
+           None if out_k is None else (out_k.shape, out_k.stride(), out_k.dtype, out_k.get_device()), dev)
     known = _ROPE_PARAMS.get(key)
     if known is None:
+        _on_device(dev, q, k, out_q, out_k)
         known = _rope_params(q, k, out_q, out_k, table.d)
         if len(_ROPE_PARAMS) >= 256:
             _ROPE_PARAMS.clear()
@@ -705,20 +722,27 @@ def _rope(call, what, q, k, table, positions, pos0, out_q, out_k):
     else:
         if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.numel() != p.b * p.s:
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor of {p.b * p.s} values")
+        if positions.get_device() != dev:
+            _on_device(dev, positions)
         p.positions = positions.data_ptr()
     xq = xk = yq = yk = 0
     if q is not None:
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out_q = _contiguous_like(q)
         xq, yq = q.data_ptr(), out_q.data_ptr()
     if k is not None:
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            out_k = _contiguous_like(k)
         xk, yk = k.data_ptr(), out_k.data_ptr()
-    rc = call(p, table, xq, xk, yq, yk, _raw_stream(dev)) if p.s else OK
+    rc = _FAST[what](ctypes.addressof(p), ctypes.addressof(table), xq, xk, yq, yk, _raw_stream(dev)) if p.s else OK
     if rc != OK:
         raise AttnCoreError(rc, what)
     return out_q, out_k
+
+
+def _contiguous_like(x):
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def rope_fwd(q, k, table: RopeTable, *, positions=None, pos0: int = 0, out_q=None, out_k=None):
@@ -726,12 +750,12 @@ def rope_fwd(q, k, table: RopeTable, *, positions=None, pos0: int = 0, out_q=Non
     packed [tokens, h, d] of any strides with d contiguous.  ``positions``:
     int32, one per (batch element, token); by default pos0 + token.  ``out_q`` /
     ``out_k`` may be the inputs themselves.  Returns (q, k) rotated."""
-    return _rope(attn_core_rope_fwd, "attn_core_rope_fwd", q, k, table, positions, pos0, out_q, out_k)
+    return _rope("attn_core_rope_fwd", q, k, table, positions, pos0, out_q, out_k)
 
 
 def rope_bwd(dq, dk, table: RopeTable, *, positions=None, pos0: int = 0, out_q=None, out_k=None):
     """Gradients of rope_fwd's inputs from those of its outputs."""
-    return _rope(attn_core_rope_bwd, "attn_core_rope_bwd", dq, dk, table, positions, pos0, out_q, out_k)
+    return _rope("attn_core_rope_bwd", dq, dk, table, positions, pos0, out_q, out_k)
 
 
 class PagedBatch:
@@ -767,6 +791,8 @@ class PagedBatch:
             workspace = torch.empty(need, dtype=torch.uint8, device=cu_seqlens_q.device)
         self.workspace = workspace
         self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self._address = ctypes.addressof(self.params)
+        self._strides = {}      # by paged_append's layouts: three token strides
         self._q_shape = torch.Size((int(n_tokens), int(h_q), int(d)))
         self._kv_shape = torch.Size((int(n_tokens), int(h_kv), int(d)))
         self._page_shape = torch.Size((int(n_pages), int(h_kv), int(page_size), int(d)))
@@ -791,22 +817,34 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     [n_tokens, h_q, d] (or None).  Returns q's rotation, packed."""
     import torch
     dev, bf16 = _device(), torch.bfloat16
-    strides = [0, _token_stride(k, "k", batch._kv_shape), _token_stride(v, "v", batch._kv_shape)]
+    # what a layout needs follows from shapes, strides and types alone
+    key = (None if q is None else (q.shape, q.stride(), q.dtype), k.shape, k.stride(), k.dtype, v.shape, v.stride(),
+           v.dtype)
+    strides = batch._strides.get(key)
+    if strides is None:
+        three = (0 if q is None else _token_stride(q, "q", batch._q_shape), _token_stride(k, "k", batch._kv_shape),
+                 _token_stride(v, "v", batch._kv_shape))
+        if len(batch._strides) >= 64:
+            batch._strides.clear()
+        batch._strides[key] = strides = (ctypes.c_int64 * 3)(*three)
     _need(k_pages, "k_pages", bf16, batch._page_shape, dev)
     _need(v_pages, "v_pages", bf16, batch._page_shape, dev)
+    xq = yq = 0
     if q is not None:
-        strides[0] = _token_stride(q, "q", batch._q_shape)
         if out_q is None:
             out_q = torch.empty(batch._q_shape, dtype=bf16, device=q.device)
         else:
             _need(out_q, "out_q", bf16, batch._q_shape, dev)
+        xq, yq = q.data_ptr(), out_q.data_ptr()
     elif out_q is not None:
         raise ValueError("out_q without q")
-    _on_device(dev, q, k, v, batch.workspace)
+    if k.get_device() != dev or v.get_device() != dev or (q is not None and q.get_device() != dev) \
+            or batch.workspace.get_device() != dev:
+        _on_device(dev, q, k, v, batch.workspace)
     if batch.params.n_tokens:
-        rc = attn_core_paged_append(batch.params, table, q.data_ptr() if q is not None else 0, k.data_ptr(),
-                                    v.data_ptr(), strides, out_q.data_ptr() if q is not None else 0,
-                                    k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev))
+        rc = _FAST["attn_core_paged_append"](batch._address, 0 if table is None else ctypes.addressof(table), xq,
+                                             k.data_ptr(), v.data_ptr(), ctypes.addressof(strides), yq,
+                                             k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_append")
     return out_q
@@ -829,10 +867,12 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
         lse = torch.empty(batch._lse_shape, dtype=torch.float32, device=q.device)
     else:
         _need(lse, "lse", torch.float32, batch._lse_shape, dev)
-    _on_device(dev, batch.workspace)
+    if batch.workspace.get_device() != dev:
+        _on_device(dev, batch.workspace)
     if batch.params.n_tokens:
-        rc = attn_core_paged_fwd(batch.params, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), *batch._ws, _raw_stream(dev))
+        ws, ws_bytes = batch._ws
+        rc = _FAST["attn_core_paged_fwd"](batch._address, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_fwd")
     return out, lse
@@ -872,7 +912,8 @@ def page_copy(pages, pairs) -> None:
             raise ValueError("no pages to copy")
         return
     page_bytes = shape[-3] * shape[-2] * shape[-1] * pages.element_size()
-    rc = attn_core_page_copy(pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes, arr.ctypes.data,
-                             len(arr) if arr.size else 0, _raw_stream(dev))
+    load_library()
+    rc = _FAST["attn_core_page_copy"](pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes,
+                                      arr.ctypes.data, len(arr) if arr.size else 0, _raw_stream(dev))
     if rc != OK:
         raise AttnCoreError(rc, "attn_core_page_copy")
