@@ -242,7 +242,7 @@ struct RopeArgs {
     int32_t pos0;
     const int32_t* positions;   // [b, s], or null
     float sign;                 // 1 forward, -1 backward
-    int32_t tile;               // tokens per block (set by the launcher)
+    int32_t tile, heads;        // tokens and heads per block (set by the launcher)
 };
 int launch_rope(const RopeTable& t, RopeArgs& a, int b, int sms, cudaStream_t stream);
 
@@ -268,7 +268,7 @@ struct AppendArgs {
     uint16_t* q_out;
     uint16_t* k_pages;
     uint16_t* v_pages;
-    int32_t tile;               // tokens per block (set by the launcher)
+    int32_t tile, heads;        // tokens and heads per block (set by the launcher)
 };
 int launch_append(const RopeTable& t, AppendArgs& a, int sms, cudaStream_t stream);
 

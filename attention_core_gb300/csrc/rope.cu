@@ -19,7 +19,8 @@ namespace ac {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kAhead = 2;   // heads whose loads a thread has in flight
 
 __device__ __forceinline__ uint32_t rot_pair16(uint32_t xa, uint32_t xb, float c0, float s0, float c1, float s1,
                                                uint32_t& yb)
@@ -40,12 +41,15 @@ struct Unit {
     float c[PAIRS], s[PAIRS];
     int u, n_pair_units, half, rot;
 
-    __device__ __forceinline__ void init(const RopeTable& t, int unit, int64_t pos, float sign)
+    __device__ __forceinline__ void place(const RopeTable& t, int unit)
     {
         u = unit;
         rot = t.rot;
         half = t.rot / 2;
         n_pair_units = half / PAIRS;
+    }
+    __device__ __forceinline__ void turn(const RopeTable& t, int64_t pos, float sign)
+    {
         if (u >= n_pair_units) return;
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) {
@@ -132,8 +136,9 @@ __host__ __device__ inline int units_of(int mode, int d, int rot)
 
 }  // namespace
 
-// One block: `tile` tokens of one batch element, all heads.  Thread: one unit of
-// one token, heads `lane`, lane + n_lanes, ...
+// One block: `tile` tokens of one batch element and, of the list of all heads (Q's,
+// then K's), the blockIdx.y-th `heads` of them.  Thread: one unit of one token,
+// heads `lane`, lane + lanes, ... of those.
 template <int MODE>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable t, const RopeArgs a)
 {
@@ -147,24 +152,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     if (lane >= lanes || tok >= a.s) return;
     const int64_t pos = a.positions ? a.positions[(int64_t)batch * a.s + tok] : (int64_t)a.pos0 + tok;
     Unit<MODE> un;
-    un.init(t, slot % units, pos, a.sign);
-    auto walk = [&](const uint16_t* x, const int64_t (&xs)[3], uint16_t* y, const int64_t (&ys)[3], int heads,
-                    int first) {
-        const uint16_t* xr = x + batch * xs[0] + tok * xs[2];
-        uint16_t* yr = y + batch * ys[0] + tok * ys[2];
-        for (int h = first; h < heads; h += 2 * lanes) {
-            const bool two = h + lanes < heads;
-            const auto d0 = un.load(xr + h * xs[1]);
-            const auto d1 = two ? un.load(xr + (h + lanes) * xs[1]) : d0;
-            un.store(yr + h * ys[1], d0);
-            if (two) un.store(yr + (h + lanes) * ys[1], d1);
-        }
+    un.place(t, slot % units);
+    // Heads of Q, then of K, as one list.  The first ones' loads go out before the
+    // angles are formed.
+    const uint16_t* xq = a.q + batch * a.q_stride[0] + tok * a.q_stride[2];
+    const uint16_t* xk = a.k + batch * a.k_stride[0] + tok * a.k_stride[2];
+    uint16_t* yq = a.yq + batch * a.yq_stride[0] + tok * a.yq_stride[2];
+    uint16_t* yk = a.yk + batch * a.yk_stride[0] + tok * a.yk_stride[2];
+    const int h0 = (int)blockIdx.y * a.heads + lane;
+    const int h1 = min(((int)blockIdx.y + 1) * a.heads, a.h_q + a.h_kv);
+    auto load = [&](int h) {
+        return un.load(h < a.h_q ? xq + h * a.q_stride[1] : xk + (h - a.h_q) * a.k_stride[1]);
     };
-    walk(a.q, a.q_stride, a.yq, a.yq_stride, a.h_q, lane);
-    walk(a.k, a.k_stride, a.yk, a.yk_stride, a.h_kv, lane);
+    auto store = [&](int h, const typename Unit<MODE>::Data& d) {
+        un.store(h < a.h_q ? yq + h * a.yq_stride[1] : yk + (h - a.h_q) * a.yk_stride[1], d);
+    };
+    typename Unit<MODE>::Data d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * lanes < h1) d[i] = load(h0 + i * lanes);
+    un.turn(t, pos, a.sign);
+    for (int h = h0; h < h1; h += kAhead * lanes) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (h + i * lanes < h1) store(h + i * lanes, d[i]);
+            const int next = h + (kAhead + i) * lanes;
+            if (next < h1) d[i] = load(next);
+        }
+    }
 }
 
-// One block: `tile` new tokens, all heads of Q, K and V.
+// One block: `tile` new tokens and a part of the heads, as rope_kernel's.
 template <int MODE>
 __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_constant__ RopeTable t, const AppendArgs a)
 {
@@ -196,27 +214,41 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     const bool placed = page >= 0 && page < pt.n_pages;
     if (!placed && pt.status) atomicCAS(pt.status, 0, kStatusTable);
     Unit<MODE> un;
-    un.init(t, slot % units, pos, 1.0f);
-    const int d = t.d;
-    if (a.q) {
-        const uint16_t* x = a.q + tok * a.q_stride;
-        uint16_t* y = a.q_out + (int64_t)tok * pt.h_q * d;
-        for (int h = lane; h < pt.h_q; h += 2 * lanes) {
-            const bool two = h + lanes < pt.h_q;
-            const auto d0 = un.load(x + h * d);
-            const auto d1 = two ? un.load(x + (h + lanes) * d) : d0;
-            un.store(y + h * d, d0);
-            if (two) un.store(y + (h + lanes) * d, d1);
-        }
-    }
-    if (!placed) return;
+    un.place(t, slot % units);
+    // Heads of Q (where wanted), then of K, then of V, as one list; K's and V's go to
+    // the page, if there is one for this token.
+    const int d = t.d, h_q = a.q ? pt.h_q : 0;
     const int64_t row0 = ((int64_t)page * pt.h_kv * pt.page_size + (pos & (pt.page_size - 1))) * d;
     const int64_t head = (int64_t)pt.page_size * d;
-    for (int h = lane; h < pt.h_kv; h += lanes) {
-        const auto dk = un.load(a.k + tok * a.k_stride + h * d);
-        const auto dv = un.load(a.v + tok * a.v_stride + h * d);
-        un.store(a.k_pages + row0 + h * head, dk);
-        un.store_raw(a.v_pages + row0 + h * head, dv);
+    const int h0 = (int)blockIdx.y * a.heads + lane;
+    const int all = h_q + (placed ? 2 * pt.h_kv : 0);
+    const int h1 = min(((int)blockIdx.y + 1) * a.heads, all);
+    auto load = [&](int h) {
+        if (h < h_q) return un.load(a.q + tok * a.q_stride + h * d);
+        h -= h_q;
+        return un.load(h < pt.h_kv ? a.k + tok * a.k_stride + h * d : a.v + tok * a.v_stride + (h - pt.h_kv) * d);
+    };
+    auto store = [&](int h, const typename Unit<MODE>::Data& x) {
+        if (h < h_q) {
+            un.store(a.q_out + ((int64_t)tok * pt.h_q + h) * d, x);
+        } else if (h - h_q < pt.h_kv) {
+            un.store(a.k_pages + row0 + (h - h_q) * head, x);
+        } else {
+            un.store_raw(a.v_pages + row0 + (h - h_q - pt.h_kv) * head, x);
+        }
+    };
+    typename Unit<MODE>::Data x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * lanes < h1) x[i] = load(h0 + i * lanes);
+    un.turn(t, pos, 1.0f);
+    for (int h = h0; h < h1; h += kAhead * lanes) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (h + i * lanes < h1) store(h + i * lanes, x[i]);
+            const int next = h + (kAhead + i) * lanes;
+            if (next < h1) x[i] = load(next);
+        }
     }
 }
 
@@ -224,14 +256,25 @@ namespace {
 
 int mode_of(const RopeTable& t) { return t.interleaved ? 2 : (t.rot % 16 == 0 ? 0 : 1); }
 
-// Tokens per block: as many as fit the block's threads (fewer evaluations of each
-// angle), but no more than leaves four blocks for every SM, so that short calls
-// spread over the whole chip.
-int tile_of(int units, int64_t tokens, int sms)
+// Tokens per block: as many as fit its threads, so that each angle is formed once
+// per block and a head's rows are read in long runs; the heads are then shared out
+// over as many blocks as give every SM kBlocksPerSm.
+constexpr int kBlocksPerSm = 24;
+struct Split {
+    int tile, heads;
+    dim3 grid;
+};
+Split split(int units, int batches, int tokens, int heads, int sms)
 {
-    int tile = 1;
-    while (2 * tile * units <= kRopeThreads && tokens / (2 * tile) >= 4ll * sms) tile *= 2;
-    return tile;
+    Split s;
+    s.tile = 1;
+    while (2 * s.tile * units <= kRopeThreads && s.tile < tokens) s.tile *= 2;
+    const int64_t x = (int64_t)batches * ((tokens + s.tile - 1) / s.tile);
+    int64_t groups = ((int64_t)kBlocksPerSm * sms + x - 1) / x;
+    groups = groups < heads ? groups : heads;
+    s.heads = (int)((heads + groups - 1) / groups);
+    s.grid = dim3((unsigned)x, (unsigned)((heads + s.heads - 1) / s.heads));
+    return s;
 }
 
 }  // namespace
@@ -239,8 +282,10 @@ int tile_of(int units, int64_t tokens, int sms)
 int launch_rope(const RopeTable& t, RopeArgs& a, int b, int sms, cudaStream_t st)
 {
     const int mode = mode_of(t);
-    a.tile = tile_of(units_of(mode, t.d, t.rot), (int64_t)b * a.s, sms);
-    const unsigned grid = (unsigned)b * (unsigned)((a.s + a.tile - 1) / a.tile);
+    const Split sp = split(units_of(mode, t.d, t.rot), b, a.s, a.h_q + a.h_kv, sms);
+    a.tile = sp.tile;
+    a.heads = sp.heads;
+    const dim3 grid = sp.grid;
     if (mode == 0)
         rope_kernel<0><<<grid, kRopeThreads, 0, st>>>(t, a);
     else if (mode == 1)
@@ -253,8 +298,10 @@ int launch_rope(const RopeTable& t, RopeArgs& a, int b, int sms, cudaStream_t st
 int launch_append(const RopeTable& t, AppendArgs& a, int sms, cudaStream_t st)
 {
     const int mode = mode_of(t);
-    a.tile = tile_of(units_of(mode, t.d, t.rot), a.t.n_tokens, sms);
-    const unsigned grid = (unsigned)((a.t.n_tokens + a.tile - 1) / a.tile);
+    const Split sp = split(units_of(mode, t.d, t.rot), 1, a.t.n_tokens, (a.q ? a.t.h_q : 0) + 2 * a.t.h_kv, sms);
+    a.tile = sp.tile;
+    a.heads = sp.heads;
+    const dim3 grid = sp.grid;
     if (mode == 0)
         append_kernel<0><<<grid, kRopeThreads, 0, st>>>(t, a);
     else if (mode == 1)
