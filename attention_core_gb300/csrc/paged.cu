@@ -823,60 +823,71 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 }
 
 // Joins the parts of the tiles that were cut: block (c, y) takes rows 4y .. 4y + 3 of
-// the tile that CTA c cut at its end, a warp per row.  Lanes over the parts form the
-// weights, lanes over d (16 bytes each) the sums; up to eight parts' loads are in
-// flight.  Launched while the attention kernel still runs, it waits for its end.
+// the tile that CTA c cut at its end, a warp per row.  Up to 32 parts at a time: lane
+// p forms part p's weight, then lanes over d sum the parts' rows, eight in flight and
+// the first eight on their way while the weights are formed (a chain of loads is all
+// that this kernel's time consists of).  Launched programmatically, it waits for the
+// attention kernel's end.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedTables& t = a.t;
     const CutTile cut = reinterpret_cast<const CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = (int)blockIdx.y * 4 + warp;
+    const int lane = threadIdx.x & 31;
+    const int r = (int)blockIdx.y * 4 + (int)(threadIdx.x >> 5);
     if (cut.last_cta == 0 || r >= cut.n_rows) return;
-    __shared__ float weight[4][kPagedMaxCtas];
     const int parts = cut.last_cta - (int)blockIdx.x + 1;
     const float* lse = reinterpret_cast<const float*>(a.ws + ws_lse_offset(D));
-    const float* rows = reinterpret_cast<const float*>(a.ws);
+    const float* rows = reinterpret_cast<const float*>(a.ws) + lane;
     auto row_of = [&](int p) { return part_row((int)blockIdx.x + p, p == 0 ? 1 : 0) + r; };
-    float mx = -INFINITY;
-    for (int p = lane; p < parts; p += 32) {
-        const float x = lse[row_of(p)];
-        weight[warp][p] = x;
-        mx = fmaxf(mx, x);
-    }
+    constexpr int E = D / 32, AHEAD = 8;
+    float x[AHEAD][E];
+    auto load = [&](int p0) {
 #pragma unroll
-    for (int o = 16; o; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float m_ref = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-        const float w = exp2f(weight[warp][p] - m_ref);
-        weight[warp][p] = w;
-        sum += w;
-    }
+        for (int k = 0; k < AHEAD; ++k)
+            if (p0 + k < parts) {
 #pragma unroll
-    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
+                for (int e = 0; e < E; ++e) x[k][e] = rows[row_of(p0 + k) * D + e * 32];
+            }
+    };
+    float m = -INFINITY, sum = 0.f, acc[E] = {};
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+        const float z = p0 + lane < parts ? lse[row_of(p0 + lane)] : -INFINITY;
+        load(p0);
+        float top = z;
+#pragma unroll
+        for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m_new = fmaxf(m, top);
+        const float m_ref = m_new == -INFINITY ? 0.f : m_new;
+        const float f = exp2f(m - m_ref);                     // 0 the first time
+        const float w = exp2f(z - m_ref);
+        m = m_new;
+        float ws = w;
+#pragma unroll
+        for (int o = 16; o; o /= 2) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+        sum = sum * f + ws;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+        for (int p = p0; p < parts && p < p0 + 32; p += AHEAD) {
+            if (p > p0) load(p);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, (p - p0 + k) & 31);
+                if (p + k < parts) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += wk * x[k][e];
+                }
+            }
+        }
+    }
     const float inv = sum > 0.f ? 1.0f / sum : 0.f;
     const int tok = cut.q_tok + r / a.group, head = cut.head * a.group + r % a.group;
-    uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D;
-    for (int c = lane * 4; c < D; c += 128) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int p = 0; p < parts; ++p) {
-            const float w = weight[warp][p];
-            const float4 x = *reinterpret_cast<const float4*>(rows + row_of(p) * D + c);
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
-        }
-        *reinterpret_cast<uint2*>(orow + c) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    }
+    uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D + lane;
+#pragma unroll
+    for (int e = 0; e < E; ++e) orow[e * 32] = (uint16_t)(pack_bf16x2(acc[e] * inv, 0.f) & 0xffffu);
     if (lane == 0)
-        a.lse[(size_t)head * t.n_tokens + tok] = sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+        a.lse[(size_t)head * t.n_tokens + tok] = sum > 0.f ? (m + log2f(sum)) * 0.693147180559945309f : -INFINITY;
 }
 
 size_t paged_ws_bytes(int d)
