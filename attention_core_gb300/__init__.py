@@ -789,6 +789,11 @@ class PagedBatch:
                                 else ERR_INVALID_ARG, "PagedBatch")
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=cu_seqlens_q.device)
+        elif workspace.get_device() != cu_seqlens_q.get_device():
+            raise ValueError(f"workspace must be on {cu_seqlens_q.device}, got {workspace.device}")
+        for name, t in (("kv_lens", kv_lens), ("page_table", page_table)):
+            if t.device != cu_seqlens_q.device:
+                raise ValueError(f"{name} must be on {cu_seqlens_q.device}, got {t.device}")
         self.workspace = workspace
         self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
         self._address = ctypes.addressof(self.params)

@@ -831,6 +831,8 @@ int rope_call(const attn_core_rope_params* p, const attn_core_rope_table* t, con
     if (p->h_kv && ((rc = check_rope_strides(p->k_stride, p->b, p->h_kv, p->s, t->d, k == yk)) ||
                     (rc = check_rope_strides(p->yk_stride, p->b, p->h_kv, p->s, t->d, true))))
         return rc;
+    // an output may be its own input, but neither the other input nor the other output
+    if (p->h_q && p->h_kv && p->s > 0 && (yq == yk || yq == k || yk == q)) return ATTN_CORE_ERR_INVALID_ARG;
     // in place means the same element at the same place
     for (int i = 0; i < 3; ++i)
         if ((p->h_q && q == yq && p->q_stride[i] != p->yq_stride[i]) ||
@@ -1044,6 +1046,8 @@ int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope
     }
     if (!strides) strides = packed;
     if (q && q == q_out && strides[0] != packed[0]) return ATTN_CORE_ERR_INVALID_ARG;
+    if (k_pages == v_pages || (q_out && (q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)))
+        return ATTN_CORE_ERR_INVALID_ARG;
     for (const void* x : {q, k, v, (const void*)q_out, (const void*)k_pages, (const void*)v_pages})
         if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
     if (p->n_tokens == 0) return ATTN_CORE_OK;
@@ -1079,6 +1083,7 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
     int rc = check_paged(p);
     if (rc) return rc;
     if (!q || !k_pages || !v_pages || !o || !lse || !workspace) return ATTN_CORE_ERR_INVALID_ARG;
+    if (o == q || o == k_pages || o == v_pages) return ATTN_CORE_ERR_INVALID_ARG;
     for (const void* x : {q, k_pages, v_pages, (const void*)o, (const void*)lse})
         if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_CORE_ERR_MISALIGNED;

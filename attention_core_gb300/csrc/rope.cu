@@ -272,6 +272,7 @@ Split split(int units, int batches, int tokens, int heads, int sms)
     const int64_t x = (int64_t)batches * ((tokens + s.tile - 1) / s.tile);
     int64_t groups = ((int64_t)kBlocksPerSm * sms + x - 1) / x;
     groups = groups < heads ? groups : heads;
+    groups = groups < 65535 ? groups : 65535;      // the grid's limit in y
     s.heads = (int)((heads + groups - 1) / groups);
     s.grid = dim3((unsigned)x, (unsigned)((heads + s.heads - 1) / s.heads));
     return s;

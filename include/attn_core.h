@@ -367,8 +367,8 @@ int attn_core_rope_init(const attn_core_rope_config* c, attn_core_rope_table* ou
  * in elements, non-negative multiples of 8; an input's may be 0 (a broadcast
  * tensor), an output's must keep its rows apart.  [b, h, s, d] is
  * {h s d, s d, d}; a packed [tokens, h, d] is b = 1, {0, d, h d}.  Pointers are
- * 16-byte aligned.  An output may be its own input (same pointer and strides),
- * otherwise it overlaps no input.  h_q or h_kv may be 0 (its pointers are then
+ * 16-byte aligned.  An output may be its own input (same pointer and strides);
+ * otherwise no output overlaps an input or the other output.  h_q or h_kv may be 0 (its pointers are then
  * ignored); s = 0 does nothing. */
 typedef struct {
     int32_t b, s, h_q, h_kv;
@@ -399,8 +399,10 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
  * A row that sees no key (kv_lens[i] < n, or no keys at all) gets O = 0 and
  * LSE = -inf.  Tokens from cu_seqlens_q[n_seq] on belong to no sequence: their
  * rows are left as they were.  What pages hold past a sequence's end is never
- * used, NaN included, nor are page_table entries past its last page.  Values
- * of keys that are visible to some row of a 128-row tile must be finite.
+ * used, NaN included, nor are page_table entries past its last page.  (Within
+ * a sequence a probability of 0 still meets its value in the product: an
+ * infinite or NaN value of one key reaches rows of the same sequence that the
+ * mask keeps from seeing it.)
  *
  * The three tables are in device memory and read by the kernels only, so a
  * captured graph follows them: one capture serves every step as long as the
@@ -442,13 +444,14 @@ int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope
                            void* v_pages, void* stream);
 
 /* Attention of the new tokens over the cache (which already holds their own
- * keys and values): O and LSE.  `workspace`: caller-owned device memory of at
- * least attn_core_paged_workspace_bytes(p) bytes, 256-byte aligned, for the
- * partial results of rows whose keys are shared out among thread blocks; its
- * contents on entry do not matter, and calls (or graph replays) that may overlap on the GPU need
- * one each.  The size depends on h_q / h_kv's and the tables' values not at
- * all: only on d.  Results do not depend on timing (no atomics): the same
- * inputs give the same bits on the same device. */
+ * keys and values): O and LSE, which overlap no input.  `workspace`:
+ * caller-owned device memory of at least attn_core_paged_workspace_bytes(p)
+ * bytes (it depends on d alone: 21 MB at d = 128), 256-byte aligned, for the
+ * partial results of rows whose keys are shared out among thread blocks.  Its
+ * contents on entry do not matter; calls (or graph replays) that may overlap on
+ * the GPU need one each.  One kernel, and where tiles may be cut a second one
+ * that joins their parts.  Nothing is summed in an order that depends on timing:
+ * the same inputs give the same bits on the same device. */
 size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p);
 int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
                         void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -79,6 +79,16 @@ def test_long_context_is_shared_out(d, hq, hkv):
     check_attention(o, lse, attend(p), p)
 
 
+def test_more_sequences_than_threads():
+    """A thousand single tokens: every thread of a block looks after several
+    sequences when it finds its share."""
+    nk = [1 + (37 * i) % 300 for i in range(1000)]
+    nq = [0 if i % 11 == 0 else 1 for i in range(1000)]
+    p = Paged(nq, nk, 2, 1, 64, 16, seed=15)
+    o, lse = _run(p)
+    check_attention(o, lse, attend(p), p)
+
+
 def test_chunk_over_long_context():
     p = Paged([33, 128], [9000, 20000], 8, 2, 128, 128, seed=4)
     o, lse = _run(p)
@@ -313,6 +323,39 @@ def test_wait_that_runs_out_is_reported():
     check_attention(o, lse, attend(p), p)
 
 
+def test_captured_graphs_with_cut_tiles():
+    """Two graphs, each with a batch of its own, replayed on two streams at once
+    while their contexts change length: the tiles are cut elsewhere each time."""
+    ps = [Paged([1, 3], [9000, 700], 8, 2, 128, 64, seed=s) for s in (30, 31)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in ps]
+    for p in ps:
+        b, o, lse = p.batch(), torch.empty_like(p.q), torch.empty(8, 4, device=DEV)
+        ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+        graphs.append((g, b))
+        outs.append((o, lse))
+    for lens in ([9000, 700], [4000, 3], [8191, 650]):
+        for p in ps:
+            p.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for (g, _), s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for p, (o, lse) in zip(ps, outs):
+            sub = Paged.__new__(Paged)
+            sub.__dict__.update(p.__dict__)
+            sub.nk = lens
+            sub.keys = [k[:n] for k, n in zip(p.keys, lens)]
+            sub.values = [v[:n] for v, n in zip(p.values, lens)]
+            check_attention(o, lse, attend(sub), sub)
+            assert int(p.status.item()) == 0
+
+
 def test_two_streams_with_a_batch_each():
     ps = [Paged([1, 40], [6000, 300], 8, 2, 128, 64, seed=s) for s in (20, 21)]
     streams = [torch.cuda.Stream() for _ in ps]
@@ -362,6 +405,10 @@ def test_python_refusals():
     assert e.value.code == ac.ERR_UNSUPPORTED
     with pytest.raises(ac.AttnCoreError):
         p.batch(h_q=3, h_kv=2)
+    with pytest.raises(ValueError):
+        p.batch(workspace=torch.empty(64, dtype=torch.uint8))
+    with pytest.raises(ac.AttnCoreError):
+        ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=p.q)
     small = p.batch(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     if ac.attn_core_paged_workspace_bytes(b.params) > 64:
         with pytest.raises(ac.AttnCoreError) as e:

@@ -95,6 +95,8 @@ def test_rope_refusals(fn):
     assert rc(_rope(), (0, k, yq, yk)) == ac.ERR_INVALID_ARG
     assert rc(_rope(), (q, k, yq, 0)) == ac.ERR_INVALID_ARG
     assert rc(_rope(q_stride=(4 * 640, 0, 64)), (q, k, q, yk)) == ac.ERR_INVALID_ARG       # in place elsewhere
+    for ptr in ((q, k, yq, yq), (q, k, k, yk), (q, k, yq, q), (q, k, k, q)):               # one tensor in two roles
+        assert rc(_rope(), ptr) == ac.ERR_INVALID_ARG
     assert rc(_rope(), table=None) == ac.ERR_INVALID_ARG
     assert rc(None) == ac.ERR_INVALID_ARG
     bad = ac.rope_table(64)
@@ -115,7 +117,7 @@ PAGED_INVALID = [dict(n_seq=0), dict(n_tokens=-1), dict(h_q=0), dict(h_q=3), dic
                  dict(max_pages=0), dict(causal=2), dict(scale=math.nan), dict(scale=math.inf), dict(cu_seqlens_q=None),
                  dict(kv_lens=None), dict(page_table=None), dict(n_pages=1 << 30, h_kv=4),
                  dict(max_pages=1 << 28), dict(n_tokens=1 << 30), dict(flags=1)]
-PAGED_UNSUPPORTED = [dict(d=72), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(h_q=258, h_kv=2)]
+PAGED_UNSUPPORTED = [dict(d=72), dict(max_pages=1 << 20, n_tokens=1 << 29, h_q=1, h_kv=1, page_size=256), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(h_q=258, h_kv=2)]
 
 
 def test_paged_refusals():
@@ -153,6 +155,9 @@ def test_paged_refusals():
     assert app(_paged(), st=(256, 130, 128)) == ac.ERR_MISALIGNED
     assert app(_paged(), st=(256, -128, 128)) == ac.ERR_INVALID_ARG
     assert app(_paged(), st=(512, 128, 128), out=(q, kp, vp)) == ac.ERR_INVALID_ARG    # in place, not packed
+    assert app(_paged(), out=(o, kp, kp)) == ac.ERR_INVALID_ARG
+    assert app(_paged(), (q, o, vp)) == ac.ERR_INVALID_ARG              # q_out over the new keys
+    assert fwd(_paged(), (q, kp, vp, q, lse, ws)) == ac.ERR_INVALID_ARG
     assert app(_paged(), t=ac.rope_table(96)) == ac.ERR_INVALID_ARG
     assert app(_paged(flags=ac.FLAG_TEST_WAIT_TIMEOUT)) == ac.ERR_INVALID_ARG
 
