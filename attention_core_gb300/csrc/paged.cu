@@ -20,8 +20,8 @@
 //   warp 2  V, into its own ring; rows past the sequence's end are zeroed in
 //           shared memory, so that what the page holds there (NaN included)
 //           meets no product
-//   warp 1  issues S_j = Q K_j^T (tcgen05) into one of two TMEM score buffers
-//   warp 3  issues O += P_j V_j with P read from TMEM
+//   warp 1  issues the tcgen05 MMAs: S_j = Q K_j^T into one of two TMEM score
+//           buffers, then O += P_{j-1} V_{j-1} with P read from TMEM
 //   warps 4-11  online softmax, one row per TMEM lane, two column halves of 64
 //           keys; for d <= 128 each half keeps its own maximum, sum and O
 //           accumulator, merged at the tile's end; for d = 160 TMEM has room
@@ -115,9 +115,8 @@ struct PagedCfg {
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[6], v_full[6], s_full[6], pv_done[6];
-    uint64_t pv_issued[2];  // the P.V that reads the score buffer has been issued
     uint64_t v_tail;        // a tile's last, partial V block has landed (rows past its end still to be zeroed)
-    uint64_t drain[2];      // every product of an issuing warp is done (before TMEM is released)
+    uint64_t drain;         // every product is done (before TMEM is released)
     uint64_t never;
     // completed by all row threads
     uint64_t p_full[2][2];  // [part][score buffer] P of the part (32 keys of each half) is in TMEM
@@ -136,7 +135,7 @@ static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
     kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
-    kSitePFull, kSiteSFull, kSitePvDone, kSitePvIssued, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
+    kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -275,7 +274,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             mbar_init(bar(all[i]), i < kBarsOnce ? 1 : kRowThreads);
         if (lane == 0) {
             bars->abort_flag = 0;
-            reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
+            // (a grid of whole tiles may be larger than the workspace's list, and cuts nothing)
+            if (!a.whole) reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
         }
         fence_mbar_init();
     }
@@ -302,7 +302,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     int per_head = 0;
     SeqTable table{};
     for (int s = s0; s < s1; ++s) {
-        table = read_seq(t, s, a.tpt, a.causal);
+        table = read_seq(t, s, a.tpt, a.causal, a.whole);
         if (table.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
         per_head = table.s.units(table.s.tiles());
         mine += (int64_t)per_head * t.h_kv;
@@ -325,7 +325,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         total += x;
     }
     int64_t per = quot(total + gridDim.x - 1, gridDim.x);
-    per = per > kMinUnits ? per : kMinUnits;
+    per = a.whole ? 1 : (per > kMinUnits ? per : kMinUnits);
     const int64_t u0 = (int64_t)blockIdx.x * per;
     const int64_t u1 = u0 + per < total ? u0 + per : total;
     const bool found = u0 < u1 && u0 >= upto - mine && u0 < upto;
@@ -335,7 +335,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         int64_t rel = u0 - (upto - mine);
         int s = s0;
         for (; found && run > 1; ++s) {              // with one sequence a thread it is at hand
-            table = read_seq(t, s, a.tpt, a.causal);
+            table = read_seq(t, s, a.tpt, a.causal, a.whole);
             per_head = table.s.units(table.s.tiles());
             if (rel < (int64_t)per_head * t.h_kv) break;
             rel -= (int64_t)per_head * t.h_kv;
@@ -344,11 +344,12 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         s = __shfl_sync(0xffffffffu, s, src);
         rel = __shfl_sync(0xffffffffu, rel, src);
         per_head = __shfl_sync(0xffffffffu, per_head, src);
-        table = read_seq(t, s, a.tpt, a.causal);
+        table = read_seq(t, s, a.tpt, a.causal, a.whole);
         const int head = (int)quot(rel, per_head);
         SegmentWalk w;
         w.tpt = a.tpt;
         w.causal = a.causal;
+        w.whole_tiles = a.whole;
         w.start(s, table, head, (int)(rel - (int64_t)head * per_head), u0, u1);
         if (lane == 0) bars->walk = w;
     }
@@ -456,23 +457,67 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     } else if (alive && warp == 2) {
         produce(std::true_type{}, maps.v, bars->v_full, bars->pv_done, sb + C::OFF_V);
     } else if (alive && warp == 1) {
-        // ---- S = Q K^T of every block (the whole warp issues, see mma_ss).  A score
-        // buffer holds S, then P, until its P.V has read it; the tensor pipe takes
-        // products in the order in which they are issued, so it is enough that the
-        // other warp has issued that P.V (the fences on both sides of the barrier
-        // carry the order from warp to warp).
-        constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);
+        // ---- MMA issuer (the whole warp, see mma_ss): one stream over all blocks of
+        // all segments, S of a block before P.V of the block before.  One warp issues
+        // both products because the tensor pipe takes one thread's products in order:
+        // S of block g + 1 may then overwrite the buffer that P.V of block g - 1 reads.
+        // (Issued from two warps, with the second told that the first had issued, they
+        // were seen to run out of order.)
+        constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);               // S = Q K^T
+        constexpr uint32_t IDO = idesc_bf16(128, P::WIDE * 64, false, true);       // O += P V, wide columns
+        constexpr uint32_t IDN = idesc_bf16(128, 32, false, true);                 // and the narrow chunk's
         Ring<C::SK> rs;
-        Ring<2> bs;
+        Ring<C::SV> rv;
+        Ring<2> bs, bv;             // score buffers of the next S and the next P.V
         Ring<C::NQ> qr;
+        uint32_t o_phase = 1;       // o_free: the first tile finds O free
+        bool pending = false;       // a block has its S but not its P.V
+        bool first = false;         // it is its tile's first
+        auto issue_pv = [&]() -> bool {
+            if (first) {
+                if (!wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
+                o_phase ^= 1;
+            }
+            const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
+            const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
+            const uint32_t more = first ? 0u : 1u;
+            if (!wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull))) return false;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                if (!wait_w(wc, bar(bars->p_full[part][bv.slot]), bv.phase, timeout_code(kSitePFull))) return false;
+                tc_fence_after();
+                // key slices of 16: 0, 1 | 2, 3 of half 0, and of half 1
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = 4 * (i / 2) + 2 * part + (i & 1);
+                    const bool fresh = C::SPLIT ? (kk & 3) == 0 : kk == 0;         // the accumulator's first slice
+                    const uint32_t tO = tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O);
+                    const uint32_t tA = tP + split_a_col(kk, 128);
+                    mma_ts(tO, tA, P::desc_wide(vbase, kk), IDO, fresh ? more : 1u);
+                    if constexpr (P::NARROW)
+                        mma_ts(tO + P::WIDE * 64, tA, P::desc_narrow(vbase, kk), IDN, fresh ? more : 1u);
+                }
+            }
+            mma_commit(bar(bars->pv_done[rv.slot]));
+            rv.advance();
+            bv.advance();
+            pending = false;
+            return true;
+        };
         bool ok = true;
         Work g;
         while (ok && next_work(walk, t, g)) {
+            // At a tile boundary the previous tile's last P.V goes first unless this
+            // tile's Q and first K block are already resident.
+            if (pending && (!test_wait_warp(bar(bars->q_full[qr.slot]), qr.phase) ||
+                            !test_wait_warp(bar(bars->k_full[rs.slot]), rs.phase))) {
+                ok = issue_pv();
+                if (!ok) break;
+            }
             ok = wait_w(wc, bar(bars->q_full[qr.slot]), qr.phase, timeout_code(kSiteQFull));
             const uint32_t qbase = sb + C::OFF_Q + qr.slot * C::TILE;
             for (int j = g.j0; j < g.j1 && ok; ++j) {
-                ok = wait_w(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull)) &&
-                     wait_w(wc, bar(bars->pv_issued[bs.slot]), bs.phase ^ 1, timeout_code(kSitePvIssued));
+                ok = wait_w(wc, bar(bars->k_full[rs.slot]), rs.phase, timeout_code(kSiteKFull));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t kbase = sb + C::OFF_K + rs.slot * C::TILE;
@@ -484,59 +529,16 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if (j == g.j1 - 1) mma_commit(bar(bars->q_empty[qr.slot]));
                 rs.advance();
                 bs.advance();
+                if (pending) ok = issue_pv();
+                pending = true;
+                first = j == g.j0;
             }
             qr.advance();
         }
+        if (ok && pending) ok = issue_pv();
         // every MMA must be complete before the CTA releases TMEM
-        mma_commit(bar(bars->drain[0]));
-        wait_w(wc, bar(bars->drain[0]), 0, timeout_code(kSiteDrain));
-    } else if (alive && warp == 3) {
-        // ---- O += P V of every block, from a warp (and SM sub-partition) of its own: one
-        // warp issuing both products was what bounded compute-heavy batches (1870
-        // cycles a block at d = 128 where the products take 1040).
-        constexpr uint32_t IDO = idesc_bf16(128, P::WIDE * 64, false, true);
-        constexpr uint32_t IDN = idesc_bf16(128, 32, false, true);
-        Ring<C::SV> rv;
-        Ring<2> bv;
-        uint32_t o_phase = 1;       // o_free: the first tile finds O free
-        bool ok = true;
-        Work g;
-        while (ok && next_work(walk, t, g)) {
-            ok = wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree));
-            o_phase ^= 1;
-            for (int j = g.j0; j < g.j1 && ok; ++j) {
-                const uint32_t vbase = sb + C::OFF_V + rv.slot * C::TILE;
-                const uint32_t tP = tmem + (bv.slot ? C::T_S1 : C::T_S0);
-                const uint32_t more = j > g.j0 ? 1u : 0u;
-                ok = wait_w(wc, bar(bars->v_full[rv.slot]), rv.phase, timeout_code(kSiteVFull));
-#pragma unroll
-                for (int part = 0; part < 2 && ok; ++part) {
-                    ok = wait_w(wc, bar(bars->p_full[part][bv.slot]), bv.phase, timeout_code(kSitePFull));
-                    if (!ok) break;
-                    tc_fence_after();
-                    // key slices of 16: 0, 1 | 2, 3 of half 0, and of half 1
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = 4 * (i / 2) + 2 * part + (i & 1);
-                        const bool fresh = C::SPLIT ? (kk & 3) == 0 : kk == 0;     // the accumulator's first slice
-                        const uint32_t tO = tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O);
-                        const uint32_t tA = tP + split_a_col(kk, 128);
-                        mma_ts(tO, tA, P::desc_wide(vbase, kk), IDO, fresh ? more : 1u);
-                        if constexpr (P::NARROW)
-                            mma_ts(tO + P::WIDE * 64, tA, P::desc_narrow(vbase, kk), IDN, fresh ? more : 1u);
-                    }
-                }
-                if (!ok) break;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bars->pv_issued[bv.slot]));
-                mma_commit(bar(bars->pv_done[rv.slot]));
-                rv.advance();
-                bv.advance();
-            }
-        }
-        mma_commit(bar(bars->drain[1]));
-        wait_w(wc, bar(bars->drain[1]), 0, timeout_code(kSiteDrain));
+        mma_commit(bar(bars->drain));
+        wait_w(wc, bar(bars->drain), 0, timeout_code(kSiteDrain));
     } else if (alive && warp >= 4) {
         // ---- softmax / epilogue: row = TMEM lane, half = which 64 keys of a block
         const RowThread rt = row_thread();
@@ -901,7 +903,7 @@ int paged_tokens_per_tile(int group) { return 128 / group; }
 namespace {
 
 template <int D>
-int launch_paged_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t st)
+int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
 {
     constexpr uint32_t smem = PagedCfg<D>::SMEM;
     auto kern = paged_attn_kernel<D>;
@@ -909,16 +911,18 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return (int)e;
     // The most units that the tables can ask for bounds the grid (short batches
     // need few CTAs), and the most blocks of a tile tells whether any can be cut.
-    const int64_t blocks = ((int64_t)a.t.max_pages * a.t.page_size + 127) / 128;
-    const int64_t tiles = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt + a.t.n_seq;
-    const int64_t want = (tiles * a.t.h_kv * blocks + kMinUnits - 1) / kMinUnits;
-    int grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
-    if (want < grid) grid = (int)want;
-    kern<<<grid, kThreads, smem, st>>>(m, a);
+    const int64_t blocks = ((int64_t)args.t.max_pages * args.t.page_size + 127) / 128;
+    const int64_t tiles = (((int64_t)args.t.n_tokens + args.tpt - 1) / args.tpt + args.t.n_seq) * args.t.h_kv;
+    const int64_t want = (tiles * blocks + kMinUnits - 1) / kMinUnits;
+    PagedArgs a = args;
+    a.whole = 0;
+    int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
+    if (want < grid) grid = want;
+    if (a.whole) grid = tiles;
+    kern<<<(unsigned)grid, kThreads, smem, st>>>(m, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
-    if (grid > 1 && blocks > kSnap) {
-        const int64_t rows = (int64_t)a.tpt * a.group < (int64_t)a.t.n_tokens * a.group ? (int64_t)a.tpt * a.group
-                                                                                      : (int64_t)a.t.n_tokens * a.group;
+    if (!a.whole && grid > 1 && blocks > kSnap) {
+        const int64_t rows = (int64_t)(a.tpt < a.t.n_tokens ? a.tpt : a.t.n_tokens) * a.group;
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;

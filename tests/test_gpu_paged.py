@@ -151,6 +151,24 @@ def test_same_inputs_same_bits():
         assert all(torch.equal(x, y) for x, y in zip(first, again))
 
 
+@pytest.mark.parametrize("d,hq,hkv,ps", [(128, 8, 8, 64), (128, 16, 2, 64), (160, 16, 4, 16), (64, 4, 4, 32)])
+def test_a_hundred_runs_agree(d, hq, hkv, ps):
+    """Memory-bound batches whose tiles are cut, over and over without a pause and
+    with a workspace that starts as NaN each time: the first result is the
+    definition's and every other one is the same bits."""
+    nk = [300 + (977 * i) % 3700 for i in range(24)]
+    p = Paged([1 + (5 * i) % 40 for i in range(24)], nk, hq, hkv, d, ps, seed=d + hq)
+    b = p.batch()
+    o, lse = _run(p)
+    check_attention(o, lse, attend(p), p)
+    differ = torch.zeros(1, dtype=torch.int64, device=DEV)
+    for _ in range(100):
+        b.workspace.fill_(0xFF)
+        o2, lse2 = ac.paged_fwd(b, p.q, p.k_pages, p.v_pages)
+        differ += (o2 != o).any() | (lse2 != lse).any()
+    assert int(differ.item()) == 0
+
+
 def test_large_offsets():
     """Pages whose elements lie past 2^31 (and bytes past 2^32) of the cache."""
     d, ps, hkv = 128, 128, 8
