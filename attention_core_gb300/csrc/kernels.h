@@ -280,7 +280,7 @@ struct PagedArgs {
     uint8_t* ws;                // paged_ws_bytes(d)
     int32_t d, causal;
     int32_t group, tpt;         // h_q / h_kv, and new tokens per tile of 128 rows
-    int32_t whole;              // a tile per CTA (paged_sched.cuh; set by the launcher)
+    uint32_t* counter;          // next tile, where the kernel may hand tiles out (set by the launcher), or null
     float scale_log2;           // score scale * log2(e)
     uint64_t timeout_ns;
     int32_t inject_timeout;

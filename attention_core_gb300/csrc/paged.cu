@@ -100,7 +100,7 @@ struct PagedCfg {
     static constexpr uint32_t OFF_V = OFF_K + SK * TILE;
     static constexpr uint32_t OFF_OST = OFF_V + SV * TILE;
     static constexpr uint32_t OFF_BAR = OFF_OST + (STAGE_O ? TILE : 0);
-    static constexpr uint32_t BAR_BYTES = 640;
+    static constexpr uint32_t BAR_BYTES = 1024;
     static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
     static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
     static constexpr uint32_t SMEM = OFF_XCH + XCH_BYTES + 1024;
@@ -112,6 +112,7 @@ struct PagedCfg {
 // Barriers of block g's ring slots (g % SK for K, g % SV for V) serve every role that waits for the
 // same event, so each product is committed once: s_full (S_g is in TMEM; K's slot is free) and
 // pv_done (O has block g; V's slot and the score buffer with P are free).
+constexpr int kJobs = 4;
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[6], v_full[6], s_full[6], pv_done[6];
@@ -124,17 +125,21 @@ struct PagedBars {
     uint64_t lsum, lsum2;   // row-statistics exchange at the end of a tile
     uint64_t o_free;        // the tile's O has been read
     uint64_t ost_full;      // a full tile's O is in the stage
+    uint64_t job_empty[kJobs];   // every consumer has read the job
+    uint64_t job_full[kJobs];
+    int64_t warp_sum[kThreads / 32], warp_tiles[kThreads / 32];
+    SegmentWalk walk;       // where this CTA's share starts
     uint32_t tmem_base;
     int32_t abort_flag;
-    int64_t warp_sum[kThreads / 32];
-    SegmentWalk walk;       // where this CTA's share starts
+    Segment job[kJobs];     // what the scheduling warp hands to the others
 };
+constexpr int kJobReaders = 3 + kRowThreads / 32;              // warps: K, V, MMA and the rows
 constexpr int kBarsOnce = offsetof(PagedBars, p_full) / 8;     // one arrival (a commit or a producer)
-constexpr int kBarsAll = offsetof(PagedBars, tmem_base) / 8;   // kRowThreads
+constexpr int kBarsRows = offsetof(PagedBars, job_empty) / 8;  // kRowThreads
 static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
-    kSiteInject = 1, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
+    kSiteInject = 1, kSiteJobEmpty, kSiteJobFull, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
     kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
@@ -218,6 +223,11 @@ struct Ring {
     }
 };
 
+__host__ __device__ inline size_t ws_counter_offset(int d)
+{
+    return (ws_cut_offset(d) + kPagedMaxCtas * sizeof(CutTile) + 255) & ~(size_t)255;
+}
+
 // A value that all lanes of a warp hold alike, in a form that the compiler knows to
 // be warp-uniform.  The producing and issuing warps' operands (descriptors,
 // coordinates, barriers) then live in uniform registers; from ordinary ones each
@@ -225,26 +235,60 @@ struct Ring {
 // product, against 28 and 23).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// The next segment with blocks to visit, for the producing and issuing warps (the
-// other segments only have zeros to write, which is the row threads' business).
-struct Work {
-    int seq, head, q_tok, kv, j0, j1;
-};
-__device__ __forceinline__ bool next_work(SegmentWalk& w, const PagedTables& t, Work& k)
+// Which split (paged_sched.cuh) a batch gets: `tiles` tiles of `units` blocks in all,
+// in `heads` pairs of a sequence and a KV head, over `ctas` CTAs.  Whole tiles want
+// enough of them to go round (fewer than 1.4 a CTA leave CTAs without work) and
+// several per KV head (or they bring nothing).  Then they win while they are few, by
+// the parts that need no join, and beyond that where the keys do not fit L2 and
+// would be read again for each row tile.  Measured, cut shares against whole tiles:
+//   336 tiles, 174 MB of keys and values, d = 160      88 -> 75 us
+//   512 tiles, 262 MB                                 171 -> 113
+//   536 tiles, 356 MB, 8 heads a KV head              210 -> 152
+//   272 tiles, 40 MB                                   32 -> 30
+//   256 tiles, 17 MB, one sequence                     39 -> 37
+//   1024 tiles, 34 MB                                 309 -> 313
+//   512 tiles of 2.5 blocks, 33 MB                     27 -> 29
+//   256 tiles, one per head, 333 MB                    67 -> 73
+// (the last three with the counter set on both sides).
+constexpr int64_t kManyBytes = 100000000;
+__device__ __forceinline__ bool hand_out_tiles(int64_t units, int64_t tiles, int64_t heads, int64_t ctas, int d)
 {
-    Segment g;
-    bool more;
-    do {
-        more = w.next(t, g);
-    } while (more && g.j1 <= g.j0);
-    if (!__all_sync(0xffffffffu, more)) return false;
-    k.seq = uniform(g.seq);
-    k.head = uniform(g.head);
-    k.q_tok = uniform(g.q_tok);
-    k.kv = uniform(g.kv);
-    k.j0 = uniform(g.j0);
-    k.j1 = uniform(g.j1);
-    return true;
+    if (10 * tiles < 14 * ctas || 2 * tiles < 3 * heads) return false;
+    if (2 * tiles <= 5 * ctas) return true;
+    // bytes of the keys and values, whose blocks each head's tiles visit again
+    return quot(units * heads, tiles) * (128 * 4 * d) > kManyBytes;
+}
+
+// A reader's side of the jobs: false at the end (or on a wait that ran out).
+template <bool SPECIAL>
+__device__ __forceinline__ bool next_job(PagedBars* bars, const WaitCtx& wc, Ring<kJobs>& jr, Segment& g)
+{
+    const uint32_t full = smem_u32(&bars->job_full[jr.slot]);
+    if constexpr (SPECIAL) {
+        if (!wait_w(wc, full, jr.phase, timeout_code(kSiteJobFull))) return false;
+        const Segment& s = bars->job[jr.slot];
+        g.seq = uniform(s.seq);
+        g.head = uniform(s.head);
+        g.q_tok = uniform(s.q_tok);
+        g.kv = uniform(s.kv);
+        g.j0 = uniform(s.j0);
+        g.j1 = uniform(s.j1);
+    } else {
+        if (!wait_warp(wc, full, jr.phase, timeout_code(kSiteJobFull))) return false;
+        g = bars->job[jr.slot];
+    }
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&bars->job_empty[jr.slot]));
+    jr.advance();
+    return g.j0 >= 0;
+}
+// The next one with blocks to visit, for the producing and issuing warps (the others
+// only have zeros to write, which is the row threads' business).
+__device__ __forceinline__ bool next_work(PagedBars* bars, const WaitCtx& wc, Ring<kJobs>& jr, Segment& g)
+{
+    while (next_job<true>(bars, wc, jr, g))
+        if (g.j1 > g.j0) return true;
+    return false;
 }
 
 }  // namespace
@@ -270,12 +314,14 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     // descriptors, and from warp 4 on the lengths.
     if (warp == 3) {
         uint64_t* all = reinterpret_cast<uint64_t*>(bars);
-        for (int i = lane; i < kBarsAll; i += 32)
-            mbar_init(bar(all[i]), i < kBarsOnce ? 1 : kRowThreads);
+        for (int i = lane; i < kBarsRows; i += 32) mbar_init(bar(all[i]), i < kBarsOnce ? 1 : kRowThreads);
+        if (lane < kJobs) {
+            mbar_init(bar(bars->job_empty[lane]), kJobReaders);
+            mbar_init(bar(bars->job_full[lane]), 1);
+        }
         if (lane == 0) {
             bars->abort_flag = 0;
-            // (a grid of whole tiles may be larger than the workspace's list, and cuts nothing)
-            if (!a.whole) reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
+            reinterpret_cast<CutTile*>(a.ws + ws_cut_offset(D))[blockIdx.x].last_cta = 0;
         }
         fence_mbar_init();
     }
@@ -298,14 +344,16 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     const int run = (t.n_seq + kThreads - 1) / kThreads;
     const int s0 = order * run < t.n_seq ? order * run : t.n_seq;
     const int s1 = s0 + run < t.n_seq ? s0 + run : t.n_seq;
-    int64_t mine = 0;
+    int64_t mine = 0, mine_tiles = 0, mine_heads = 0;
     int per_head = 0;
     SeqTable table{};
     for (int s = s0; s < s1; ++s) {
-        table = read_seq(t, s, a.tpt, a.causal, a.whole);
+        table = read_seq(t, s, a.tpt, a.causal);
         if (table.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
         per_head = table.s.units(table.s.tiles());
         mine += (int64_t)per_head * t.h_kv;
+        mine_tiles += (int64_t)table.s.tiles() * t.h_kv;
+        mine_heads += table.s.nq > 0 ? t.h_kv : 0;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -313,29 +361,37 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
         if ((int)lane >= o) upto += x;
     }
-    if (lane == 31) bars->warp_sum[order / 32] = upto;
+    int64_t tiles_heads = mine_tiles << 32 | mine_heads;       // both below 2^31 in all (the entry point's limits)
+#pragma unroll
+    for (int o = 16; o; o /= 2) tiles_heads += __shfl_xor_sync(0xffffffffu, tiles_heads, o);
+    if (lane == 31) {
+        bars->warp_sum[order / 32] = upto;
+        bars->warp_tiles[order / 32] = tiles_heads;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int64_t total = 0;
+    int64_t total = 0, all_tiles = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         const int64_t x = bars->warp_sum[w];
         if (w < order / 32) upto += x;
         total += x;
+        all_tiles += bars->warp_tiles[w];
     }
+    const bool hand_out = a.counter && hand_out_tiles(total, all_tiles >> 32, all_tiles & 0xffffffff, gridDim.x, D);
     int64_t per = quot(total + gridDim.x - 1, gridDim.x);
-    per = a.whole ? 1 : (per > kMinUnits ? per : kMinUnits);
+    per = per > kMinUnits ? per : kMinUnits;
     const int64_t u0 = (int64_t)blockIdx.x * per;
     const int64_t u1 = u0 + per < total ? u0 + per : total;
-    const bool found = u0 < u1 && u0 >= upto - mine && u0 < upto;
+    const bool found = !hand_out && u0 < u1 && u0 >= upto - mine && u0 < upto;
     const uint32_t who = __ballot_sync(0xffffffffu, found);
     if (who) {
         // the warp that holds the first unit finds its tile, all lanes together
         int64_t rel = u0 - (upto - mine);
         int s = s0;
         for (; found && run > 1; ++s) {              // with one sequence a thread it is at hand
-            table = read_seq(t, s, a.tpt, a.causal, a.whole);
+            table = read_seq(t, s, a.tpt, a.causal);
             per_head = table.s.units(table.s.tiles());
             if (rel < (int64_t)per_head * t.h_kv) break;
             rel -= (int64_t)per_head * t.h_kv;
@@ -344,12 +400,11 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         s = __shfl_sync(0xffffffffu, s, src);
         rel = __shfl_sync(0xffffffffu, rel, src);
         per_head = __shfl_sync(0xffffffffu, per_head, src);
-        table = read_seq(t, s, a.tpt, a.causal, a.whole);
+        table = read_seq(t, s, a.tpt, a.causal);
         const int head = (int)quot(rel, per_head);
         SegmentWalk w;
         w.tpt = a.tpt;
         w.causal = a.causal;
-        w.whole_tiles = a.whole;
         w.start(s, table, head, (int)(rel - (int64_t)head * per_head), u0, u1);
         if (lane == 0) bars->walk = w;
     }
@@ -357,7 +412,6 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     __syncthreads();
     const uint32_t tmem = (uint32_t)uniform((int)bars->tmem_base);
     const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
-    SegmentWalk walk = bars->walk;
     const int group = a.group;
 
     // the join may take its place on the chip (it waits for this grid's end)
@@ -366,6 +420,66 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     bool alive = true;
     if (a.inject_timeout) alive = wait_warp(wc, bar(bars->never), 0, timeout_code(kSiteInject));
 
+    if (alive && warp == 3) {
+        // ---- Scheduler: this CTA's segments, or tiles from the counter, into the jobs.
+        // Tiles are taken one ahead of the rows (every reader has read the one before),
+        // so that a CTA does not take what another could start on first.
+        Ring<kJobs> jr, before;
+        bool ok = true, more = true;
+        SegmentWalk walk = bars->walk;
+        int seq0 = 0;                        // tiles come in order: 32 sequences at a time,
+        int64_t base = 0, upto32 = 0;        // from tile `base` on, lane's own up to `upto32`
+        int tiles32 = 0;
+        SeqTable mine32{};
+        auto group32 = [&](int s) {
+            mine32 = s + (int)lane < t.n_seq ? read_seq(t, s + (int)lane, a.tpt, a.causal) : SeqTable{};
+            tiles32 = mine32.s.nq > 0 ? mine32.s.tiles() : 0;
+            upto32 = (int64_t)tiles32 * t.h_kv;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto32, o);
+                if ((int)lane >= o) upto32 += x;
+            }
+        };
+        if (hand_out) group32(0);
+        for (int n = 0; ok && more; ++n) {
+            ok = wait_w(wc, bar(bars->job_empty[jr.slot]), jr.phase ^ 1, timeout_code(kSiteJobEmpty));
+            if (ok && hand_out && n > 0)
+                ok = wait_w(wc, bar(bars->job_empty[before.slot]), before.phase, timeout_code(kSiteJobEmpty));
+            if (!ok) break;
+            Segment g;
+            if (hand_out) {
+                int64_t i = 0;
+                if (lane == 0) i = atomicAdd(a.counter, 1u);
+                i = __shfl_sync(0xffffffffu, i, 0);
+                more = i < (all_tiles >> 32);
+                while (more && i >= base + __shfl_sync(0xffffffffu, upto32, 31)) {
+                    base += __shfl_sync(0xffffffffu, upto32, 31);
+                    seq0 += 32;
+                    more = seq0 < t.n_seq;             // (always, of tables in order)
+                    group32(seq0);
+                }
+                if (more) {
+                    const int who32 = __ffs(__ballot_sync(0xffffffffu, i < base + upto32)) - 1;
+                    const int rel = (int)(i - base - (__shfl_sync(0xffffffffu, upto32 - (int64_t)tiles32 * t.h_kv, who32)));
+                    const int n_tiles = __shfl_sync(0xffffffffu, tiles32, who32);
+                    const int head = rel / n_tiles;
+                    g = whole_tile(read_seq(t, seq0 + who32, a.tpt, a.causal), seq0 + who32, head, rel - head * n_tiles);
+                }
+            } else {
+                more = __all_sync(0xffffffffu, walk.next(t, g));
+                if (more) g.last_cta = g.whole || !g.from_start ? 0 : (int)quot(g.tile_end - 1, per);
+            }
+            if (!more) g.j0 = g.j1 = -1;
+            if (lane == 0) {
+                bars->job[jr.slot] = g;
+                mbar_arrive(bar(bars->job_full[jr.slot]));
+            }
+            __syncwarp();
+            before = jr;
+            jr.advance();
+        }
+    }
     // ---- TMA producers.  The page_table entries of a tile come 32 at a time, one a
     // lane, the next 32 on their way.  A page outside the cache reads as zeros
     // (coordinates outside the tensor map) and is reported.
@@ -378,8 +492,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         Ring<C::NQ> qr;
         int tails = 0;
         bool ok = true;
-        Work g;
-        while (ok && next_work(walk, t, g)) {
+        Ring<kJobs> jr;
+        Segment g;
+        while (ok && next_work(bars, wc, jr, g)) {
             if constexpr (!is_v) {
                 // the tile's Q as soon as its buffer is free
                 const int qs = qr.slot;
@@ -505,10 +620,19 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             return true;
         };
         bool ok = true;
-        Work g;
-        while (ok && next_work(walk, t, g)) {
-            // At a tile boundary the previous tile's last P.V goes first unless this
-            // tile's Q and first K block are already resident.
+        Ring<kJobs> jr;
+        Segment g;
+        for (;;) {
+            // At a tile boundary the previous tile's last P.V goes first unless the next
+            // job is at hand (it may come only after the rows, which wait for that P.V,
+            // are done with this one) ...
+            if (pending && !test_wait_warp(bar(bars->job_full[jr.slot]), jr.phase)) {
+                ok = issue_pv();
+                if (!ok) break;
+            }
+            if (!next_job<true>(bars, wc, jr, g)) break;
+            if (g.j1 <= g.j0) continue;
+            // ... and its Q and first K block are resident.
             if (pending && (!test_wait_warp(bar(bars->q_full[qr.slot]), qr.phase) ||
                             !test_wait_warp(bar(bars->k_full[rs.slot]), rs.phase))) {
                 ok = issue_pv();
@@ -533,6 +657,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 pending = true;
                 first = j == g.j0;
             }
+            if (!ok) break;
             qr.advance();
         }
         if (ok && pending) ok = issue_pv();
@@ -552,8 +677,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         Ring<2> bs;                 // and its score buffer
         uint32_t tile_phase = 0, stage_phase = 0;
         bool ok = true;
+        Ring<kJobs> jr;
         Segment g;
-        while (ok && walk.next(t, g)) {
+        while (ok && next_job<false>(bars, wc, jr, g)) {
             const int nk = g.j1 - g.j0;
             const bool live = r_tok < g.n_tok && r < a.tpt * group;
             const bool warp_live = __any_sync(0xffffffffu, live);
@@ -785,7 +911,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     cut->q_tok = g.q_tok;
                     cut->n_rows = g.n_tok * group;
                     cut->head = g.head;
-                    cut->last_cta = (int32_t)((g.tile_end - 1) / per);
+                    cut->last_cta = g.last_cta;
                 }
             }
             tc_fence_before();
@@ -892,11 +1018,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
         a.lse[(size_t)head * t.n_tokens + tok] = sum > 0.f ? (m + log2f(sum)) * 0.693147180559945309f : -INFINITY;
 }
 
-size_t paged_ws_bytes(int d)
-{
-    const size_t b = ws_cut_offset(d) + kPagedMaxCtas * sizeof(CutTile);
-    return (b + 255) & ~(size_t)255;
-}
+size_t paged_ws_bytes(int d) { return ws_counter_offset(d) + 256; }
 
 int paged_tokens_per_tile(int group) { return 128 / group; }
 
@@ -915,13 +1037,22 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
     const int64_t tiles = (((int64_t)args.t.n_tokens + args.tpt - 1) / args.tpt + args.t.n_seq) * args.t.h_kv;
     const int64_t want = (tiles * blocks + kMinUnits - 1) / kMinUnits;
     PagedArgs a = args;
-    a.whole = 0;
     int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
     if (want < grid) grid = want;
-    if (a.whole) grid = tiles;
+    // The kernel may hand out tiles where hand_out_tiles() could say so of any lengths
+    // that these sizes allow, and sequences have half a tile's new tokens on average, not
+    // one or two.  The counter starts at 0; setting it costs 3 to 7 us, so other batches
+    // do without.
+    const int64_t least = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt * a.t.h_kv;         // tiles
+    const int64_t most_bytes = (int64_t)a.t.n_seq * a.t.max_pages * a.t.page_size * a.t.h_kv * (4 * D);
+    if (10 * tiles >= 14 * grid && 2ll * a.t.n_tokens >= (int64_t)a.tpt * a.t.n_seq && a.t.n_tokens >= 2ll * a.t.n_seq &&
+        (2 * least <= 5 * grid || most_bytes > kManyBytes)) {
+        a.counter = reinterpret_cast<uint32_t*>(a.ws + ws_counter_offset(D));
+        if ((e = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), st)) != cudaSuccess) return (int)e;
+    }
     kern<<<(unsigned)grid, kThreads, smem, st>>>(m, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
-    if (!a.whole && grid > 1 && blocks > kSnap) {
+    if (grid > 1 && blocks > kSnap) {
         const int64_t rows = (int64_t)(a.tpt < a.t.n_tokens ? a.tpt : a.t.n_tokens) * a.group;
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

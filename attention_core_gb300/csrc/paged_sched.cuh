@@ -11,9 +11,11 @@
 // the CTA whose share holds a tile's first unit takes all of it (cutting one
 // costs more, in the join, than the imbalance of a few blocks).
 //
-// The other split, `whole`: a unit is a tile and a CTA takes one.  Neighbouring CTAs
-// then visit the same keys at the same time, which matters where a KV head has a
-// few row tiles and the keys of all heads do not fit L2.
+// The other split hands out whole tiles, in the same order, to whichever CTA is
+// ready for one (a counter in the workspace).  Nothing is cut and joined, and
+// neighbouring CTAs visit the same keys at the same time, which matters where a KV
+// head has several row tiles and the keys of all heads do not fit L2; but the last
+// tiles leave CTAs without work.  hand_out_tiles() chooses.
 //
 // Lengths are device data, so every CTA finds its share by itself: a block-wide
 // sum over the sequences' units (closed form under the causal mask), then a walk
@@ -61,7 +63,7 @@ __host__ __device__ inline uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a
 // One sequence's shape: nq new tokens, kv keys (both below 2^31 - 256), tiles of
 // tpt tokens.  The units of one KV head fit 31 bits (the caller sees to it).
 struct SeqShape {
-    int nq, kv, tpt, causal, whole;
+    int nq, kv, tpt, causal;
     __host__ __device__ int tiles() const { return (int)(((uint32_t)nq + tpt - 1) / (uint32_t)tpt); }
     // blocks of 128 keys that tile m sees: those of its last row
     __host__ __device__ int blocks(int m) const
@@ -76,7 +78,7 @@ struct SeqShape {
     __host__ __device__ int cost(int m) const
     {
         const int n = blocks(m);
-        return n > 0 && !whole ? n : 1;
+        return n > 0 ? n : 1;
     }
     // units of the tiles 0 .. m - 1
     __host__ __device__ int units(int m) const;
@@ -89,7 +91,7 @@ __noinline__
 #endif
 __host__ __device__ inline int units_before(int m, int nq, int kv, int tpt, int causal)
 {
-    const SeqShape q{nq, kv, tpt, causal, 0};
+    const SeqShape q{nq, kv, tpt, causal};
     if (m <= 0) return 0;
     if (kv <= 0) return m;
     if (!causal) return m * q.cost(0);
@@ -103,10 +105,7 @@ __host__ __device__ inline int units_before(int m, int nq, int kv, int tpt, int 
     if (m > last) s += q.cost(last);
     return (int)s;
 }
-__host__ __device__ inline int SeqShape::units(int m) const
-{
-    return whole ? (m > 0 ? m : 0) : units_before(m, nq, kv, tpt, causal);
-}
+__host__ __device__ inline int SeqShape::units(int m) const { return units_before(m, nq, kv, tpt, causal); }
 
 // The last row tile of a head that starts at or before unit r of it.  On the
 // device a whole warp calls this with one r: each round its lanes test 32
@@ -136,13 +135,13 @@ struct SeqTable {
     SeqShape s;
     bool bad;
 };
-__host__ __device__ inline SeqTable read_seq(const PagedTables& t, int seq, int tpt, int causal, int whole)
+__host__ __device__ inline SeqTable read_seq(const PagedTables& t, int seq, int tpt, int causal)
 {
     SeqTable r;
     const int q0 = t.cu_q[seq], q1 = t.cu_q[seq + 1], kv = t.kv_lens[seq];
     r.bad = q0 < 0 || q1 < q0 || q1 > t.n_tokens || kv < 0 || kv > (int64_t)t.max_pages * t.page_size;
     r.q0 = q0;
-    r.s = SeqShape{r.bad ? 0 : q1 - q0, r.bad ? 0 : kv, tpt, causal, whole};
+    r.s = SeqShape{r.bad ? 0 : q1 - q0, r.bad ? 0 : kv, tpt, causal};
     return r;
 }
 
@@ -153,20 +152,40 @@ struct Segment {
     int kv;                // keys of the sequence
     int first_pos;         // position of the tile's first token (negative: no key for it)
     int j0, j1;            // blocks of this piece; both 0: the tile sees no key
-    bool whole;            // the whole tile
-    bool from_start;       // the tile's first unit is in it
+    int whole;             // the whole tile
+    int from_start;        // the tile's first unit is in it
+    int last_cta;          // a cut tile's first piece: the CTA of its last one
     int64_t tile_end;      // unit after the tile's last
 };
+
+// Tile m of a KV head's, whole.
+__host__ __device__ inline Segment whole_tile(const SeqTable& s, int seq, int head, int m)
+{
+    Segment g;
+    g.seq = seq;
+    g.head = head;
+    g.m = m;
+    g.q_tok = s.q0 + m * s.s.tpt;
+    g.n_tok = s.s.nq - m * s.s.tpt < s.s.tpt ? s.s.nq - m * s.s.tpt : s.s.tpt;
+    g.kv = s.s.kv;
+    g.first_pos = s.s.kv - s.s.nq + m * s.s.tpt;
+    g.j0 = 0;
+    g.j1 = s.s.blocks(m);
+    g.whole = g.from_start = 1;
+    g.last_cta = 0;
+    g.tile_end = 0;
+    return g;
+}
 
 // Walks a CTA's share of the line.  `at` is the unit at which the next segment
 // starts; the CTA's share ends at `end`.
 struct SegmentWalk {
-    int tpt, causal, whole_tiles;
+    int tpt, causal;
     int64_t at, end;
     int seq, head, m, b;   // where `at` is: block b of row tile m
     SeqTable cur;
 
-    __host__ __device__ void load(const PagedTables& t) { cur = read_seq(t, seq, tpt, causal, whole_tiles); }
+    __host__ __device__ void load(const PagedTables& t) { cur = read_seq(t, seq, tpt, causal); }
 
     // Unit `at_` lies r units into KV head h of sequence sq.  (Whole warps, see
     // find_tile.)
@@ -209,16 +228,10 @@ struct SegmentWalk {
         }
         const int64_t left = end - at;
         const int take = (n <= kSnap || left > n - b) ? n - b : (int)left;
-        g.seq = seq;
-        g.head = head;
-        g.m = m;
-        g.q_tok = cur.q0 + m * tpt;
-        g.n_tok = cur.s.nq - m * tpt < tpt ? cur.s.nq - m * tpt : tpt;
-        g.kv = cur.s.kv;
-        g.first_pos = cur.s.kv - cur.s.nq + m * tpt;
-        const int blocks = cur.s.blocks(m);
-        g.j0 = blocks > 0 ? b : 0;
-        g.j1 = whole_tiles ? blocks : (blocks > 0 ? b + take : 0);
+        g = whole_tile(cur, seq, head, m);
+        const bool sees = cur.s.blocks(m) > 0;
+        g.j0 = sees ? b : 0;
+        g.j1 = sees ? b + take : 0;
         g.whole = take == n;
         g.from_start = b == 0;
         g.tile_end = at + (n - b);
