@@ -241,15 +241,15 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // several per KV head (or they bring nothing).  Then they win while they are few, by
 // the parts that need no join, and beyond that where the keys do not fit L2 and
 // would be read again for each row tile.  Measured, cut shares against whole tiles:
-//   336 tiles, 174 MB of keys and values, d = 160      88 -> 75 us
+//   336 tiles, 174 MB of keys and values, d = 160      88 -> 66 us
 //   512 tiles, 262 MB                                 171 -> 113
-//   536 tiles, 356 MB, 8 heads a KV head              210 -> 152
+//   536 tiles, 356 MB, 8 heads a KV head              210 -> 141
 //   272 tiles, 40 MB                                   32 -> 30
-//   256 tiles, 17 MB, one sequence                     39 -> 37
+//   256 tiles, 17 MB, one sequence                     39 -> 39
 //   1024 tiles, 34 MB                                 309 -> 313
 //   512 tiles of 2.5 blocks, 33 MB                     27 -> 29
 //   256 tiles, one per head, 333 MB                    67 -> 73
-// (the last three with the counter set on both sides).
+// (the last three with the counter set on both sides, tiles in the sequences' order).
 constexpr int64_t kManyBytes = 100000000;
 __device__ __forceinline__ bool hand_out_tiles(int64_t units, int64_t tiles, int64_t heads, int64_t ctas, int d)
 {
@@ -427,13 +427,23 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         Ring<kJobs> jr, before;
         bool ok = true, more = true;
         SegmentWalk walk = bars->walk;
-        int seq0 = 0;                        // tiles come in order: 32 sequences at a time,
-        int64_t base = 0, upto32 = 0;        // from tile `base` on, lane's own up to `upto32`
-        int tiles32 = 0;
-        SeqTable mine32{};
+        // Tiles go out 32 sequences at a time, those with the most keys first (so that the
+        // last ones out are short): lane l holds the group's l-th, with the group's tiles
+        // up to and with its own.
+        int seq0 = 0, seq32 = 0, tiles32 = 0;
+        int64_t base = 0, upto32 = 0;        // the group's first tile
         auto group32 = [&](int s) {
-            mine32 = s + (int)lane < t.n_seq ? read_seq(t, s + (int)lane, a.tpt, a.causal) : SeqTable{};
-            tiles32 = mine32.s.nq > 0 ? mine32.s.tiles() : 0;
+            const SeqTable q = s + (int)lane < t.n_seq ? read_seq(t, s + (int)lane, a.tpt, a.causal) : SeqTable{};
+            const int tiles = q.s.nq > 0 ? q.s.tiles() : 0;
+            int rank = 0, from = 0;
+            for (int i = 0; i < 32; ++i) {
+                const int kv = __shfl_sync(0xffffffffu, q.s.kv, i);
+                rank += kv > q.s.kv || (kv == q.s.kv && i < (int)lane);
+            }
+            for (int i = 0; i < 32; ++i)
+                if (__shfl_sync(0xffffffffu, rank, i) == (int)lane) from = i;
+            seq32 = s + from;
+            tiles32 = __shfl_sync(0xffffffffu, tiles, from);
             upto32 = (int64_t)tiles32 * t.h_kv;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -463,8 +473,10 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     const int who32 = __ffs(__ballot_sync(0xffffffffu, i < base + upto32)) - 1;
                     const int rel = (int)(i - base - (__shfl_sync(0xffffffffu, upto32 - (int64_t)tiles32 * t.h_kv, who32)));
                     const int n_tiles = __shfl_sync(0xffffffffu, tiles32, who32);
+                    const int seq = __shfl_sync(0xffffffffu, seq32, who32);
                     const int head = rel / n_tiles;
-                    g = whole_tile(read_seq(t, seq0 + who32, a.tpt, a.causal), seq0 + who32, head, rel - head * n_tiles);
+                    // the last row tile first: under the causal mask it is the longest
+                    g = whole_tile(read_seq(t, seq, a.tpt, a.causal), seq, head, n_tiles - 1 - (rel - head * n_tiles));
                 }
             } else {
                 more = __all_sync(0xffffffffu, walk.next(t, g));
