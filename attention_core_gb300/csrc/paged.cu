@@ -7,15 +7,23 @@
 // tile, so a KV head's pages are read once per tile, not once per head.
 //
 // Bounds: with few rows per KV head (single tokens) the pages' bytes over HBM;
-// with many, the row work of the softmax beside the two products of each
-// 128 x 128 block.  The tile is M = 128 in both: with 8 live rows the padded
-// products still take less time (about 1000 cycles a block at d = 128) than the
-// block's 64 KB take to arrive at one SM's share of HBM (about 2700), and warps
-// without a live row skip the softmax.
+// with many, the chain scores -> softmax -> P.V of each 128 x 128 block, whose
+// products alone take about 1000 cycles at d = 128 and which now takes about 1400,
+// and under sustained load the power limit (1380 W, SM clock 1.8 of 2.07 GHz).  The
+// tile is M = 128 in both: with 8 live rows the padded products still take less
+// time than the block's 64 KB take to arrive at one SM's share of HBM (about 2700
+// cycles), and warps without a live row skip the softmax.  Measured on one GB300:
+//   one new token, 64/8 heads of 128, one sequence of 131072 keys   87 us (6.1 TB/s)
+//   the same for 64 sequences of up to 8192 keys                   200 us (6.6 TB/s)
+//   2048 new tokens over 8192 keys, 64/8 heads of 128              337 us in a loop,
+//                              300 us before the power limit (1.43 / 1.6 PFLOP/s)
+//   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160   66 us
+//   one new token over 500 keys                                      9 us in a graph
 //
-// Persistent, one CTA per SM; each takes an equal share of all blocks
-// (paged_sched.cuh), cutting long tiles.  Structure (384 threads), as the
-// forward of the core:
+// Persistent, one CTA per SM.  The work is cut into equal shares of blocks, or
+// handed out in whole tiles (paged_sched.cuh).  Structure (384 threads):
+//   warp 3  scheduler: the CTA's next segments (tiles, or pieces of them), in a ring
+//           of jobs that the others read
 //   warp 0  K, by TMA: one box per page and column chunk; and each tile's Q
 //   warp 2  V, into its own ring; rows past the sequence's end are zeroed in
 //           shared memory, so that what the page holds there (NaN included)
@@ -109,10 +117,11 @@ struct PagedCfg {
     static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
 };
 
-// Barriers of block g's ring slots (g % SK for K, g % SV for V) serve every role that waits for the
-// same event, so each product is committed once: s_full (S_g is in TMEM; K's slot is free) and
-// pv_done (O has block g; V's slot and the score buffer with P are free).
 constexpr int kJobs = 4;
+// Barriers of block g's ring slots (g % SK for K, g % SV for V) serve every role that
+// waits for the same event, so each product is committed once: s_full (S_g is in TMEM;
+// K's slot is free) and pv_done (O has block g; V's slot and the score buffer with P
+// are free).
 struct PagedBars {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[6], v_full[6], s_full[6], pv_done[6];
@@ -139,8 +148,8 @@ constexpr int kBarsRows = offsetof(PagedBars, job_empty) / 8;  // kRowThreads
 static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
-    kSiteInject = 1, kSiteJobEmpty, kSiteJobFull, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull, kSiteVFull, kSiteVTail,
-    kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
+    kSiteInject = 1, kSiteJobEmpty, kSiteJobFull, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull,
+    kSiteVFull, kSiteVTail, kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -338,8 +347,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     }
 
     // ---- this CTA's share of the line: every thread sums the units of its run of
-    // sequences, the block sums those, and the run that holds the share's first
-    // unit finds the sequence.
+    // sequences, the block sums those, and the warp whose runs hold the share's first
+    // unit finds its tile.
     const int order = ((int)threadIdx.x + kThreads - 128) % kThreads;     // warp 4 first
     const int run = (t.n_seq + kThreads - 1) / kThreads;
     const int s0 = order * run < t.n_seq ? order * run : t.n_seq;

@@ -10,8 +10,13 @@
 //
 // Both kernels are bound by HBM: every element is read and written once.  A
 // thread owns one 16-byte unit of pairs of one token, keeps its cosines and
-// sines in registers and walks over the heads, so the angles cost one
-// evaluation per (token, unit, head lane) and no shared memory.
+// sines in registers and walks over some of the heads, so an angle is formed
+// once for all of those and there is no shared memory; the first heads' loads go
+// out before the angles are formed.  Measured: Q and K of [1, 64 + 8, 8192, 128]
+// 49.5 us (6.1 TB/s; 54.0 with all heads in one block and loads behind the
+// angles), [2, 12 + 12, 2048, 128] with half of each head 13.5 us, the tiny
+// [1, 2 + 2, 128, 64] 2.4 us, all in a graph; as single calls the last two take the
+// host's 15 us.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -259,6 +264,9 @@ int mode_of(const RopeTable& t) { return t.interleaved ? 2 : (t.rot % 16 == 0 ? 
 // Tokens per block: as many as fit its threads, so that each angle is formed once
 // per block and a head's rows are read in long runs; the heads are then shared out
 // over as many blocks as give every SM kBlocksPerSm.
+// Measured per blocks an SM at 128 threads, on the [64 + 8, 8192, 128] layer and on
+// [2, 12 + 12, 2048, 128]: 8: 56.5 and 14.9 us, 16: 52.1 and 12.8, 24: 49.5 and 13.5,
+// 32: 48.2 and 13.8, 64: 48.5 and 15.9; 256 threads are slower on both.
 constexpr int kBlocksPerSm = 24;
 struct Split {
     int tile, heads;
