@@ -89,6 +89,68 @@ def test_more_sequences_than_threads():
     check_attention(o, lse, attend(p), p)
 
 
+# batches whose tiles are handed out whole: at least 1.4 per CTA, several per KV head
+HANDED_OUT = [
+    ([500] * 5, [700, 2500, 500, 1300, 512], 16, 16, 160, 32, True),
+    ([300, 1, 0, 450, 64, 200, 129], [300, 9, 40, 0, 1000, 150, 4000], 24, 24, 64, 16, True),   # no keys; fewer keys than tokens
+    ([130 + 3 * i for i in range(40)], [200 + 31 * i for i in range(40)], 4, 4, 96, 64, True),   # more than 32 sequences
+    ([700, 900], [4000, 900], 32, 4, 128, 128, False),
+    ([100, 90, 77, 128], [3000, 90, 2000, 128], 128, 16, 128, 64, True),
+]
+
+
+@pytest.mark.parametrize("case", HANDED_OUT, ids=lambda c: f"n{len(c[0])}_h{c[2]}-{c[3]}_d{c[4]}")
+def test_whole_tiles_handed_out(case):
+    nq, nk, hq, hkv, d, ps, causal = case
+    p = Paged(nq, nk, hq, hkv, d, ps, seed=16, n_tokens=sum(nq) + 9)
+    tiles = sum(-(-n // (128 // (hq // hkv))) for n in nq) * hkv
+    assert tiles >= 1.4 * 152
+    o, lse = torch.full_like(p.q, 7.0), torch.full((hq, p.n_tokens), 7.0, device=DEV)
+    b = p.batch(causal=causal)
+    for _ in range(3):
+        b.workspace.fill_(0xFF)
+        ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    check_attention(o, lse, attend(p, causal), p)
+    assert (o[sum(nq):] == 7).all() and (lse[:, sum(nq):] == 7).all()
+    # one bad sequence: reported, the others' rows unchanged
+    good = o.clone()
+    p.kv_lens[0] = -1
+    ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) & 0xff == ac.ERR_DEVICE_TABLE
+    rest = slice(nq[0], sum(nq))
+    assert ((o[rest].double() - good[rest].double()).abs() <= 2.0 ** -7 * (1 + good[rest].double().abs())).all()
+
+
+def test_graph_moves_between_the_splits():
+    """A captured call whose lengths change: tiles handed out whole at one replay,
+    equal shares of cut tiles at the next."""
+    n = [500] * 6
+    p = Paged(n, [2000] * 6, 16, 16, 64, 64, seed=17)
+    b = p.batch()
+    o, lse = torch.empty_like(p.q), torch.empty(16, p.n_tokens, device=DEV)
+    ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ac.paged_fwd(b, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+    for lens in ([500] * 6, [100, 3, 2, 1, 0, 50], [1, 1, 1, 1, 1, 500], [500, 500, 0, 0, 500, 500]):
+        cu = [0]
+        for x in lens:
+            cu.append(cu[-1] + x)
+        p.cu.copy_(torch.tensor(cu, dtype=torch.int32, device=DEV))
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        sub = Paged.__new__(Paged)
+        sub.__dict__.update(p.__dict__)
+        sub.nq, sub.cu_host = lens, cu
+        check_attention(o, lse, attend(sub), sub)
+        assert int(p.status.item()) == 0
+
+
 def test_chunk_over_long_context():
     p = Paged([33, 128], [9000, 20000], 8, 2, 128, 128, seed=4)
     o, lse = _run(p)

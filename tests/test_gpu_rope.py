@@ -39,6 +39,9 @@ CASES = [
     (3, 2, 1, 19, 160, 8, True, "linear", 4.0),
     (1, 16, 16, 517, 512, 256, False, "bands", 4.0),
     (1, 64, 8, 2500, 128, 128, True, "yarn", 8.0),
+    (1, 1, 1, 1, 8, 8, True, "none", 1.0),           # the smallest head, one token
+    (3, 1, 2, 70, 16, 16, False, "none", 1.0),
+    (1, 300, 1, 2, 32, 8, False, "linear", 2.0),     # more heads than tokens
 ]
 
 
