@@ -13,10 +13,10 @@
 // sines in registers and walks over some of the heads, so an angle is formed
 // once for all of those and there is no shared memory; the first heads' loads go
 // out before the angles are formed.  Measured: Q and K of [1, 64 + 8, 8192, 128]
-// 49.5 us (6.1 TB/s; 54.0 with all heads in one block and loads behind the
-// angles), [2, 12 + 12, 2048, 128] with half of each head 13.5 us, the tiny
-// [1, 2 + 2, 128, 64] 2.4 us, all in a graph; as single calls the last two take the
-// host's 15 us.
+// 46.2 us (6.5 TB/s, 96% of a plain copy's rate; 54.0 with all heads in one block and
+// loads behind the angles), [2, 12 + 12, 2048, 128] with half of each head 11.8 us,
+// the tiny [1, 2 + 2, 128, 64] 2.4 us, all in a graph; as single calls the last two
+// take the host's 15 us.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -25,7 +25,7 @@ namespace ac {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kAhead = 2;   // heads whose loads a thread has in flight
+constexpr int kAhead = 4;   // heads whose loads a thread has in flight
 
 __device__ __forceinline__ uint32_t rot_pair16(uint32_t xa, uint32_t xb, float c0, float s0, float c1, float s1,
                                                uint32_t& yb)
@@ -261,13 +261,15 @@ namespace {
 
 int mode_of(const RopeTable& t) { return t.interleaved ? 2 : (t.rot % 16 == 0 ? 0 : 1); }
 
-// Tokens per block: as many as fit its threads, so that each angle is formed once
-// per block and a head's rows are read in long runs; the heads are then shared out
-// over as many blocks as give every SM kBlocksPerSm.
-// Measured per blocks an SM at 128 threads, on the [64 + 8, 8192, 128] layer and on
-// [2, 12 + 12, 2048, 128]: 8: 56.5 and 14.9 us, 16: 52.1 and 12.8, 24: 49.5 and 13.5,
-// 32: 48.2 and 13.8, 64: 48.5 and 15.9; 256 threads are slower on both.
-constexpr int kBlocksPerSm = 24;
+// Tokens per block: as many as fit its threads, so that each angle is formed once per
+// block and a head's rows are read in long runs.  Heads per block: as many as a thread
+// has loads in flight, so that all of its reads go out at once and none waits behind a
+// write; fewer where that leaves an SM without eight blocks.  Measured on the
+// [64 + 8, 8192, 128] layer and on [2, 12 + 12, 2048, 128] (half of each head), in a
+// graph, with 2, 3, 4, 5, 6 and 8 heads and loads: 59.3 and 15.8 us, 48.7 and 13.0,
+// 46.2 and 11.8, 46.6 and 11.3, 47.2 and 11.3, 47.1 and 11.9; two loads ahead in a
+// longer loop: 48.4 to 49 and 13.3 to 14; 256 threads: 47.3 and 12.5.
+constexpr int kBlocksPerSm = 8;
 struct Split {
     int tile, heads;
     dim3 grid;
@@ -277,8 +279,11 @@ Split split(int units, int batches, int tokens, int heads, int sms)
     Split s;
     s.tile = 1;
     while (2 * s.tile * units <= kRopeThreads && s.tile < tokens) s.tile *= 2;
+    const int lanes = kRopeThreads / (s.tile * units);
     const int64_t x = (int64_t)batches * ((tokens + s.tile - 1) / s.tile);
     int64_t groups = ((int64_t)kBlocksPerSm * sms + x - 1) / x;
+    const int64_t by_heads = (heads + kAhead * lanes - 1) / (kAhead * lanes);
+    groups = groups > by_heads ? groups : by_heads;
     groups = groups < heads ? groups : heads;
     groups = groups < 65535 ? groups : 65535;      // the grid's limit in y
     s.heads = (int)((heads + groups - 1) / groups);
