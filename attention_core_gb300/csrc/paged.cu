@@ -414,6 +414,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         SegmentWalk w;
         w.tpt = a.tpt;
         w.causal = a.causal;
+        w.snap = snap_blocks(all_tiles >> 32, gridDim.x);
         w.start(s, table, head, (int)(rel - (int64_t)head * per_head), u0, u1);
         if (lane == 0) bars->walk = w;
     }
@@ -1073,7 +1074,7 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
     }
     kern<<<(unsigned)grid, kThreads, smem, st>>>(m, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
-    if (grid > 1 && blocks > kSnap) {
+    if (grid > 1 && blocks > kLeastSnap) {
         const int64_t rows = (int64_t)(a.tpt < a.t.n_tokens ? a.tpt : a.t.n_tokens) * a.group;
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -7,9 +7,9 @@
 // line of T units, and CTA c takes the units [c * per, (c + 1) * per), per =
 // ceil(T / grid): every CTA gets the same number of blocks whatever the lengths
 // are, and a tile is cut only where a CTA's share ends.  The parts of a cut tile
-// are joined by a second kernel.  Tiles of at most kSnap blocks are not cut:
-// the CTA whose share holds a tile's first unit takes all of it (cutting one
-// costs more, in the join, than the imbalance of a few blocks).
+// are joined by a second kernel.  Short tiles are not cut: the CTA whose share holds
+// a tile's first unit takes all of it (cutting one costs more, in the join, than the
+// imbalance of a few blocks).  How short goes by the tiles (snap_blocks).
 //
 // The other split hands out whole tiles, in the same order, to whichever CTA is
 // ready for one (a counter in the workspace).  Nothing is cut and joined, and
@@ -27,8 +27,14 @@
 
 namespace ac {
 
-constexpr int kSnap = 4;        // tiles of at most this many blocks stay whole
 constexpr int kMinUnits = 2;    // least share of a CTA
+constexpr int kLeastSnap = 4;
+// Tiles of at most this many blocks stay whole: few tiles have to be shared out, many
+// go round by themselves.  Measured at 4 and 8 (64/8 heads, a single token each): one
+// sequence of 1000 keys (8 tiles of 8 blocks) 10.0 and 11.8 us, 16 of 1000 keys 21.4 and
+// 17.9, 64 of 700 keys 39.3 and 38.6; a least share of 1 or 4 instead of 2 is within 3%
+// or slower.
+__host__ __device__ inline int snap_blocks(int64_t tiles, int64_t ctas) { return 2 * tiles >= ctas ? 8 : kLeastSnap; }
 
 // a / b in the 32-bit divide where both fit (nearly always), which takes a
 // fraction of the 64-bit one's time
@@ -180,7 +186,7 @@ __host__ __device__ inline Segment whole_tile(const SeqTable& s, int seq, int he
 // Walks a CTA's share of the line.  `at` is the unit at which the next segment
 // starts; the CTA's share ends at `end`.
 struct SegmentWalk {
-    int tpt, causal;
+    int tpt, causal, snap;
     int64_t at, end;
     int seq, head, m, b;   // where `at` is: block b of row tile m
     SeqTable cur;
@@ -199,7 +205,7 @@ struct SegmentWalk {
         m = find_tile(cur.s, r);
         b = r - cur.s.units(m);
         const int n = cur.s.cost(m);
-        if (b > 0 && n <= kSnap) {                           // another CTA has all of this tile
+        if (b > 0 && n <= snap) {                           // another CTA has all of this tile
             at += n - b;
             b = n;
         }
@@ -227,7 +233,7 @@ struct SegmentWalk {
             n = cur.s.cost(m);
         }
         const int64_t left = end - at;
-        const int take = (n <= kSnap || left > n - b) ? n - b : (int)left;
+        const int take = (n <= snap || left > n - b) ? n - b : (int)left;
         g = whole_tile(cur, seq, head, m);
         const bool sees = cur.s.blocks(m) > 0;
         g.j0 = sees ? b : 0;

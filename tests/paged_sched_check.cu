@@ -47,6 +47,7 @@ static void one()
     t.max_pages = 1000;
     t.page_size = 16;
     std::vector<int64_t> first(1, 0);
+    int64_t tiles = 0;
     for (int i = 0; i < ns; ++i) {
         const SeqTable q = read_seq(t, i, tpt, causal);
         WANT(!q.bad);
@@ -58,7 +59,9 @@ static void one()
         }
         WANT(q.s.units(q.s.tiles()) == sum);
         first.push_back(first.back() + sum * h_kv);
+        tiles += q.s.tiles() * h_kv;
     }
+    const int snap = snap_blocks(tiles, ctas);
     const int64_t total = first.back();
     int64_t per = (total + ctas - 1) / ctas;
     if (per < kMinUnits) per = kMinUnits;
@@ -73,6 +76,7 @@ static void one()
         SegmentWalk w;
         w.tpt = tpt;
         w.causal = causal;
+        w.snap = snap;
         w.start(s, q, (int)(rel / head), (int)(rel % head), u0, u1);
         Segment g;
         int starts = 0, continues = 0;
@@ -82,7 +86,7 @@ static void one()
             if (g.whole) continue;
             ++cuts;
             WANT(g.j1 - g.j0 < read_seq(t, g.seq, tpt, causal).s.blocks(g.m));
-            WANT(read_seq(t, g.seq, tpt, causal).s.blocks(g.m) > kSnap);
+            WANT(read_seq(t, g.seq, tpt, causal).s.blocks(g.m) > snap);
             if (g.from_start) {
                 ++starts;
                 const int64_t last = (g.tile_end - 1) / per;
