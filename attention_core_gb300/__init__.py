@@ -229,7 +229,8 @@ def load_library(path: str = LIB_PATH):
     lib.attn_core_page_copy.restype = ctypes.c_int
     i64 = ctypes.c_int64
     for name, argtypes in (("attn_core_rope_fwd", [vp] * 7), ("attn_core_rope_bwd", [vp] * 7),
-                           ("attn_core_paged_append", [vp] * 10), ("attn_core_paged_fwd", [vp] * 7 + [ctypes.c_size_t, vp]),
+                           ("attn_core_paged_append", [vp] * 10),
+                           ("attn_core_paged_fwd", [vp] * 7 + [ctypes.c_size_t, vp]),
                            ("attn_core_page_copy", [vp, i64, i64, i64, i64, vp, i64, vp])):
         f = lib[name]
         f.argtypes, f.restype = argtypes, ctypes.c_int

@@ -149,7 +149,8 @@ static_assert(sizeof(PagedBars) <= PagedCfg<64>::BAR_BYTES, "barrier block");
 
 enum : int32_t {
     kSiteInject = 1, kSiteJobEmpty, kSiteJobFull, kSiteKEmpty, kSiteVEmpty, kSiteQEmpty, kSiteQFull, kSiteKFull,
-    kSiteVFull, kSiteVTail, kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage, kSiteDrain
+    kSiteVFull, kSiteVTail, kSitePFull, kSiteSFull, kSitePvDone, kSiteXmax, kSiteOFree, kSiteLsum, kSiteStage,
+    kSiteDrain
 };
 __device__ __forceinline__ int32_t timeout_code(int32_t site) { return 6 | (site << 8); }
 
@@ -481,7 +482,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 }
                 if (more) {
                     const int who32 = __ffs(__ballot_sync(0xffffffffu, i < base + upto32)) - 1;
-                    const int rel = (int)(i - base - (__shfl_sync(0xffffffffu, upto32 - (int64_t)tiles32 * t.h_kv, who32)));
+                    const int64_t before32 = upto32 - (int64_t)tiles32 * t.h_kv;
+                    const int rel = (int)(i - base - __shfl_sync(0xffffffffu, before32, who32));
                     const int n_tiles = __shfl_sync(0xffffffffu, tiles32, who32);
                     const int seq = __shfl_sync(0xffffffffu, seq32, who32);
                     const int head = rel / n_tiles;
@@ -693,7 +695,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         const uint32_t lane_off = rt.lane_off;
         const uint32_t tX = tmem + C::T_X + lane_off;
         float2* xch = reinterpret_cast<float2*>(smem_raw + pad + C::OFF_XCH);
-        const int r_tok = r / group, r_head = r % group;       // row r: token r_tok of the tile, head r_head of the group
+        const int r_tok = r / group, r_head = r % group;       // row r: token of the tile, head of the group
         Ring<C::SK> rg;             // this block's slot of K
         Ring<C::SV> rv;             // and of V
         Ring<2> bs;                 // and its score buffer
@@ -907,20 +909,18 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(rr[e]) * a0;
                     }
-                    if (staged) {
+                    if (g.whole) {
 #pragma unroll
-                        for (int u4 = 0; u4 < 4; ++u4)
-                            st_shared_v4(sb + C::OFF_OST + G::template unit_offset<128>(r, c32 * 32 + 8 * u4),
-                                         pack_bf16x2(f[8 * u4], f[8 * u4 + 1]), pack_bf16x2(f[8 * u4 + 2], f[8 * u4 + 3]),
-                                         pack_bf16x2(f[8 * u4 + 4], f[8 * u4 + 5]),
-                                         pack_bf16x2(f[8 * u4 + 6], f[8 * u4 + 7]));
-                    } else if (live && g.whole) {
+                        for (int u4 = 0; u4 < 4; ++u4) {
+                            uint32_t w[4];
 #pragma unroll
-                        for (int u4 = 0; u4 < 4; ++u4)
-                            reinterpret_cast<uint4*>(orow)[c32 * 4 + u4] =
-                                make_uint4(pack_bf16x2(f[8 * u4], f[8 * u4 + 1]), pack_bf16x2(f[8 * u4 + 2], f[8 * u4 + 3]),
-                                           pack_bf16x2(f[8 * u4 + 4], f[8 * u4 + 5]),
-                                           pack_bf16x2(f[8 * u4 + 6], f[8 * u4 + 7]));
+                            for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(f[8 * u4 + 2 * e], f[8 * u4 + 2 * e + 1]);
+                            if (staged)
+                                st_shared_v4(sb + C::OFF_OST + G::template unit_offset<128>(r, c32 * 32 + 8 * u4), w[0],
+                                             w[1], w[2], w[3]);
+                            else if (live)
+                                reinterpret_cast<uint4*>(orow)[c32 * 4 + u4] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     } else if (live) {
 #pragma unroll
                         for (int u4 = 0; u4 < 8; ++u4)
@@ -1067,8 +1067,8 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
     // do without.
     const int64_t least = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt * a.t.h_kv;         // tiles
     const int64_t most_bytes = (int64_t)a.t.n_seq * a.t.max_pages * a.t.page_size * a.t.h_kv * (4 * D);
-    if (10 * tiles >= 14 * grid && 2ll * a.t.n_tokens >= (int64_t)a.tpt * a.t.n_seq && a.t.n_tokens >= 2ll * a.t.n_seq &&
-        (2 * least <= 5 * grid || most_bytes > kManyBytes)) {
+    if (10 * tiles >= 14 * grid && 2ll * a.t.n_tokens >= (int64_t)a.tpt * a.t.n_seq &&
+        a.t.n_tokens >= 2ll * a.t.n_seq && (2 * least <= 5 * grid || most_bytes > kManyBytes)) {
         a.counter = reinterpret_cast<uint32_t*>(a.ws + ws_counter_offset(D));
         if ((e = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), st)) != cudaSuccess) return (int)e;
     }

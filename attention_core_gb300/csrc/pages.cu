@@ -25,7 +25,8 @@ struct PairList {
 
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads)
-page_copy_kernel(uint4* pages, int64_t plane_units, int64_t page_units, int pieces, const __grid_constant__ PairList<N> list)
+page_copy_kernel(uint4* pages, int64_t plane_units, int64_t page_units, int pieces,
+                 const __grid_constant__ PairList<N> list)
 {
     const int2 pr = list.p[blockIdx.x / pieces];
     uint4* plane = pages + blockIdx.y * plane_units;
@@ -67,8 +68,8 @@ int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t
     for (int64_t i = 0; i < n_pairs;) {
         const int64_t left = n_pairs - i;
         const int n = (int)(left < 960 ? left : 960);
-        const int e = n <= 32 ? launch_list<32>(base, n_planes, plane_bytes / 16, page_bytes / 16, pairs + 2 * i, n, st)
-                              : launch_list<960>(base, n_planes, plane_bytes / 16, page_bytes / 16, pairs + 2 * i, n, st);
+        const auto launch = n <= 32 ? launch_list<32> : launch_list<960>;
+        const int e = launch(base, n_planes, plane_bytes / 16, page_bytes / 16, pairs + 2 * i, n, st);
         if (e) return e;
         i += n;
     }

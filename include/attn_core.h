@@ -449,8 +449,9 @@ int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope
  * bytes (it depends on d alone: 21 MB at d = 128), 256-byte aligned, for the
  * partial results of rows whose keys are shared out among thread blocks.  Its
  * contents on entry do not matter; calls (or graph replays) that may overlap on
- * the GPU need one each.  One kernel, and where tiles may be cut a second one
- * that joins their parts.  Nothing is summed in an order that depends on timing:
+ * the GPU need one each.  One kernel, where tiles may be cut a second one that
+ * joins their parts, and where they may be handed out whole a 4-byte memset
+ * before.  Nothing is summed in an order that depends on timing:
  * the same inputs give the same bits on the same device. */
 size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p);
 int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,

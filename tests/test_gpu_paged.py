@@ -51,7 +51,12 @@ CASES = [
 ]
 
 
-@pytest.mark.parametrize("case", CASES, ids=lambda c: f"q{'-'.join(map(str, c[0]))}_k{'-'.join(map(str, c[1]))}_h{c[2]}-{c[3]}_d{c[4]}_p{c[5]}_{'c' if c[6] else 'n'}")
+def _id(c):
+    return "q{}_k{}_h{}-{}_d{}_p{}_{}".format("-".join(map(str, c[0])), "-".join(map(str, c[1])), *c[2:6],
+                                              "c" if c[6] else "n")
+
+
+@pytest.mark.parametrize("case", CASES, ids=_id)
 def test_attention_matches_definition(case):
     nq, nk, hq, hkv, d, ps, causal = case
     p = Paged(nq, nk, hq, hkv, d, ps, seed=len(nq) + d)
