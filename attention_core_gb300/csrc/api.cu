@@ -822,7 +822,7 @@ int rope_call(const attn_core_rope_params* p, const attn_core_rope_table* t, con
     int rc = check_rope_table(t);
     if (rc) return rc;
     if (p == nullptr || p->b <= 0 || p->s < 0 || p->h_q < 0 || p->h_kv < 0 || p->h_q + (int64_t)p->h_kv == 0 ||
-        (int64_t)p->b * p->s >= (int64_t)INT32_MAX)
+        (int64_t)p->b * p->s >= (int64_t)INT32_MAX - kBlockRows)     // tokens, counted in whole blocks
         return ATTN_CORE_ERR_INVALID_ARG;
     if ((p->h_q && (!q || !yq)) || (p->h_kv && (!k || !yk))) return ATTN_CORE_ERR_INVALID_ARG;
     if (p->h_q && ((rc = check_rope_strides(p->q_stride, p->b, p->h_q, p->s, t->d, q == yq)) ||
