@@ -15,8 +15,8 @@
 // out before the angles are formed.  Measured: Q and K of [1, 64 + 8, 8192, 128]
 // 46.2 us (6.5 TB/s, 96% of a plain copy's rate; 54.0 with all heads in one block and
 // loads behind the angles), [2, 12 + 12, 2048, 128] with half of each head 11.8 us,
-// the tiny [1, 2 + 2, 128, 64] 2.4 us, all in a graph; as single calls the last two
-// take the host's 15 us.
+// the tiny [1, 2 + 2, 128, 64] 2.4 us, all in a graph; single calls of the last one
+// take the host's 12 us.
 #include "kernels.h"
 #include "ptx.cuh"
 
