@@ -247,19 +247,21 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 // Which split (paged_sched.cuh) a batch gets: `tiles` tiles of `units` blocks in all,
 // in `heads` pairs of a sequence and a KV head, over `ctas` CTAs.  Whole tiles want
-// enough of them to go round (fewer than 1.4 a CTA leave CTAs without work) and
-// several per KV head (or they bring nothing).  Then they win while they are few, by
-// the parts that need no join, and beyond that where the keys do not fit L2 and
-// would be read again for each row tile.  Measured, cut shares against whole tiles:
+// enough of them to go round (fewer than 1.4 a CTA leave CTAs without work), several
+// per KV head (or they bring nothing).  Then they win while they are few, by the parts
+// that need no join, and beyond that where the keys do not fit L2 and would be read
+// again for each row tile.  Measured, cut shares against whole tiles:
 //   336 tiles, 174 MB of keys and values, d = 160      88 -> 66 us
 //   512 tiles, 262 MB                                 171 -> 113
-//   536 tiles, 356 MB, 8 heads a KV head              210 -> 141
-//   272 tiles, 40 MB                                   32 -> 30
+//   536 tiles, 356 MB, 8 heads a KV head              211 -> 143
+//   296 tiles, 87 MB, d = 160                          70 -> 64
 //   256 tiles, 17 MB, one sequence                     39 -> 39
+// and with the counter set on both sides (the launcher leaves it out where these sizes
+// cannot gain):
+//   272 tiles of 5 blocks, 40 MB                       33 -> 29
 //   1024 tiles, 34 MB                                 309 -> 313
 //   512 tiles of 2.5 blocks, 33 MB                     27 -> 29
 //   256 tiles, one per head, 333 MB                    67 -> 73
-// (the last three with the counter set on both sides, tiles in the sequences' order).
 constexpr int64_t kManyBytes = 100000000;
 __device__ __forceinline__ bool hand_out_tiles(int64_t units, int64_t tiles, int64_t heads, int64_t ctas, int d)
 {
@@ -446,12 +448,13 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         auto group32 = [&](int s) {
             const SeqTable q = s + (int)lane < t.n_seq ? read_seq(t, s + (int)lane, a.tpt, a.causal) : SeqTable{};
             const int tiles = q.s.nq > 0 ? q.s.tiles() : 0;
-            int rank = 0, from = 0;
-            for (int i = 0; i < 32; ++i) {
+            const int n = t.n_seq - s < 32 ? t.n_seq - s : 32;
+            int rank = 0, from = (int)lane;
+            for (int i = 0; i < n; ++i) {
                 const int kv = __shfl_sync(0xffffffffu, q.s.kv, i);
                 rank += kv > q.s.kv || (kv == q.s.kv && i < (int)lane);
             }
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < n; ++i)
                 if (__shfl_sync(0xffffffffu, rank, i) == (int)lane) from = i;
             seq32 = s + from;
             tiles32 = __shfl_sync(0xffffffffu, tiles, from);
@@ -462,7 +465,11 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if ((int)lane >= o) upto32 += x;
             }
         };
-        if (hand_out) group32(0);
+        uint32_t ticket = 0;                 // lane 0's; the first while the group is read
+        if (hand_out) {
+            if (lane == 0) ticket = atomicAdd(a.counter, 1u);
+            group32(0);
+        }
         for (int n = 0; ok && more; ++n) {
             ok = wait_w(wc, bar(bars->job_empty[jr.slot]), jr.phase ^ 1, timeout_code(kSiteJobEmpty));
             if (ok && hand_out && n > 0)
@@ -470,9 +477,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             if (!ok) break;
             Segment g;
             if (hand_out) {
-                int64_t i = 0;
-                if (lane == 0) i = atomicAdd(a.counter, 1u);
-                i = __shfl_sync(0xffffffffu, i, 0);
+                if (lane == 0 && n > 0) ticket = atomicAdd(a.counter, 1u);
+                const int64_t i = __shfl_sync(0xffffffffu, ticket, 0);
                 more = i < (all_tiles >> 32);
                 while (more && i >= base + __shfl_sync(0xffffffffu, upto32, 31)) {
                     base += __shfl_sync(0xffffffffu, upto32, 31);
@@ -1062,12 +1068,13 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
     int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
     if (want < grid) grid = want;
     // The kernel may hand out tiles where hand_out_tiles() could say so of any lengths
-    // that these sizes allow, and sequences have half a tile's new tokens on average, not
-    // one or two.  The counter starts at 0; setting it costs 3 to 7 us, so other batches
-    // do without.
+    // that these sizes allow, tiles may be longer than the 8 blocks up to which many stay
+    // whole anyway (272 tiles of 5 blocks: 28 us so), and sequences have half a tile's new
+    // tokens on average, not one or two.  The counter starts at 0; setting it costs 3 to
+    // 7 us, so other batches do without.
     const int64_t least = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt * a.t.h_kv;         // tiles
     const int64_t most_bytes = (int64_t)a.t.n_seq * a.t.max_pages * a.t.page_size * a.t.h_kv * (4 * D);
-    if (10 * tiles >= 14 * grid && 2ll * a.t.n_tokens >= (int64_t)a.tpt * a.t.n_seq &&
+    if (blocks > 8 && 10 * tiles >= 14 * grid && 2ll * a.t.n_tokens >= (int64_t)a.tpt * a.t.n_seq &&
         a.t.n_tokens >= 2ll * a.t.n_seq && (2 * least <= 5 * grid || most_bytes > kManyBytes)) {
         a.counter = reinterpret_cast<uint32_t*>(a.ws + ws_counter_offset(D));
         if ((e = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), st)) != cudaSuccess) return (int)e;
