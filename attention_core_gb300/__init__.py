@@ -372,12 +372,35 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _raw_stream(device: int) -> int:
-    """The current stream's handle without the Stream object around it (0.1
-    against 3 us on a Grace host: a short call's time)."""
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+class _Host:
+    """What a short call asks of torch, looked up once: on a Grace host the public
+    ways cost several microseconds of a call's ten.
+
+    device()  the current device
+    stream(d) the current stream's handle, without the Stream object around it
+    empty(size, strides, dtype)  an output on the current device: torch's compiled
+              code allocates through an entry of its own that skips the dispatcher
+              (two outputs and a launch cost 6.4 us with it, 10.6 with torch.empty)
+    """
+
+    def __init__(self):
+        import torch
+        c = torch._C
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.device = getattr(c, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.stream = getattr(c, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        self.empty = getattr(getattr(getattr(c, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or (
+            lambda size, strides, dtype: torch.empty_strided(size, strides, dtype=dtype, device="cuda"))
+
+
+_HOST: list = []
+
+
+def _host() -> _Host:
+    if not _HOST:
+        _HOST.append(_Host())
+    return _HOST[0]
 
 
 def _params_from(q, k, causal, p_drop, seed, offset, scale, **kw) -> Params:
@@ -630,33 +653,13 @@ def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: i
                                               n_pairs, stream or None)
 
 
-def _device() -> int:
-    import torch
-    return torch.cuda.current_device()
-
-
 def _layout(shape) -> tuple:
-    """(sizes, strides) of a contiguous tensor, as _empty takes them."""
+    """(sizes, strides) of a contiguous tensor."""
     out, n = [], 1
     for d in reversed(shape):
         out.append(n)
         n *= max(int(d), 1)
     return tuple(int(d) for d in shape), tuple(reversed(out))
-
-
-_EMPTY: list = []
-
-
-def _empty(layout, dtype):
-    """An output on the current device.  torch's compiled code allocates through
-    an entry of its own that skips the dispatcher; two outputs and a launch cost
-    a Grace host 6.4 us with it and 10.6 us with torch.empty."""
-    if not _EMPTY:
-        import torch
-        guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-        _EMPTY.append(getattr(guards, "_empty_strided_cuda", None) or
-                      (lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda")))
-    return _EMPTY[0](*layout, dtype)
 
 
 def _need(t, name, dtype, shape, device: int) -> None:
@@ -727,8 +730,8 @@ def _rope_params(q, k, out_q, out_k, d):
 
 
 def _rope(what, q, k, table, positions, pos0, out_q, out_k):
-    import torch
-    dev = _device()
+    host = _host()
+    dev = host.device()
     key = (table.d,
            None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()),
            None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
@@ -742,12 +745,12 @@ def _rope(what, q, k, table, positions, pos0, out_q, out_k):
         if len(_ROPE_PARAMS) >= 256:
             _ROPE_PARAMS.clear()
         _ROPE_PARAMS[key] = known
-    known, q_layout, k_layout = known
-    p = _CRopeParams.from_buffer_copy(known)
+    params, q_layout, k_layout = known
+    p = _CRopeParams.from_buffer_copy(params)
     if positions is None:
         p.pos0 = int(pos0)
     else:
-        if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.numel() != p.b * p.s:
+        if positions.dtype != host.i32 or not positions.is_contiguous() or positions.numel() != p.b * p.s:
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor of {p.b * p.s} values")
         if positions.get_device() != dev:
             _on_device(dev, positions)
@@ -755,13 +758,13 @@ def _rope(what, q, k, table, positions, pos0, out_q, out_k):
     xq = xk = yq = yk = 0
     if q is not None:
         if out_q is None:
-            out_q = _empty(q_layout, torch.bfloat16)
+            out_q = host.empty(*q_layout, host.bf16)
         xq, yq = q.data_ptr(), out_q.data_ptr()
     if k is not None:
         if out_k is None:
-            out_k = _empty(k_layout, torch.bfloat16)
+            out_k = host.empty(*k_layout, host.bf16)
         xk, yk = k.data_ptr(), out_k.data_ptr()
-    rc = _FAST[what](ctypes.addressof(p), ctypes.addressof(table), xq, xk, yq, yk, _raw_stream(dev)) if p.s else OK
+    rc = _FAST[what](ctypes.addressof(p), ctypes.addressof(table), xq, xk, yq, yk, host.stream(dev)) if p.s else OK
     if rc != OK:
         raise AttnCoreError(rc, what)
     return out_q, out_k
@@ -843,8 +846,8 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     """Add the new tokens' k and v [n_tokens, h_kv, d] to the cache, rotated by
     ``table`` at their positions (None: as they are), and rotate q
     [n_tokens, h_q, d] (or None).  Returns q's rotation, packed."""
-    import torch
-    dev, bf16 = _device(), torch.bfloat16
+    host = _host()
+    dev, bf16 = host.device(), host.bf16
     # what a layout needs follows from shapes, strides and types alone
     key = (None if q is None else (q.shape, q.stride(), q.dtype), k.shape, k.stride(), k.dtype, v.shape, v.stride(),
            v.dtype)
@@ -860,7 +863,7 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     xq = yq = 0
     if q is not None:
         if out_q is None:
-            out_q = _empty(batch._q_layout, bf16)
+            out_q = host.empty(*batch._q_layout, bf16)
         else:
             _need(out_q, "out_q", bf16, batch._q_shape, dev)
         xq, yq = q.data_ptr(), out_q.data_ptr()
@@ -872,7 +875,7 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     if batch.params.n_tokens:
         rc = _FAST["attn_core_paged_append"](batch._address, 0 if table is None else ctypes.addressof(table), xq,
                                              k.data_ptr(), v.data_ptr(), ctypes.addressof(strides), yq,
-                                             k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev))
+                                             k_pages.data_ptr(), v_pages.data_ptr(), host.stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_append")
     return out_q
@@ -882,25 +885,25 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
     """Attention of the batch's new tokens q [n_tokens, h_q, d] over the cache
     (which already holds their keys and values).  Returns (O like q, LSE fp32
     [h_q, n_tokens])."""
-    import torch
-    dev, bf16 = _device(), torch.bfloat16
+    host = _host()
+    dev, bf16 = host.device(), host.bf16
     _need(q, "q", bf16, batch._q_shape, dev)
     _need(k_pages, "k_pages", bf16, batch._page_shape, dev)
     _need(v_pages, "v_pages", bf16, batch._page_shape, dev)
     if out is None:
-        out = _empty(batch._q_layout, bf16)
+        out = host.empty(*batch._q_layout, bf16)
     else:
         _need(out, "out", bf16, batch._q_shape, dev)
     if lse is None:
-        lse = _empty(batch._lse_layout, torch.float32)
+        lse = host.empty(*batch._lse_layout, host.f32)
     else:
-        _need(lse, "lse", torch.float32, batch._lse_shape, dev)
+        _need(lse, "lse", host.f32, batch._lse_shape, dev)
     if batch.workspace.get_device() != dev:
         _on_device(dev, batch.workspace)
     if batch.params.n_tokens:
         ws, ws_bytes = batch._ws
         rc = _FAST["attn_core_paged_fwd"](batch._address, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev))
+                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, host.stream(dev))
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_fwd")
     return out, lse
@@ -931,7 +934,8 @@ def page_copy(pages, pairs) -> None:
         arr = np.ascontiguousarray(wide, dtype=np.int32)
         if not np.array_equal(arr, wide):
             raise ValueError("pairs must fit 32 bits")
-    dev = _device()
+    host = _host()
+    dev = host.device()
     _on_device(dev, pages)
     shape = pages.shape
     planes, n_pages = (shape[0] if len(shape) == 5 else 1), shape[-4]
@@ -942,6 +946,6 @@ def page_copy(pages, pairs) -> None:
     page_bytes = shape[-3] * shape[-2] * shape[-1] * pages.element_size()
     load_library()
     rc = _FAST["attn_core_page_copy"](pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes,
-                                      arr.ctypes.data, len(arr) if arr.size else 0, _raw_stream(dev))
+                                      arr.ctypes.data, len(arr) if arr.size else 0, host.stream(dev))
     if rc != OK:
         raise AttnCoreError(rc, "attn_core_page_copy")

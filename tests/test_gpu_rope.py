@@ -178,7 +178,7 @@ def test_outputs_without_the_short_allocation_path(monkeypatch):
     x = _randn(2, 3, 10, 64)
     t = ac.rope_table(64)
     want = ac.rope_fwd(x, None, t)[0]
-    monkeypatch.setattr(ac, "_EMPTY", [])
+    monkeypatch.setattr(ac, "_HOST", [])
     monkeypatch.delattr(torch._C._dynamo.guards, "_empty_strided_cuda", raising=False)
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
     got = ac.rope_fwd(x.transpose(1, 2).contiguous().transpose(1, 2), None, t)[0]
