@@ -778,6 +778,7 @@ static_assert(ac::kStatusTable == ATTN_CORE_ERR_DEVICE_TABLE, "status code");
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586;
+constexpr int kMaxHeads = 65535;    // heads may be shared out over as many rows of blocks
 
 bool positive(double x) { return x > 0.0 && !isinf(x); }
 
@@ -824,6 +825,7 @@ int rope_call(const attn_core_rope_params* p, const attn_core_rope_table* t, con
     if (p == nullptr || p->b <= 0 || p->s < 0 || p->h_q < 0 || p->h_kv < 0 || p->h_q + (int64_t)p->h_kv == 0 ||
         (int64_t)p->b * p->s >= (int64_t)INT32_MAX - kBlockRows)     // tokens, counted in whole blocks
         return ATTN_CORE_ERR_INVALID_ARG;
+    if (p->h_q + (int64_t)p->h_kv > kMaxHeads) return ATTN_CORE_ERR_UNSUPPORTED;
     if ((p->h_q && (!q || !yq)) || (p->h_kv && (!k || !yk))) return ATTN_CORE_ERR_INVALID_ARG;
     if (p->h_q && ((rc = check_rope_strides(p->q_stride, p->b, p->h_q, p->s, t->d, q == yq)) ||
                    (rc = check_rope_strides(p->yq_stride, p->b, p->h_q, p->s, t->d, true))))
@@ -956,7 +958,8 @@ int check_paged(const attn_core_paged_params* p)
     if (p->flags & ~ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) return ATTN_CORE_ERR_INVALID_ARG;
     const int ps = p->page_size;
     if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return ATTN_CORE_ERR_UNSUPPORTED;
-    if (!supported_d(p->d) || p->h_q / p->h_kv > kBlockRows) return ATTN_CORE_ERR_UNSUPPORTED;
+    if (!supported_d(p->d) || p->h_q / p->h_kv > kBlockRows || p->h_q + 2 * (int64_t)p->h_kv > kMaxHeads)
+        return ATTN_CORE_ERR_UNSUPPORTED;
     // row counts that the kernels hold in 32 bits; element offsets are 64-bit
     if ((int64_t)p->n_pages * p->h_kv >= (int64_t)INT32_MAX ||
         (int64_t)p->max_pages * ps >= (int64_t)INT32_MAX - 2 * kBlockRows ||

@@ -25,7 +25,7 @@ namespace ac {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kAhead = 4;   // heads whose loads a thread has in flight
+constexpr int kAhead = 4;   // heads of a thread: the loads that it has in flight
 
 __device__ __forceinline__ uint32_t rot_pair16(uint32_t xa, uint32_t xb, float c0, float s0, float c1, float s1,
                                                uint32_t& yb)
@@ -177,14 +177,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     for (int i = 0; i < kAhead; ++i)
         if (h0 + i * lanes < h1) d[i] = load(h0 + i * lanes);
     un.turn(t, pos, a.sign);
-    for (int h = h0; h < h1; h += kAhead * lanes) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (h + i * lanes < h1) store(h + i * lanes, d[i]);
-            const int next = h + (kAhead + i) * lanes;
-            if (next < h1) d[i] = load(next);
-        }
-    }
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * lanes < h1) store(h0 + i * lanes, d[i]);
 }
 
 // One block: `tile` new tokens and a part of the heads, as rope_kernel's.
@@ -247,14 +242,9 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     for (int i = 0; i < kAhead; ++i)
         if (h0 + i * lanes < h1) x[i] = load(h0 + i * lanes);
     un.turn(t, pos, 1.0f);
-    for (int h = h0; h < h1; h += kAhead * lanes) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (h + i * lanes < h1) store(h + i * lanes, x[i]);
-            const int next = h + (kAhead + i) * lanes;
-            if (next < h1) x[i] = load(next);
-        }
-    }
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * lanes < h1) store(h0 + i * lanes, x[i]);
 }
 
 namespace {
@@ -285,7 +275,6 @@ Split split(int units, int batches, int tokens, int heads, int sms)
     const int64_t by_heads = (heads + kAhead * lanes - 1) / (kAhead * lanes);
     groups = groups > by_heads ? groups : by_heads;
     groups = groups < heads ? groups : heads;
-    groups = groups < 65535 ? groups : 65535;      // the grid's limit in y
     s.heads = (int)((heads + groups - 1) / groups);
     s.grid = dim3((unsigned)x, (unsigned)((heads + s.heads - 1) / s.heads));
     return s;

@@ -368,8 +368,9 @@ int attn_core_rope_init(const attn_core_rope_config* c, attn_core_rope_table* ou
  * tensor), an output's must keep its rows apart.  [b, h, s, d] is
  * {h s d, s d, d}; a packed [tokens, h, d] is b = 1, {0, d, h d}.  Pointers are
  * 16-byte aligned.  An output may be its own input (same pointer and strides);
- * otherwise no output overlaps an input or the other output.  h_q or h_kv may be 0 (its pointers are then
- * ignored); s = 0 does nothing. */
+ * otherwise no output overlaps an input or the other output.  h_q or h_kv may be
+ * 0 (its pointers are then ignored), their sum is at most 65535; s = 0 does
+ * nothing. */
 typedef struct {
     int32_t b, s, h_q, h_kv;
     int64_t q_stride[3], k_stride[3];     /* inputs: batch, head, token */
@@ -417,7 +418,8 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
 typedef struct {
     int32_t n_seq;          /* >= 1 */
     int32_t n_tokens;       /* rows of q and o; 0: nothing to do */
-    int32_t h_q, h_kv, d;   /* h_q % h_kv == 0, h_q / h_kv <= 128, d in {64, 96, 128, 160} */
+    int32_t h_q, h_kv, d;   /* h_q % h_kv == 0, h_q / h_kv <= 128, h_q + 2 h_kv <= 65535,
+                               d in {64, 96, 128, 160} */
     int32_t page_size;      /* 16, 32, 64, 128 or 256 */
     int32_t n_pages;        /* pages in the cache */
     int32_t max_pages;      /* entries per sequence in page_table */

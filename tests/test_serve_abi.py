@@ -88,6 +88,7 @@ def test_rope_refusals(fn):
                dict(q_stride=(-8, 640, 64)), dict(yq_stride=(4 * 640, 640, 0)), dict(yk_stride=(0, 640, 64)),
                dict(yq_stride=(640, 640, 64)), dict(yq_stride=(4 * 640, 632, 64)), dict(yq_stride=(1 << 43, 640, 64))):
         assert rc(_rope(**kw)) == ac.ERR_INVALID_ARG, kw
+    assert rc(_rope(h_q=40000, h_kv=30000)) == ac.ERR_UNSUPPORTED
     for kw in (dict(q_stride=(4 * 640, 641, 64)), dict(yk_stride=(2 * 640, 640, 68)), dict(positions=FAKE + 2)):
         assert rc(_rope(**kw)) == ac.ERR_MISALIGNED, kw
     assert rc(_rope(), (q + 2, k, yq, yk)) == ac.ERR_MISALIGNED
@@ -117,7 +118,8 @@ PAGED_INVALID = [dict(n_seq=0), dict(n_tokens=-1), dict(h_q=0), dict(h_q=3), dic
                  dict(max_pages=0), dict(causal=2), dict(scale=math.nan), dict(scale=math.inf), dict(cu_seqlens_q=None),
                  dict(kv_lens=None), dict(page_table=None), dict(n_pages=1 << 30, h_kv=4),
                  dict(max_pages=1 << 28), dict(n_tokens=1 << 30), dict(flags=1)]
-PAGED_UNSUPPORTED = [dict(d=72), dict(max_pages=1 << 20, n_tokens=1 << 29, h_q=1, h_kv=1, page_size=256), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(h_q=258, h_kv=2)]
+PAGED_UNSUPPORTED = [dict(d=72), dict(max_pages=1 << 20, n_tokens=1 << 29, h_q=1, h_kv=1, page_size=256), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(h_q=258, h_kv=2),
+                     dict(h_q=30000, h_kv=30000)]
 
 
 def test_paged_refusals():
