@@ -13,8 +13,8 @@
 // tile is M = 128 in both: with 8 live rows the padded products still take less
 // time than the block's 64 KB take to arrive at one SM's share of HBM (about 2700
 // cycles), and warps without a live row skip the softmax.  Measured on one GB300:
-//   one new token, 64/8 heads of 128, one sequence of 131072 keys   87 us (6.1 TB/s)
-//   the same for 64 sequences of up to 8192 keys                   200 us (6.6 TB/s)
+//   one new token, 64/8 heads of 128, one sequence of 131072 keys   89 us (6.0 TB/s)
+//   the same for 64 sequences of up to 8192 keys                   206 us (6.4 TB/s)
 //   2048 new tokens over 8192 keys, 64/8 heads of 128              337 us in a loop,
 //                              300 us before the power limit (1.43 / 1.6 PFLOP/s)
 //   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160   66 us
@@ -35,8 +35,8 @@
 //           accumulator, merged at the tile's end; for d = 160 TMEM has room
 //           for one accumulator and the halves exchange their block maxima
 // Probabilities are rounded to bf16 for the product (the row sum is taken
-// before), everything else is fp32; the running maximum moves only when it
-// grows by more than 2^8.
+// before; tiles of few rows carry the remainder along, kFineRows), everything else
+// is fp32; the running maximum moves only when it grows by more than 2^8.
 //
 // A whole tile's rows go to O; a cut tile's parts go to the workspace as fp32
 // rows divided by their own sum, with their own base-2 LSE, and a second kernel
@@ -54,6 +54,13 @@ namespace ac {
 
 namespace {
 
+// Tiles of at most this many rows are bound by their keys' bytes, with the tensor core
+// idle most of the time.  In batches of such tiles (single tokens) P goes in as two bf16
+// terms, the rounded value and what the rounding left, so that only O's own rounding is
+// left of the error: 1.7e-3 in the 2-norm, against 2.3e-3 with P rounded.  Measured: 64
+// sequences to 8192 keys 200 -> 206 us, one of 131072 keys 87 -> 89.  A kernel of its
+// own: the choice inside the loop cost the others 3 to 4%.
+constexpr int kFineRows = 32;
 constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
 
 // Layout of a [128 x D] tile of Q, K or V: column chunks of 64 with the 128-byte
@@ -282,6 +289,7 @@ __device__ __forceinline__ bool next_job(PagedBars* bars, const WaitCtx& wc, Rin
         g.seq = uniform(s.seq);
         g.head = uniform(s.head);
         g.q_tok = uniform(s.q_tok);
+        g.n_tok = uniform(s.n_tok);
         g.kv = uniform(s.kv);
         g.j0 = uniform(s.j0);
         g.j1 = uniform(s.j1);
@@ -305,7 +313,8 @@ __device__ __forceinline__ bool next_work(PagedBars* bars, const WaitCtx& wc, Ri
 
 }  // namespace
 
-template <int D>
+// FINE: tiles of at most kFineRows rows carry P in two terms.
+template <int D, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 {
@@ -618,6 +627,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         uint32_t o_phase = 1;       // o_free: the first tile finds O free
         bool pending = false;       // a block has its S but not its P.V
         bool first = false;         // it is its tile's first
+        bool fine = false;          // its tile's P comes in two terms (kFineRows)
         auto issue_pv = [&]() -> bool {
             if (first) {
                 if (!wait_w(wc, bar(bars->o_free), o_phase, timeout_code(kSiteOFree))) return false;
@@ -641,6 +651,17 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     mma_ts(tO, tA, P::desc_wide(vbase, kk), IDO, fresh ? more : 1u);
                     if constexpr (P::NARROW)
                         mma_ts(tO + P::WIDE * 64, tA, P::desc_narrow(vbase, kk), IDN, fresh ? more : 1u);
+                }
+                if (FINE && fine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = 4 * (i / 2) + 2 * part + (i & 1);
+                        const uint32_t tO = tmem + (C::SPLIT && kk >= 4 ? C::T_O1 : C::T_O);
+                        const uint32_t tA = tP + split_a_col(kk, 128) + 32;
+                        mma_ts(tO, tA, P::desc_wide(vbase, kk), IDO, 1u);
+                        if constexpr (P::NARROW)
+                            mma_ts(tO + P::WIDE * 64, tA, P::desc_narrow(vbase, kk), IDN, 1u);
+                    }
                 }
             }
             mma_commit(bar(bars->pv_done[rv.slot]));
@@ -686,6 +707,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if (pending) ok = issue_pv();
                 pending = true;
                 first = j == g.j0;
+                fine = FINE && g.n_tok * group <= kFineRows;
             }
             if (!ok) break;
             qr.advance();
@@ -832,6 +854,18 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                         pw[e] = pack_bf16x2(lo, hi);
                     }
                     tmem_st16(tS + 16 * part, pw);
+                    if (FINE && g.n_tok * group <= kFineRows) {
+                        // what the rounding left, into the half's other 32 columns (p formed
+                        // again, which costs the other tiles no registers)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float lo, hi;
+                            f2_unpack(f2_fma(f2_pack(x[32 * part + 2 * e], x[32 * part + 2 * e + 1]), sc2, nm2), lo, hi);
+                            pw[e] = pack_bf16x2(ex2_approx(lo) - __uint_as_float(pw[e] << 16),
+                                                ex2_approx(hi) - __uint_as_float(pw[e] & 0xffff0000u));
+                        }
+                        tmem_st16(tS + 32 + 16 * part, pw);
+                    }
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(bar(bars->p_full[part][bs.slot]));
@@ -1056,7 +1090,9 @@ template <int D>
 int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
 {
     constexpr uint32_t smem = PagedCfg<D>::SMEM;
-    auto kern = paged_attn_kernel<D>;
+    // new tokens that make tiles of few rows, on average
+    const bool fine = (int64_t)args.t.n_tokens * args.group <= (int64_t)kFineRows * args.t.n_seq;
+    auto kern = fine ? paged_attn_kernel<D, true> : paged_attn_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return (int)e;
     // The most units that the tables can ask for bounds the grid (short batches

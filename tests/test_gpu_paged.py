@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import attention_core_gb300 as ac
-from tests.serve_ref import ORIGINAL, Paged, attend, check_attention, rope_tolerance, rotate
+from tests.serve_ref import BF16, ORIGINAL, Paged, attend, check_attention, rope_tolerance, rotate
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -62,6 +62,34 @@ def test_attention_matches_definition(case):
     p = Paged(nq, nk, hq, hkv, d, ps, seed=len(nq) + d)
     o, lse = _run(p, causal=causal)
     check_attention(o, lse, attend(p, causal), p)
+
+
+def _with_rounded_probabilities(p):
+    """O in 64 bits but for the probabilities, rounded to bf16 relative to their row's largest."""
+    o = torch.zeros(p.q.shape, dtype=torch.float64, device=p.q.device)
+    for i, m in enumerate(p.nk):
+        rows = slice(p.cu_host[i], p.cu_host[i + 1])
+        k, v = (x[i].double().repeat_interleave(p.h_q // p.h_kv, 1) for x in (p.keys, p.values))
+        x = torch.einsum("qhd,khd->hqk", p.q[rows].double(), k) / math.sqrt(p.d)
+        w = torch.exp(x - x.amax(-1, keepdim=True))
+        o[rows] = torch.einsum("hqk,khd->qhd", w.to(torch.bfloat16).double(), v) / w.sum(-1).t()[..., None]
+    return o
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 32, 1), (96, 6, 2), (128, 8, 1), (160, 4, 4)])
+def test_single_tokens_round_only_the_result(d, hq, hkv):
+    """Batches of single tokens: the probabilities keep two bf16 terms, so what the
+    second rounding leaves is 2^-16 of each (2^-15 here, a probability's fp32
+    exponential included) and only O's own rounding remains.  Few keys, so that
+    rounded probabilities' errors do not average out; those would be seen."""
+    nk = [3 + i % 9 for i in range(40)]
+    p = Paged([1] * len(nk), nk, hq, hkv, d, 16, seed=d)
+    ro, _, size = attend(p)
+    tol = BF16 * ro.abs() + (2.0 ** -12 + 2.0 ** -15) * size
+    assert ((_with_rounded_probabilities(p) - ro).abs() > 2 * tol).any()
+    o, _ = _run(p)
+    err = (o.double() - ro).abs()
+    assert (err <= tol).all(), float((err - tol).max())
 
 
 @pytest.mark.parametrize("d", [64, 96, 128, 160])
