@@ -804,7 +804,10 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     mx = fmaxf(mx, __uint_as_float(tmem_ld1(tX + bs.slot * 2 + (h ^ 1))));
                 }
                 const float m_new = fmaxf(m_run, mx * a.scale_log2);
-                if (__any_sync(0xffffffffu, m_new > m_run + 8.0f)) {
+                // Only rows that are used have a say: the others' queries are the next
+                // tokens', or what shared memory held before, and must not decide where
+                // this tile's maxima move (which its roundings follow).
+                if (__any_sync(0xffffffffu, live && m_new > m_run + 8.0f)) {
                     if (j > 0) {
                         // the accumulator's last P.V (block j - 1) must be done
                         ok = wait_warp(wc, bar(bars->pv_done[before.slot]), before.phase, timeout_code(kSitePvDone));

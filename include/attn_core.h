@@ -407,7 +407,10 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
  *
  * Probabilities are rounded to bf16 for their product with the values, in
  * batches of at most 32 rows (new tokens times group) a sequence on average to
- * two bf16 terms, so the last bits of a sequence's O depend on its batch.
+ * two bf16 terms; and where a sequence's keys are cut into the parts that are
+ * joined goes by the lengths of the whole batch.  So the last bits of a
+ * sequence's O depend on the sizes and lengths of its batch, but never on the
+ * other sequences' values, nor on what ran before.
  *
  * The three tables are in device memory and read by the kernels only, so a
  * captured graph follows them: one capture serves every step as long as the

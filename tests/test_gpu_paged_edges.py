@@ -1,0 +1,62 @@
+"""The paged cache's operators at their edges: results that depend on nothing but
+their inputs, lengths and pages; tables that are out of order; NaN among the
+keys; who owns the workspace, and for how long."""
+import math
+
+import pytest
+import torch
+
+import attention_core_gb300 as ac
+from tests.serve_ref import Paged, attend, check_attention
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+# (new tokens a sequence, sequences, h_q, h_kv, d): head groups that leave rows of a
+# tile unused (3: 126 rows of 128, 5: 125, 6: 126, 7: 126, 100: 100)
+LEFT_OVER = [(42, 20, 24, 8, 128), (25, 40, 20, 4, 96), (21, 20, 48, 8, 160), (18, 40, 28, 4, 64), (8, 20, 100, 1, 128)]
+
+
+@pytest.mark.parametrize("case", LEFT_OVER, ids=lambda c: "g{}_d{}".format(c[2] // c[3], c[4]))
+def test_bits_do_not_depend_on_what_ran_before(case):
+    """Rows of a tile that no head uses hold what an earlier kernel left in shared
+    memory: a launch whose tiles are full, of large values or of zeros, changes no
+    bit of the next launch's results."""
+    n, n_seq, hq, hkv, d = case
+    p = Paged([n] * n_seq, [1024] * n_seq, hq, hkv, d, 64, seed=40 + d)
+    full = Paged([128] * 20, [256] * 20, 8, 8, d, 64, seed=41)       # one head a KV head: every row of a tile
+    b, before = p.batch(), full.batch()
+    results = []
+    for scale in (0.0, 30.0, 0.0, 200.0):
+        q = (full.q.float() * scale).to(torch.bfloat16)
+        ac.paged_fwd(before, q, full.k_pages, full.v_pages)
+        results.append(ac.paged_fwd(b, p.q, p.k_pages, p.v_pages))
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    check_attention(*results[0], attend(p), p)
+    for o, lse in results[1:]:
+        assert torch.equal(o, results[0][0]) and torch.equal(lse, results[0][1])
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(1, 8, 1, 128), (5, 8, 1, 128), (1, 4, 2, 160), (9, 3, 1, 64), (1, 1, 1, 96)])
+def test_bits_do_not_depend_on_the_neighbours_queries(n, hq, hkv, d):
+    """Rows of a tile behind a sequence's last new token hold the next sequences'
+    queries: other queries there change no bit of this one's results."""
+    n_seq = 160 // hkv
+    p = Paged([n] * n_seq, [1024] * n_seq, hq, hkv, d, 64, seed=42 + d)
+    b = p.batch()
+    o, lse = ac.paged_fwd(b, p.q, p.k_pages, p.v_pages)
+    q = p.q.view(n_seq, n, hq, d).clone()
+    q[1::2] = (q[1::2].float() * 30).to(torch.bfloat16)
+    o2, lse2 = ac.paged_fwd(b, q.view_as(p.q), p.k_pages, p.v_pages)
+    torch.cuda.synchronize()
+    check_attention(o, lse, attend(p), p)
+    assert torch.equal(o2.view_as(q)[::2], o.view_as(q)[::2])
+    assert torch.equal(lse2.view(hq, n_seq, n)[:, ::2], lse.view(hq, n_seq, n)[:, ::2])
