@@ -881,7 +881,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             }
             if (!ok) break;
             // Final row statistics: O = a0 O_0 + a1 O_1 (SPLIT), O = a0 O (else); a
-            // row that saw no key has l = 0 and gets zeros.
+            // row that saw no key has l = 0 and gets zeros.  (Compared with 0: the sum of
+            // a row that saw a NaN score is NaN, and has to reach O and the LSE.)
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
             // a full tile's O leaves through the stage: free once its last store has read it
             const bool staged = C::STAGE_O && g.whole && g.n_tok == a.tpt;
@@ -897,10 +898,10 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     const float m_ref = (m == -INFINITY) ? 0.f : m;
                     const float f0 = ex2_approx(m_run - m_ref), f1 = ex2_approx(o1.x - m_ref);
                     const float l_tot = l_run * f0 + o1.y * f1;
-                    const float inv = l_tot > 0.f ? 1.0f / l_tot : 0.f;
+                    const float inv = l_tot == 0.f ? 0.f : 1.0f / l_tot;
                     a0 = f0 * inv;
                     a1 = f1 * inv;
-                    lse2 = l_tot > 0.f ? m_ref + log2f(l_tot) : -INFINITY;
+                    lse2 = l_tot == 0.f ? -INFINITY : m_ref + log2f(l_tot);
                     xch[r] = make_float2(a0, a1);
                 }
                 mbar_arrive(bar(bars->lsum2));
@@ -920,8 +921,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if (!ok) break;
                 tc_fence_after();
                 const float l_tot = l_run + __uint_as_float(tmem_ld1(tX + 4 + (h ^ 1)));
-                a0 = l_tot > 0.f ? 1.0f / l_tot : 0.f;
-                lse2 = l_tot > 0.f ? m_run + log2f(l_tot) : -INFINITY;
+                a0 = l_tot == 0.f ? 0.f : 1.0f / l_tot;
+                lse2 = l_tot == 0.f ? -INFINITY : m_run + log2f(l_tot);
             }
             ok = wait_warp(wc, bar(bars->pv_done[before.slot]), before.phase, timeout_code(kSitePvDone));
             if (!ok) break;
@@ -1074,13 +1075,13 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
             }
         }
     }
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;       // NaN stays
     const int tok = cut.q_tok + r / a.group, head = cut.head * a.group + r % a.group;
     uint16_t* orow = a.o + ((size_t)tok * t.h_q + head) * D + lane;
 #pragma unroll
     for (int e = 0; e < E; ++e) orow[e * 32] = (uint16_t)(pack_bf16x2(acc[e] * inv, 0.f) & 0xffffu);
     if (lane == 0)
-        a.lse[(size_t)head * t.n_tokens + tok] = sum > 0.f ? (m + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+        a.lse[(size_t)head * t.n_tokens + tok] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
 }
 
 size_t paged_ws_bytes(int d) { return ws_counter_offset(d) + 256; }

@@ -403,7 +403,8 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
  * used, NaN included, nor are page_table entries past its last page.  (Within
  * a sequence a probability of 0 still meets its value in the product: an
  * infinite or NaN value of one key reaches rows of the same sequence that the
- * mask keeps from seeing it; rows that do see it are infinite or NaN.)
+ * mask keeps from seeing it; rows that do see it are infinite or NaN.  A NaN
+ * score makes its row's O and LSE NaN.)
  *
  * Probabilities are rounded to bf16 for their product with the values, in
  * batches of at most 32 rows (new tokens times group) a sequence on average to

@@ -60,3 +60,26 @@ def test_bits_do_not_depend_on_the_neighbours_queries(n, hq, hkv, d):
     check_attention(o, lse, attend(p), p)
     assert torch.equal(o2.view_as(q)[::2], o.view_as(q)[::2])
     assert torch.equal(lse2.view(hq, n_seq, n)[:, ::2], lse.view(hq, n_seq, n)[:, ::2])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 1, 128), (3, 1, 96), (2, 2, 160)])
+@pytest.mark.parametrize("nq,nk,at", [([1, 1], [300, 30], 7), ([1, 1], [30011, 40], 17000), ([9, 2], [500, 20], 494),
+                                      ([200, 3], [2000, 50], 1900), ([1, 1], [1, 5], 0)])
+def test_rows_that_see_a_nan_key_say_so(nq, nk, at, hq, hkv, d):
+    """One key of the first sequence is NaN: O and LSE of the rows that see it are
+    NaN (an LSE of -inf would say that they see no key), and those of the other
+    rows, which the mask keeps from it, are the definition's."""
+    p = Paged(nq, nk, hq, hkv, d, 32, seed=43 + d)
+    page, row = p.places(0, torch.tensor([at], device=DEV))
+    p.k_pages[page, :, row] = math.nan
+    o, lse = ac.paged_fwd(p.batch(), p.q, p.k_pages, p.v_pages)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    sees = torch.zeros(p.n_tokens, dtype=torch.bool, device=DEV)
+    sees[:nq[0]] = nk[0] - nq[0] + torch.arange(nq[0], device=DEV) >= at
+    assert sees.any()
+    assert torch.isnan(o[sees]).all() and torch.isnan(lse[:, sees]).all()
+    ro, rlse, size = attend(p)             # of the keys as they were
+    rest = ~sees
+    assert ((o[rest].double() - ro[rest]).abs() <= 2.0 ** -8 * (ro[rest].abs() + size[rest]) + 2.0 ** -12 * size[rest]).all()
+    assert ((lse[:, rest].double() - rlse[:, rest]).abs() <= 2.0 ** -12).all()
