@@ -195,18 +195,23 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     const int tok = tok0 + slot / units;
     // the sequence of the tile's first token: the last one that starts at or before it
     int seq = -1;
+    bool outside = false, falls = false;
     for (int i0 = 0; i0 <= pt.n_seq; i0 += kRopeThreads) {
         const int i = i0 + threadIdx.x;
-        seq += __syncthreads_count(i <= pt.n_seq && pt.cu_q[i] <= tok0);
+        const bool here = i <= pt.n_seq;
+        const int start = here ? pt.cu_q[i] : 0;
+        if (here) outside |= start < 0 || start > pt.n_tokens;
+        if (i < pt.n_seq) falls |= pt.cu_q[i + 1] < start;
+        seq += __syncthreads_count(here && start <= tok0);
     }
+    if ((outside || falls) && pt.status) atomicCAS(pt.status, 0, kStatusTable);
+    // starts that decrease: which sequence owns a token (and the page row) is not known
+    if (__syncthreads_or(falls)) return;
     if (lane >= lanes || tok >= pt.n_tokens) return;
     while (seq >= 0 && seq < pt.n_seq && pt.cu_q[seq + 1] <= tok) ++seq;
     if (seq < 0 || seq >= pt.n_seq) return;           // behind the last sequence: not ours
     const int q0 = pt.cu_q[seq], q1 = pt.cu_q[seq + 1], kv = pt.kv_lens[seq];
-    if (q0 < 0 || tok < q0 || q1 > pt.n_tokens) {     // not a table of increasing starts
-        if (pt.status) atomicCAS(pt.status, 0, kStatusTable);
-        return;
-    }
+    if (q0 < 0 || q1 > pt.n_tokens) return;           // reported above
     const int64_t pos = (int64_t)kv - q1 + tok;
     int page = -1;
     if (pos >= 0 && kv <= (int64_t)pt.max_pages * pt.page_size)

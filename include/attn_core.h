@@ -415,11 +415,12 @@ int attn_core_rope_bwd(const attn_core_rope_params* p, const attn_core_rope_tabl
  *
  * The three tables are in device memory and read by the kernels only, so a
  * captured graph follows them: one capture serves every step as long as the
- * sizes in this struct stay.  The kernels check them: an entry out of range (a
- * page outside the cache, lengths that are negative, decrease or exceed
- * n_tokens or max_pages * page_size) writes ATTN_CORE_ERR_DEVICE_TABLE to
- * dev_status, touches nothing outside the tensors, and leaves that sequence's
- * results undefined.
+ * sizes in this struct stay.  Each kernel checks the entries that it uses: one
+ * out of range (a page outside the cache, lengths that are negative or exceed
+ * max_pages * page_size, starts that are negative, decrease or exceed n_tokens)
+ * writes ATTN_CORE_ERR_DEVICE_TABLE to dev_status, touches nothing outside the
+ * tensors, and leaves that sequence's results undefined.  Starts that decrease
+ * leave every sequence's results undefined; the append then writes nothing.
  *
  * One limit on sizes: ceil(n_tokens / floor(128 / group)) * ceil(max_pages *
  * page_size / 128) < 2^31, group = h_q / h_kv (ATTN_CORE_ERR_UNSUPPORTED). */
@@ -448,7 +449,10 @@ typedef struct {
  * -- slices of a fused [tokens, (h_q + 2 h_kv) d] projection qualify.  q and
  * q_out may both be NULL (only the cache is written), and q_out may be q if q
  * is packed.  No two new tokens may share a cache row (a page that two
- * sequences share is copied before either appends to it).  One kernel. */
+ * sequences share is copied before either appends to it).  kv_lens[i] counts
+ * the new tokens: where it is smaller than their number (which the attention
+ * takes, for rows that see no key), the tokens before position 0 have no place
+ * in the cache and are a table error.  One kernel. */
 int attn_core_paged_append(const attn_core_paged_params* p, const attn_core_rope_table* t, const void* q,
                            const void* k, const void* v, const int64_t* strides, void* q_out, void* k_pages,
                            void* v_pages, void* stream);

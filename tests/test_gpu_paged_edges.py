@@ -83,3 +83,59 @@ def test_rows_that_see_a_nan_key_say_so(nq, nk, at, hq, hkv, d):
     rest = ~sees
     assert ((o[rest].double() - ro[rest]).abs() <= 2.0 ** -8 * (ro[rest].abs() + size[rest]) + 2.0 ** -12 * size[rest]).all()
     assert ((lse[:, rest].double() - rlse[:, rest]).abs() <= 2.0 ** -12).all()
+
+
+def _append_status(p, **kw):
+    k0, v0 = p.k_pages.clone(), p.v_pages.clone()
+    ac.paged_append(p.batch(**kw), p.q, p.k_new, p.v_new, p.k_pages, p.v_pages, table=ac.rope_table(p.d))
+    torch.cuda.synchronize()
+    code = int(p.status.item()) & 0xff
+    p.status.zero_()
+    same = torch.equal(k0.view(torch.int16), p.k_pages.view(torch.int16)) and \
+        torch.equal(v0.view(torch.int16), p.v_pages.view(torch.int16))
+    p.k_pages.copy_(k0), p.v_pages.copy_(v0)
+    return code, same
+
+
+def test_append_reports_starts_out_of_order():
+    """Starts that decrease leave no sequence that owns the tokens between: nothing
+    is written, and the status word says so."""
+    for cu in ([0, 5, 3, 9], [0, 3, 9, 5], [4, 0, 6, 9], [0, 9, 0, 9], [0, -3, 4, 9]):
+        p = Paged([5, 1, 3], [40, 33, 60], 4, 2, 64, 16, seed=44)
+        assert _append_status(p) == (0, False)
+        p.cu.copy_(torch.tensor(cu, dtype=torch.int32, device=DEV))
+        assert _append_status(p) == (ac.ERR_DEVICE_TABLE, True), cu
+    many = 700                                        # more starts than a block has threads
+    p = Paged([1] * many, [20] * many, 2, 1, 64, 16, seed=45)
+    assert _append_status(p) == (0, False)
+    p.cu[600] = 400
+    assert _append_status(p) == (ac.ERR_DEVICE_TABLE, True)
+
+
+def test_append_reports_every_bad_table():
+    def fresh():
+        return Paged([2, 3], [40, 60], 4, 2, 64, 16, seed=46)
+    p = fresh()
+    p.table[0, 38 // 16] = p.n_pages
+    assert _append_status(p)[0] == ac.ERR_DEVICE_TABLE
+    p = fresh()
+    p.table[0, 38 // 16] = -1
+    assert _append_status(p)[0] == ac.ERR_DEVICE_TABLE
+    for kv in (p.table.shape[1] * p.ps + 1, -5, 1):   # the last: a token before the sequence's start
+        p = fresh()
+        p.kv_lens[0] = kv
+        assert _append_status(p)[0] == ac.ERR_DEVICE_TABLE, kv
+    for cu in ([0, 2, 55], [0, 5, 55], [-2, 2, 5], [0, 6, 6]):
+        p = fresh()
+        p.cu.copy_(torch.tensor(cu, dtype=torch.int32, device=DEV))
+        assert _append_status(p)[0] == ac.ERR_DEVICE_TABLE, cu
+
+
+def test_append_writes_the_sequences_beside_a_bad_one():
+    p = Paged([2, 3], [40, 60], 4, 2, 64, 16, seed=47)
+    p.kv_lens[0] = -5
+    ac.paged_append(p.batch(), p.q, p.k_new, p.v_new, p.k_pages, p.v_pages)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) & 0xff == ac.ERR_DEVICE_TABLE
+    page, row = p.places(1, torch.arange(57, 60, device=DEV))
+    assert torch.equal(p.k_pages[page, :, row], p.k_new[2:]) and torch.equal(p.v_pages[page, :, row], p.v_new[2:])
