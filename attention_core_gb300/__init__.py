@@ -791,7 +791,9 @@ class PagedBatch:
     [n_seq, max_pages] are int32 CUDA tensors, read by the kernels when they
     run: a step's new lengths and pages are copied into them, and a captured
     graph follows.  The batch owns the attention's workspace; calls that may
-    overlap on the GPU need a batch (or a ``workspace``) each."""
+    overlap on the GPU need a batch (or a ``workspace``) each.  It may be dropped
+    right after a call, on whichever stream that was made; a captured graph needs
+    the batch for as long as it is replayed."""
 
     def __init__(self, cu_seqlens_q, kv_lens, page_table, *, n_tokens: int, h_q: int, h_kv: int, d: int,
                  page_size: int, n_pages: int, causal: bool = True, scale: float = 0.0, dev_status: int = 0,
@@ -822,12 +824,23 @@ class PagedBatch:
         self.workspace = workspace
         self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
         self._address = ctypes.addressof(self.params)
+        self._streams = set()   # handles of the streams that calls were made on
         self._strides = {}      # by paged_append's layouts: three token strides
         self._q_shape = torch.Size((int(n_tokens), int(h_q), int(d)))
         self._kv_shape = torch.Size((int(n_tokens), int(h_kv), int(d)))
         self._page_shape = torch.Size((int(n_pages), int(h_kv), int(page_size), int(d)))
         self._lse_shape = torch.Size((int(h_q), int(n_tokens)))
         self._q_layout, self._lse_layout = _layout(self._q_shape), _layout(self._lse_shape)
+
+    def _used_on(self, stream: int) -> None:
+        """The first call on the current stream: the allocator is told of it, so that
+        it does not hand the workspace out again, or tables that only the batch
+        holds, before the calls there have run (5 us, once for each stream)."""
+        import torch
+        current = torch.cuda.current_stream()
+        for t in (self.workspace, *self.tables):
+            t.record_stream(current)
+        self._streams.add(stream)
 
 
 def _token_stride(x, name, shape):
@@ -873,9 +886,12 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
             or batch.workspace.get_device() != dev:
         _on_device(dev, q, k, v, batch.workspace)
     if batch.params.n_tokens:
+        stream = host.stream(dev)
+        if stream not in batch._streams:
+            batch._used_on(stream)
         rc = _FAST["attn_core_paged_append"](batch._address, 0 if table is None else ctypes.addressof(table), xq,
                                              k.data_ptr(), v.data_ptr(), ctypes.addressof(strides), yq,
-                                             k_pages.data_ptr(), v_pages.data_ptr(), host.stream(dev))
+                                             k_pages.data_ptr(), v_pages.data_ptr(), stream)
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_append")
     return out_q
@@ -902,8 +918,11 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
         _on_device(dev, batch.workspace)
     if batch.params.n_tokens:
         ws, ws_bytes = batch._ws
+        stream = host.stream(dev)
+        if stream not in batch._streams:
+            batch._used_on(stream)
         rc = _FAST["attn_core_paged_fwd"](batch._address, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, host.stream(dev))
+                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, stream)
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_fwd")
     return out, lse

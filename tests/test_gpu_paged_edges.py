@@ -139,3 +139,30 @@ def test_append_writes_the_sequences_beside_a_bad_one():
     assert int(p.status.item()) & 0xff == ac.ERR_DEVICE_TABLE
     page, row = p.places(1, torch.arange(57, 60, device=DEV))
     assert torch.equal(p.k_pages[page, :, row], p.k_new[2:]) and torch.equal(p.v_pages[page, :, row], p.v_new[2:])
+
+
+def test_batch_dropped_while_its_call_runs():
+    """The workspace and the tables that only the batch holds are not handed out
+    again before a call on another stream has run."""
+    p = Paged([1, 1], [9000, 300], 8, 1, 128, 64, seed=48)
+    want = attend(p)
+    side = torch.cuda.Stream()
+    b = ac.PagedBatch(p.cu.clone(), p.kv_lens.clone(), p.table.clone(), n_tokens=2, h_q=8, h_kv=1, d=128, page_size=64,
+                      n_pages=p.n_pages)
+    mine = [b.workspace.data_ptr()] + [t.data_ptr() for t in b.tables]
+    sizes = [b.workspace.numel()] + [t.numel() for t in b.tables]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1 << 28)                    # about 0.15 s ahead of the call
+        o, lse = ac.paged_fwd(b, p.q, p.k_pages, p.v_pages)
+    del b
+    taken = [torch.empty(sizes[0], dtype=torch.uint8, device=DEV)]
+    taken += [torch.empty(n, dtype=torch.int32, device=DEV) for n in sizes[1:]]
+    assert not side.query()                           # the call is still ahead
+    assert not {t.data_ptr() for t in taken} & set(mine)
+    torch.cuda.synchronize()
+    check_attention(o, lse, want, p)
+    # once the stream is done, its memory is there again
+    del taken
+    again = ac.PagedBatch(p.cu, p.kv_lens, p.table, n_tokens=2, h_q=8, h_kv=1, d=128, page_size=64, n_pages=p.n_pages)
+    check_attention(*ac.paged_fwd(again, p.q, p.k_pages, p.v_pages), want, p)
