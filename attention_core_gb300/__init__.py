@@ -814,23 +814,34 @@ class PagedBatch:
         if need == 0:       # the call itself says what is wrong
             raise AttnCoreError(ERR_UNSUPPORTED if page_size not in PAGE_SIZES or d not in SUPPORTED_HEAD_DIMS
                                 else ERR_INVALID_ARG, "PagedBatch")
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=cu_seqlens_q.device)
-        elif workspace.get_device() != cu_seqlens_q.get_device():
-            raise ValueError(f"workspace must be on {cu_seqlens_q.device}, got {workspace.device}")
         for name, t in (("kv_lens", kv_lens), ("page_table", page_table)):
             if t.device != cu_seqlens_q.device:
                 raise ValueError(f"{name} must be on {cu_seqlens_q.device}, got {t.device}")
-        self.workspace = workspace
-        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        self._address = ctypes.addressof(self.params)
         self._streams = set()   # handles of the streams that calls were made on
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=cu_seqlens_q.device) if workspace is None \
+            else workspace
+        self._address = ctypes.addressof(self.params)
         self._strides = {}      # by paged_append's layouts: three token strides
         self._q_shape = torch.Size((int(n_tokens), int(h_q), int(d)))
         self._kv_shape = torch.Size((int(n_tokens), int(h_kv), int(d)))
         self._page_shape = torch.Size((int(n_pages), int(h_kv), int(page_size), int(d)))
         self._lse_shape = torch.Size((int(h_q), int(n_tokens)))
         self._q_layout, self._lse_layout = _layout(self._q_shape), _layout(self._lse_shape)
+
+    @property
+    def workspace(self):
+        """The attention's device memory; another one takes its place by assignment."""
+        return self._workspace
+
+    @workspace.setter
+    def workspace(self, t) -> None:
+        import torch
+        if not isinstance(t, torch.Tensor) or t.device != self.tables[0].device:
+            raise ValueError(f"workspace must be a tensor on {self.tables[0].device}, got "
+                             f"{t.device if isinstance(t, torch.Tensor) else type(t).__name__}")
+        self._workspace = t
+        self._ws = (t.data_ptr(), t.numel() * t.element_size())
+        self._streams.clear()
 
     def _used_on(self, stream: int) -> None:
         """The first call on the current stream: the allocator is told of it, so that
@@ -883,8 +894,8 @@ def paged_append(batch: PagedBatch, q, k, v, k_pages, v_pages, *, table: RopeTab
     elif out_q is not None:
         raise ValueError("out_q without q")
     if k.get_device() != dev or v.get_device() != dev or (q is not None and q.get_device() != dev) \
-            or batch.workspace.get_device() != dev:
-        _on_device(dev, q, k, v, batch.workspace)
+            or batch._workspace.get_device() != dev:
+        _on_device(dev, q, k, v, batch._workspace)
     if batch.params.n_tokens:
         stream = host.stream(dev)
         if stream not in batch._streams:
@@ -914,8 +925,8 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
         lse = host.empty(*batch._lse_layout, host.f32)
     else:
         _need(lse, "lse", host.f32, batch._lse_shape, dev)
-    if batch.workspace.get_device() != dev:
-        _on_device(dev, batch.workspace)
+    if batch._workspace.get_device() != dev:
+        _on_device(dev, batch._workspace)
     if batch.params.n_tokens:
         ws, ws_bytes = batch._ws
         stream = host.stream(dev)

@@ -166,3 +166,20 @@ def test_batch_dropped_while_its_call_runs():
     del taken
     again = ac.PagedBatch(p.cu, p.kv_lens, p.table, n_tokens=2, h_q=8, h_kv=1, d=128, page_size=64, n_pages=p.n_pages)
     check_attention(*ac.paged_fwd(again, p.q, p.k_pages, p.v_pages), want, p)
+
+
+def test_workspace_replaced():
+    """The workspace in use is the one that the batch shows."""
+    p = Paged([1, 2], [9000, 300], 8, 1, 128, 64, seed=49)
+    b = p.batch()
+    first, other = b.workspace, torch.zeros_like(b.workspace)
+    b.workspace = other
+    first.fill_(7)
+    o, lse = ac.paged_fwd(b, p.q, p.k_pages, p.v_pages)
+    torch.cuda.synchronize()
+    assert (first == 7).all() and (other != 0).any()
+    check_attention(o, lse, attend(p), p)
+    for bad in (torch.empty(first.numel(), dtype=torch.uint8), None):
+        with pytest.raises(ValueError):
+            b.workspace = bad
+    assert b.workspace is other
