@@ -836,9 +836,8 @@ class PagedBatch:
     @workspace.setter
     def workspace(self, t) -> None:
         import torch
-        if not isinstance(t, torch.Tensor) or t.device != self.tables[0].device:
-            raise ValueError(f"workspace must be a tensor on {self.tables[0].device}, got "
-                             f"{t.device if isinstance(t, torch.Tensor) else type(t).__name__}")
+        if not isinstance(t, torch.Tensor) or t.device != self.tables[0].device or not t.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.tables[0].device}")   # its bytes are counted
         self._workspace = t
         self._ws = (t.data_ptr(), t.numel() * t.element_size())
         self._streams.clear()

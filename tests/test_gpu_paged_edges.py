@@ -183,3 +183,13 @@ def test_workspace_replaced():
         with pytest.raises(ValueError):
             b.workspace = bad
     assert b.workspace is other
+
+
+def test_workspace_smaller_than_its_elements_say():
+    """An expanded tensor counts more elements than it has memory."""
+    p = Paged([1], [20], 2, 1, 64, 16)
+    need = p.batch().workspace.numel()
+    with pytest.raises(ValueError):
+        p.batch(workspace=torch.empty(1, dtype=torch.uint8, device=DEV).expand(need))
+    with pytest.raises(ValueError):
+        p.batch(workspace=torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2])
