@@ -610,7 +610,7 @@ def rope_table(d: int, *, rot_dim: int = 0, base: float = 10000.0, interleaved: 
     "bands" or "yarn" (formulas: include/attn_core.h)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}, got {scaling!r}")
-    c = _CRopeConfig(int(d), int(rot_dim), int(bool(interleaved)), ROPE_SCALINGS[scaling], float(base), float(factor),
+    c = _CRopeConfig(_bits32("d", d), _bits32("rot_dim", rot_dim), int(bool(interleaved)), ROPE_SCALINGS[scaling], float(base), float(factor),
                      float(original_len), float(low_freq), float(high_freq), float(beta_fast), float(beta_slow),
                      float(mscale))
     t = RopeTable()
@@ -651,6 +651,14 @@ def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: i
     """pairs: address of host int32 [n_pairs, 2]."""
     return load_library().attn_core_page_copy(pages, n_planes, plane_stride, n_pages, page_bytes, pairs or None,
                                               n_pairs, stream or None)
+
+
+def _bits32(name: str, value, low: int = -2**31, high: int = 2**31 - 1) -> int:
+    """A value for a 32-bit field, which ctypes would cut without a word."""
+    value = int(value)
+    if not low <= value <= high:
+        raise ValueError(f"{name} does not fit 32 bits: {value}")
+    return value
 
 
 def _layout(shape) -> tuple:
@@ -720,16 +728,17 @@ def _rope_params(q, k, out_q, out_k, d):
             raise ValueError(f"out_{name} must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
         else:
             yst = _rope_view(y, "out_" + name, d)[3]
-        setattr(p, "h_" + ("q" if name == "q" else "kv"), h)
+        setattr(p, "h_" + ("q" if name == "q" else "kv"), _bits32(name + "'s heads", h))
         getattr(p, name + "_stride")[:] = st
         getattr(p, "y" + name + "_stride")[:] = yst
     if lead is None:
         raise ValueError("q or k must be given")
-    p.b, p.s = lead[:2]
+    p.b, p.s = _bits32("batch", lead[0]), _bits32("tokens", lead[1])
     return p
 
 
 def _rope(what, q, k, table, positions, pos0, out_q, out_k):
+    pos0 = _bits32("pos0", pos0) if pos0 else 0
     host = _host()
     dev = host.device()
     key = (table.d,
@@ -748,7 +757,7 @@ def _rope(what, q, k, table, positions, pos0, out_q, out_k):
     params, q_layout, k_layout = known
     p = _CRopeParams.from_buffer_copy(params)
     if positions is None:
-        p.pos0 = int(pos0)
+        p.pos0 = pos0
     else:
         if positions.dtype != host.i32 or not positions.is_contiguous() or positions.numel() != p.b * p.s:
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor of {p.b * p.s} values")
@@ -802,14 +811,16 @@ class PagedBatch:
         if page_table.dim() != 2:
             raise ValueError(f"page_table must be [n_seq, max_pages], got {tuple(page_table.shape)}")
         n_seq, max_pages = page_table.shape
+        sizes = [_bits32(name, v) for name, v in
+                 (("n_seq", n_seq), ("n_tokens", n_tokens), ("h_q", h_q), ("h_kv", h_kv), ("d", d),
+                  ("page_size", page_size), ("n_pages", n_pages), ("max_pages", max_pages))]
+        flags, wait = _bits32("flags", flags), _bits32("wait_timeout_ms", wait_timeout_ms, 0, 2**32 - 1)
         _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n_seq + 1,))
         _check(kv_lens, "kv_lens", torch.int32, (n_seq,))
         _check(page_table, "page_table", torch.int32, (n_seq, max_pages))
         self.tables = (cu_seqlens_q, kv_lens, page_table)
-        self.params = _CPagedParams(n_seq, int(n_tokens), int(h_q), int(h_kv), int(d), int(page_size), int(n_pages),
-                                    max_pages, int(bool(causal)), float(scale), cu_seqlens_q.data_ptr(),
-                                    kv_lens.data_ptr(), page_table.data_ptr(), dev_status or None, int(flags),
-                                    int(wait_timeout_ms))
+        self.params = _CPagedParams(*sizes, int(bool(causal)), float(scale), cu_seqlens_q.data_ptr(),
+                                    kv_lens.data_ptr(), page_table.data_ptr(), dev_status or None, flags, wait)
         need = attn_core_paged_workspace_bytes(self.params)
         if need == 0:       # the call itself says what is wrong
             raise AttnCoreError(ERR_UNSUPPORTED if page_size not in PAGE_SIZES or d not in SUPPORTED_HEAD_DIMS

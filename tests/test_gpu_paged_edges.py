@@ -193,3 +193,19 @@ def test_workspace_smaller_than_its_elements_say():
         p.batch(workspace=torch.empty(1, dtype=torch.uint8, device=DEV).expand(need))
     with pytest.raises(ValueError):
         p.batch(workspace=torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2])
+
+
+def test_more_tokens_than_32_bits():
+    """Sizes that the argument structure cannot hold are refused, not cut."""
+    x = torch.randn(1, 1, 64, device=DEV).to(torch.bfloat16)
+    y = torch.zeros(1, 1, 64, device=DEV, dtype=torch.bfloat16)
+    n = 2 ** 32 + 1
+    with pytest.raises(ValueError):
+        ac.rope_fwd(x.expand(n, 1, 64), None, ac.rope_table(64), out_q=y.expand(n, 1, 64))
+    with pytest.raises(ValueError):
+        ac.rope_fwd(x.expand(1, n, 64), None, ac.rope_table(64), out_q=y.expand(1, n, 64))
+    p = Paged([1], [20], 2, 1, 64, 16)
+    for kw in (dict(n_tokens=n), dict(h_q=2 ** 32 + 2), dict(n_pages=2 ** 32 + p.n_pages), dict(wait_timeout_ms=2 ** 32),
+               dict(page_size=2 ** 32 + 16), dict(flags=2 ** 32)):
+        with pytest.raises(ValueError):
+            p.batch(**kw)

@@ -198,3 +198,21 @@ def test_structures_match_the_header():
     assert ctypes.sizeof(ac._CRopeConfig) == 16 + 8 * 8
     assert ctypes.sizeof(ac._CRopeParams) == 16 + 4 * 24 + 8 + 8
     assert ctypes.sizeof(ac._CPagedParams) == 40 + 4 * 8 + 8
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The binding cuts no size or position to the structures' 32 bits."""
+    import torch
+    for kw in (dict(d=2 ** 32 + 64), dict(d=64, rot_dim=2 ** 32 + 8), dict(d=-2 ** 32 + 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            ac.rope_table(**kw)
+    t = ac.rope_table(64)
+    for pos0 in (2 ** 31, -2 ** 31 - 1, 2 ** 32):
+        for f in (ac.rope_fwd, ac.rope_bwd):
+            with pytest.raises(ValueError, match="pos0"):
+                f(torch.zeros(2, 1, 64, dtype=torch.bfloat16), None, t, pos0=pos0)
+    cu, lens, table = (torch.zeros(n, dtype=torch.int32) for n in (2, 1, 4))
+    sizes = dict(n_tokens=1, h_q=2, h_kv=1, d=64, page_size=16, n_pages=4)
+    for name in ("n_tokens", "h_q", "h_kv", "d", "page_size", "n_pages", "flags", "wait_timeout_ms"):
+        with pytest.raises(ValueError, match=name):
+            ac.PagedBatch(cu, lens, table.view(1, 4), **{**sizes, name: 2 ** 32 + sizes.get(name, 0)})
