@@ -739,6 +739,8 @@ def _rope_params(q, k, out_q, out_k, d):
 
 def _rope(what, q, k, table, positions, pos0, out_q, out_k):
     pos0 = _bits32("pos0", pos0) if pos0 else 0
+    if (q is None and out_q is not None) or (k is None and out_k is not None):
+        raise ValueError("out_q without q" if q is None and out_q is not None else "out_k without k")
     host = _host()
     dev = host.device()
     key = (table.d,

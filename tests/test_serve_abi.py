@@ -216,3 +216,14 @@ def test_sizes_past_32_bits_are_refused():
     for name in ("n_tokens", "h_q", "h_kv", "d", "page_size", "n_pages", "flags", "wait_timeout_ms"):
         with pytest.raises(ValueError, match=name):
             ac.PagedBatch(cu, lens, table.view(1, 4), **{**sizes, name: 2 ** 32 + sizes.get(name, 0)})
+
+
+def test_an_output_without_its_input_is_refused():
+    """out_q or out_k beside a missing q or k would come back as it was."""
+    import torch
+    t, x = ac.rope_table(64), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    for f in (ac.rope_fwd, ac.rope_bwd):
+        with pytest.raises(ValueError, match="out_q without q"):
+            f(None, x, t, out_q=x.clone())
+        with pytest.raises(ValueError, match="out_k without k"):
+            f(x, None, t, out_k=x.clone())
