@@ -75,9 +75,10 @@ class PagePool:
 
     def fork(self, seq: int) -> int:
         """A new sequence with the same keys and values, sharing every page."""
+        pages, length = list(self._pages[seq]), self._length[seq]
         new = self.add()
-        self._pages[new], self._length[new] = list(self._pages[seq]), self._length[seq]
-        for page in self._pages[new]:
+        self._pages[new], self._length[new] = pages, length
+        for page in pages:
             self._users[page] += 1
         return new
 

@@ -127,3 +127,19 @@ def test_refusals():
         pool.extend(t, 1)
     pool.free(s)
     assert pool.extend(t, 1) == []                    # its own now
+
+
+def test_a_fork_of_nothing_leaves_nothing():
+    """Forking a sequence that is not there raises and adds no sequence."""
+    pool = PagePool(4, 4)
+    s = pool.add()
+    pool.extend(s, 6)
+    pool.free(s)
+    with pytest.raises(KeyError):
+        pool.fork(s)
+    with pytest.raises(KeyError):
+        pool.fork(99)
+    for seq in range(s, s + 3):
+        with pytest.raises(KeyError):
+            pool.length(seq)
+    assert pool.free_pages == 4 and pool.add() == s + 1
