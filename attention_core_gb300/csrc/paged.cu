@@ -13,12 +13,12 @@
 // tile is M = 128 in both: with 8 live rows the padded products still take less
 // time than the block's 64 KB take to arrive at one SM's share of HBM (about 2700
 // cycles), and warps without a live row skip the softmax.  Measured on one GB300:
-//   one new token, 64/8 heads of 128, one sequence of 131072 keys   89 us (6.0 TB/s)
-//   the same for 64 sequences of up to 8192 keys                   206 us (6.4 TB/s)
-//   2048 new tokens over 8192 keys, 64/8 heads of 128              337 us in a loop,
+//   one new token, 64/8 heads of 128, one sequence of 131072 keys   88 us (6.1 TB/s)
+//   the same for 64 sequences of up to 8192 keys                   203 us (6.5 TB/s)
+//   2048 new tokens over 8192 keys, 64/8 heads of 128              336 us in a loop,
 //                              300 us before the power limit (1.43 / 1.6 PFLOP/s)
 //   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160   66 us
-//   one new token over 500 keys                                      9 us in a graph
+//   one new token over 500 keys                                     11 us in a graph
 //
 // Persistent, one CTA per SM.  The work is cut into equal shares of blocks, or
 // handed out in whole tiles (paged_sched.cuh).  Structure (384 threads):
@@ -58,8 +58,9 @@ namespace {
 // idle most of the time.  In batches of such tiles (single tokens) P goes in as two bf16
 // terms, the rounded value and what the rounding left, so that only O's own rounding is
 // left of the error: 1.7e-3 in the 2-norm, against 2.3e-3 with P rounded.  Measured: 64
-// sequences to 8192 keys 200 -> 206 us, one of 131072 keys 87 -> 89.  A kernel of its
-// own: the choice inside the loop cost the others 3 to 4%.
+// sequences to 8192 keys 200 -> 206 us, one of 131072 keys 87 -> 89, one of 500 keys
+// 9.6 -> 10.6 in a graph (few blocks, one after another: their longer chain shows).  A
+// kernel of its own: the choice inside the loop cost the others 3 to 4%.
 constexpr int kFineRows = 32;
 constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
 
@@ -269,7 +270,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 //   1024 tiles, 34 MB                                 309 -> 313
 //   512 tiles of 2.5 blocks, 33 MB                     27 -> 29
 //   256 tiles, one per head, 333 MB                    67 -> 73
-constexpr int64_t kManyBytes = 100000000;
+constexpr int64_t kManyBytes = 100000000;   // what L2 (129 MB) holds of them beside Q, O and the parts
 __device__ __forceinline__ bool hand_out_tiles(int64_t units, int64_t tiles, int64_t heads, int64_t ctas, int d)
 {
     if (10 * tiles < 14 * ctas || 2 * tiles < 3 * heads) return false;

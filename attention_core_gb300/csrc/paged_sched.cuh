@@ -11,11 +11,12 @@
 // a tile's first unit takes all of it (cutting one costs more, in the join, than the
 // imbalance of a few blocks).  How short goes by the tiles (snap_blocks).
 //
-// The other split hands out whole tiles, in the same order, to whichever CTA is
-// ready for one (a counter in the workspace).  Nothing is cut and joined, and
-// neighbouring CTAs visit the same keys at the same time, which matters where a KV
-// head has several row tiles and the keys of all heads do not fit L2; but the last
-// tiles leave CTAs without work.  hand_out_tiles() chooses.
+// The other split hands out whole tiles to whichever CTA is ready for one (a counter
+// in the workspace): 32 sequences at a time, those with the most keys first, and of
+// each KV head the last row tile first, so that the tiles that go out last are short.
+// Nothing is cut and joined, and neighbouring CTAs visit the same keys at the same
+// time, which matters where a KV head has several row tiles and the keys of all heads
+// do not fit L2; but the last tiles leave CTAs without work.  hand_out_tiles() chooses.
 //
 // Lengths are device data, so every CTA finds its share by itself: a block-wide
 // sum over the sequences' units (closed form under the causal mask), then a walk

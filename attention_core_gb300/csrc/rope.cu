@@ -13,10 +13,10 @@
 // sines in registers and walks over some of the heads, so an angle is formed
 // once for all of those and there is no shared memory; the first heads' loads go
 // out before the angles are formed.  Measured: Q and K of [1, 64 + 8, 8192, 128]
-// 46.2 us (6.5 TB/s, 96% of a plain copy's rate; 54.0 with all heads in one block and
-// loads behind the angles), [2, 12 + 12, 2048, 128] with half of each head 11.8 us,
-// the tiny [1, 2 + 2, 128, 64] 2.4 us, all in a graph; single calls of the last one
-// take the host's 12 us.
+// 45.8 us (6.6 TB/s, 97% of a plain copy's rate; 54.0 with all heads in one block and
+// loads behind the angles), [2, 12 + 12, 2048, 128] with half of each head 11.1 us (a
+// plain copy of the same bytes: 9.1), the tiny [1, 2 + 2, 128, 64] 2.5 us, all in a
+// graph; single calls of the last one take the host's 11 us.
 #include "kernels.h"
 #include "ptx.cuh"
 
