@@ -223,7 +223,8 @@ def prepare(case, seed):
     if own:
         import attention_core_gb300 as ac
         s["batch"] = ac.PagedBatch(s["cu"], s["kv_lens"], s["page_table"], n_tokens=total, h_q=c.get("h_q", h_kv),
-                                   h_kv=h_kv, d=d, page_size=ps, n_pages=n_pages)
+                                   h_kv=h_kv, d=d, page_size=ps, n_pages=n_pages, group_starts=s.get("starts"),
+                                   prefix_pages=s.get("prefix_pages"))
     return s
 
 
@@ -334,7 +335,7 @@ def _own(s):
     import attention_core_gb300 as ac
     c = s["case"]
     if c["op"] == "prefix":
-        o, lse = ac.paged_prefix_fwd(s["batch"], s["starts"], s["prefix_pages"], s["q"], s["k_pages"], s["v_pages"])
+        o, lse = ac.paged_prefix_fwd(s["batch"], s["q"], s["k_pages"], s["v_pages"])
         return {"o": o, "lse": lse}
     if c["op"] == "weights":
         return ac.paged_weights(s["batch"], s["q"], s["lse"], s["k_pages"], s["weights"], decay=c["decay"], out=s["new_weights"])
