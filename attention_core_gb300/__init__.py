@@ -33,6 +33,7 @@ __all__ = [
     "ERR_DEVICE_TABLE", "RopeTable", "rope_table", "attn_core_rope_fwd", "attn_core_rope_bwd", "rope_fwd",
     "rope_bwd", "PAGE_SIZES", "PagedBatch", "attn_core_paged_append", "attn_core_paged_fwd",
     "attn_core_paged_workspace_bytes", "paged_append", "paged_fwd", "attn_core_page_copy", "page_copy",
+    "attn_core_paged_prefix_fwd", "attn_core_paged_prefix_workspace_bytes", "paged_prefix_fwd",
 ]
 
 OK = 0
@@ -224,6 +225,10 @@ def load_library(path: str = LIB_PATH):
     lib.attn_core_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_core_paged_fwd.argtypes = [PP, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.attn_core_paged_fwd.restype = ctypes.c_int
+    lib.attn_core_paged_prefix_workspace_bytes.argtypes = [PP, ctypes.c_int32]
+    lib.attn_core_paged_prefix_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_core_paged_prefix_fwd.argtypes = [PP, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.attn_core_paged_prefix_fwd.restype = ctypes.c_int
     lib.attn_core_page_copy.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp,
                                         ctypes.c_int64, vp]
     lib.attn_core_page_copy.restype = ctypes.c_int
@@ -231,6 +236,8 @@ def load_library(path: str = LIB_PATH):
     for name, argtypes in (("attn_core_rope_fwd", [vp] * 7), ("attn_core_rope_bwd", [vp] * 7),
                            ("attn_core_paged_append", [vp] * 10),
                            ("attn_core_paged_fwd", [vp] * 7 + [ctypes.c_size_t, vp]),
+                           ("attn_core_paged_prefix_fwd",
+                            [vp, ctypes.c_int32] + [vp] * 8 + [ctypes.c_size_t, vp]),
                            ("attn_core_page_copy", [vp, i64, i64, i64, i64, vp, i64, vp])):
         f = lib[name]
         f.argtypes, f.restype = argtypes, ctypes.c_int
@@ -646,6 +653,17 @@ def attn_core_paged_fwd(p: _CPagedParams, q: int, k_pages: int, v_pages: int, o:
                                               stream or None)
 
 
+def attn_core_paged_prefix_workspace_bytes(p: _CPagedParams, n_groups: int) -> int:
+    return int(load_library().attn_core_paged_prefix_workspace_bytes(p, n_groups))
+
+
+def attn_core_paged_prefix_fwd(p: _CPagedParams, n_groups: int, group_starts: int, prefix_pages: int, q: int,
+                               k_pages: int, v_pages: int, o: int, lse: int, workspace: int, workspace_bytes: int,
+                               stream: int) -> int:
+    return load_library().attn_core_paged_prefix_fwd(p, n_groups, group_starts, prefix_pages, q, k_pages, v_pages, o,
+                                                     lse, workspace, workspace_bytes, stream or None)
+
+
 def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: int, page_bytes: int, pairs: int,
                         n_pairs: int, stream: int) -> int:
     """pairs: address of host int32 [n_pairs, 2]."""
@@ -804,11 +822,16 @@ class PagedBatch:
     graph follows.  The batch owns the attention's workspace; calls that may
     overlap on the GPU need a batch (or a ``workspace``) each.  It may be dropped
     right after a call, on whichever stream that was made; a captured graph needs
-    the batch for as long as it is replayed."""
+    the batch for as long as it is replayed.
+
+    ``group_starts`` [n_groups + 1] and ``prefix_pages`` [n_groups], two more such
+    tables, make it a batch for paged_prefix_fwd: the sequences group_starts[g] ..
+    group_starts[g + 1] - 1 name the same pages in their first prefix_pages[g]
+    columns (PagePool.groups finds them)."""
 
     def __init__(self, cu_seqlens_q, kv_lens, page_table, *, n_tokens: int, h_q: int, h_kv: int, d: int,
                  page_size: int, n_pages: int, causal: bool = True, scale: float = 0.0, dev_status: int = 0,
-                 flags: int = 0, wait_timeout_ms: int = 0, workspace=None):
+                 flags: int = 0, wait_timeout_ms: int = 0, workspace=None, group_starts=None, prefix_pages=None):
         import torch
         if page_table.dim() != 2:
             raise ValueError(f"page_table must be [n_seq, max_pages], got {tuple(page_table.shape)}")
@@ -827,7 +850,21 @@ class PagedBatch:
         if need == 0:       # the call itself says what is wrong
             raise AttnCoreError(ERR_UNSUPPORTED if page_size not in PAGE_SIZES or d not in SUPPORTED_HEAD_DIMS
                                 else ERR_INVALID_ARG, "PagedBatch")
-        for name, t in (("kv_lens", kv_lens), ("page_table", page_table)):
+        self._groups = None     # (number of groups, their tables' addresses)
+        if (group_starts is None) != (prefix_pages is None):
+            raise ValueError("group_starts and prefix_pages go together")
+        if group_starts is not None:
+            n_groups = group_starts.numel() - 1
+            _check(group_starts, "group_starts", torch.int32, (n_groups + 1,))
+            _check(prefix_pages, "prefix_pages", torch.int32, (n_groups,))
+            self._groups = (n_groups, group_starts.data_ptr(), prefix_pages.data_ptr())
+            self.tables += (group_starts, prefix_pages)
+            more = attn_core_paged_prefix_workspace_bytes(self.params, n_groups)
+            if more == 0:
+                raise AttnCoreError(ERR_INVALID_ARG, "PagedBatch")
+            need = max(need, more)
+        names = ("kv_lens", "page_table", "group_starts", "prefix_pages")
+        for name, t in zip(names, self.tables[1:]):
             if t.device != cu_seqlens_q.device:
                 raise ValueError(f"{name} must be on {cu_seqlens_q.device}, got {t.device}")
         self._streams = set()   # handles of the streams that calls were made on
@@ -924,6 +961,21 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
     """Attention of the batch's new tokens q [n_tokens, h_q, d] over the cache
     (which already holds their keys and values).  Returns (O like q, LSE fp32
     [h_q, n_tokens])."""
+    dev, out, lse = _attend_args(batch, q, k_pages, v_pages, out, lse)
+    if batch.params.n_tokens:
+        ws, ws_bytes = batch._ws
+        stream = _host().stream(dev)
+        if stream not in batch._streams:
+            batch._used_on(stream)
+        rc = _FAST["attn_core_paged_fwd"](batch._address, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, stream)
+        if rc != OK:
+            raise AttnCoreError(rc, "attn_core_paged_fwd")
+    return out, lse
+
+
+def _attend_args(batch: PagedBatch, q, k_pages, v_pages, out, lse):
+    """The device, and O and LSE of a call of the attention over the cache."""
     host = _host()
     dev, bf16 = host.device(), host.bf16
     _need(q, "q", bf16, batch._q_shape, dev)
@@ -939,15 +991,25 @@ def paged_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
         _need(lse, "lse", host.f32, batch._lse_shape, dev)
     if batch._workspace.get_device() != dev:
         _on_device(dev, batch._workspace)
+    return dev, out, lse
+
+
+def paged_prefix_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=None):
+    """paged_fwd of a batch with groups of sequences that share their first
+    pages: the shared keys are visited once for each group.  Returns (O, LSE)."""
+    if batch._groups is None:
+        raise ValueError("the batch has no groups (group_starts, prefix_pages)")
+    dev, out, lse = _attend_args(batch, q, k_pages, v_pages, out, lse)
     if batch.params.n_tokens:
         ws, ws_bytes = batch._ws
-        stream = host.stream(dev)
+        stream = _host().stream(dev)
         if stream not in batch._streams:
             batch._used_on(stream)
-        rc = _FAST["attn_core_paged_fwd"](batch._address, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                          out.data_ptr(), lse.data_ptr(), ws, ws_bytes, stream)
+        rc = _FAST["attn_core_paged_prefix_fwd"](batch._address, *batch._groups, q.data_ptr(), k_pages.data_ptr(),
+                                                 v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, ws_bytes,
+                                                 stream)
         if rc != OK:
-            raise AttnCoreError(rc, "attn_core_paged_fwd")
+            raise AttnCoreError(rc, "attn_core_paged_prefix_fwd")
     return out, lse
 
 

@@ -1080,17 +1080,22 @@ size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p)
     return check_paged(p) ? 0 : ac::paged_ws_bytes(p->d);
 }
 
-int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
-                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream)
+}  // extern "C"
+
+namespace {
+
+// `groups`: null, or the groups of sequences that share their first pages.
+int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups, size_t need, const void* q,
+                 const void* k_pages, const void* v_pages, void* o, float* lse, void* workspace,
+                 size_t workspace_bytes, void* stream)
 {
-    int rc = check_paged(p);
-    if (rc) return rc;
+    int rc;
     if (!q || !k_pages || !v_pages || !o || !lse || !workspace) return ATTN_CORE_ERR_INVALID_ARG;
     if (o == q || o == k_pages || o == v_pages) return ATTN_CORE_ERR_INVALID_ARG;
     for (const void* x : {q, k_pages, v_pages, (const void*)o, (const void*)lse})
         if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_CORE_ERR_MISALIGNED;
-    if (workspace_bytes < ac::paged_ws_bytes(p->d)) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < need) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
     if (p->n_tokens == 0) return ATTN_CORE_OK;
     if ((rc = check_device())) return rc;
     if ((rc = get_encoder())) return rc;
@@ -1118,7 +1123,49 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
             return rc;
     }
     if ((rc = encode_map_tokens(&m.o, o, p->d % 64 ? 32 : 64, p->d, a.group, p->h_kv, p->n_tokens, a.tpt))) return rc;
-    return ac::launch_paged(m, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return (groups ? ac::launch_prefix(m, a, *groups, st) : ac::launch_paged(m, a, st)) ? ATTN_CORE_ERR_CUDA
+                                                                                        : ATTN_CORE_OK;
+}
+
+int check_groups(const attn_core_paged_params* p, int32_t n_groups)
+{
+    if (n_groups <= 0 || n_groups > p->n_seq) return ATTN_CORE_ERR_INVALID_ARG;
+    if ((int64_t)p->n_seq + n_groups >= (int64_t)INT32_MAX) return ATTN_CORE_ERR_UNSUPPORTED;
+    return ATTN_CORE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const int rc = check_paged(p);
+    if (rc) return rc;
+    return paged_attend(p, nullptr, ac::paged_ws_bytes(p->d), q, k_pages, v_pages, o, lse, workspace, workspace_bytes,
+                        stream);
+}
+
+size_t attn_core_paged_prefix_workspace_bytes(const attn_core_paged_params* p, int32_t n_groups)
+{
+    if (check_paged(p) || check_groups(p, n_groups)) return 0;
+    return ac::prefix_ws_bytes(p->d, p->n_seq, n_groups, p->n_tokens, p->h_q, p->h_kv);
+}
+
+int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups, const int32_t* group_starts,
+                               const int32_t* prefix_pages, const void* q, const void* k_pages, const void* v_pages,
+                               void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = check_paged(p);
+    if (rc || (rc = check_groups(p, n_groups))) return rc;
+    if (!group_starts || !prefix_pages) return ATTN_CORE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(group_starts) | reinterpret_cast<uintptr_t>(prefix_pages)) & 3u)
+        return ATTN_CORE_ERR_MISALIGNED;
+    const ac::PrefixGroups g{group_starts, prefix_pages, n_groups};
+    return paged_attend(p, &g, attn_core_paged_prefix_workspace_bytes(p, n_groups), q, k_pages, v_pages, o, lse,
+                        workspace, workspace_bytes, stream);
 }
 
 int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,

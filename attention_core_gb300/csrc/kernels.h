@@ -285,6 +285,11 @@ struct PagedArgs {
     uint64_t timeout_ns;
     int32_t inject_timeout;
     int32_t num_sms;
+    // batches whose sequences share their first pages (prefix.cu; set by its launcher)
+    const struct PrefixSeq* plan;
+    int32_t n_plan;
+    uint32_t* records;          // where each row's parts lie
+    size_t lse_offset;          // of the parts' LSEs in the workspace
 };
 size_t paged_ws_bytes(int d);
 int paged_tokens_per_tile(int group);
@@ -294,6 +299,15 @@ struct PagedMaps {
     CUtensorMap q[2], k[2], v[2], o;
 };
 int launch_paged(const PagedMaps& maps, const PagedArgs& a, cudaStream_t stream);
+
+// The same where groups of sequences share their first pages (prefix.cu).
+struct PrefixGroups {
+    const int32_t* starts;      // device [n + 1]
+    const int32_t* pages;       // device [n]
+    int32_t n;
+};
+size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv);
+int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, cudaStream_t stream);
 
 // Page copies (pages.cu): `pairs` is a host array.
 int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,

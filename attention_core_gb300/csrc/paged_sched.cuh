@@ -152,6 +152,31 @@ __host__ __device__ inline SeqTable read_seq(const PagedTables& t, int seq, int 
     return r;
 }
 
+// A batch whose sequences share their first pages, as prefix.cu's plan has it: each
+// group's shared keys and each sequence's own ones are sequences of their own, over the
+// same rows of q.
+enum : int32_t {
+    kKindAll = 1,       // every row sees every key
+    kKindPrefix = 2,    // a group's shared keys
+    kKindJoined = 4,    // the rows have keys in two of the plan's sequences
+    kKindBits = 3
+};
+struct PrefixSeq {
+    int32_t q0, nq, kv;
+    int32_t row, page0;     // its keys: from entry page0 of this row of the page table
+    int32_t kind;
+    int32_t pad[2];
+};
+struct PrefixTables {
+    const PrefixSeq* plan;
+    int32_t n_seq, h_kv;
+};
+__host__ __device__ inline SeqTable read_seq(const PrefixTables& t, int seq, int tpt, int)
+{
+    const PrefixSeq& p = t.plan[seq];
+    return SeqTable{p.q0, SeqShape{p.nq, p.kv, tpt, !(p.kind & kKindAll)}, false};
+}
+
 // A piece of one tile: blocks [j0, j1) of it.
 struct Segment {
     int seq, head, m;      // sequence, KV head, row tile
@@ -192,7 +217,8 @@ struct SegmentWalk {
     int seq, head, m, b;   // where `at` is: block b of row tile m
     SeqTable cur;
 
-    __host__ __device__ void load(const PagedTables& t) { cur = read_seq(t, seq, tpt, causal); }
+    template <typename Tables>
+    __host__ __device__ void load(const Tables& t) { cur = read_seq(t, seq, tpt, causal); }
 
     // Unit `at_` lies r units into KV head h of sequence sq.  (Whole warps, see
     // find_tile.)
@@ -212,7 +238,8 @@ struct SegmentWalk {
         }
     }
 
-    __host__ __device__ bool next(const PagedTables& t, Segment& g)
+    template <typename Tables>
+    __host__ __device__ bool next(const Tables& t, Segment& g)
     {
         if (at >= end) return false;
         int n = cur.s.cost(m);

@@ -471,6 +471,26 @@ size_t attn_core_paged_workspace_bytes(const attn_core_paged_params* p);
 int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const void* k_pages, const void* v_pages,
                         void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* attn_core_paged_fwd where sequences share their first pages (forks of one
+ * prompt): group g is the sequences group_starts[g] .. group_starts[g + 1] - 1,
+ * whose page_table rows name the same pages in their first prefix_pages[g]
+ * columns (only one row's entries are read there).  The shared keys are
+ * visited once for all rows of the group instead of once for each sequence;
+ * O and LSE are those of attn_core_paged_fwd up to rounding.  Both tables are
+ * in device memory (group_starts [n_groups + 1], prefix_pages [n_groups]) and
+ * followed by captured graphs; groups may be empty, and sequences outside all
+ * groups share nothing.  Of a group's pages those count that all its sequences
+ * (which have new tokens) hold before their first new token.  Groups that are
+ * out of order or range write ATTN_CORE_ERR_DEVICE_TABLE to dev_status and
+ * share nothing.  1 <= n_groups <= n_seq.  The workspace holds the rows of
+ * shared and own keys in fp32 until they are joined: about 8 n_tokens h_q d
+ * bytes more than attn_core_paged_fwd's.  Three kernels; the same inputs give
+ * the same bits. */
+size_t attn_core_paged_prefix_workspace_bytes(const attn_core_paged_params* p, int32_t n_groups);
+int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups, const int32_t* group_starts,
+                               const int32_t* prefix_pages, const void* q, const void* k_pages, const void* v_pages,
+                               void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Copies pages inside a cache: page pairs[2i + 1] <- page pairs[2i], in every
  * plane (one per layer and per K or V; a plane holds n_pages pages of
  * page_bytes and starts plane_stride bytes after the one before).  Forking a
