@@ -34,6 +34,8 @@ __all__ = [
     "rope_bwd", "PAGE_SIZES", "PagedBatch", "attn_core_paged_append", "attn_core_paged_fwd",
     "attn_core_paged_workspace_bytes", "paged_append", "paged_fwd", "attn_core_page_copy", "page_copy",
     "attn_core_paged_prefix_fwd", "attn_core_paged_prefix_workspace_bytes", "paged_prefix_fwd",
+    "attn_core_paged_weights", "attn_core_paged_weights_workspace_bytes", "paged_weights",
+    "attn_core_paged_evict", "attn_core_paged_evict_workspace_bytes", "paged_evict",
 ]
 
 OK = 0
@@ -229,6 +231,15 @@ def load_library(path: str = LIB_PATH):
     lib.attn_core_paged_prefix_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_core_paged_prefix_fwd.argtypes = [PP, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.attn_core_paged_prefix_fwd.restype = ctypes.c_int
+    lib.attn_core_paged_weights_workspace_bytes.argtypes = [PP]
+    lib.attn_core_paged_weights_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_core_paged_weights.argtypes = [PP, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.attn_core_paged_weights.restype = ctypes.c_int
+    lib.attn_core_paged_evict_workspace_bytes.argtypes = [PP]
+    lib.attn_core_paged_evict_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_core_paged_evict.argtypes = [PP, vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp,
+                                          ctypes.c_size_t, vp]
+    lib.attn_core_paged_evict.restype = ctypes.c_int
     lib.attn_core_page_copy.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp,
                                         ctypes.c_int64, vp]
     lib.attn_core_page_copy.restype = ctypes.c_int
@@ -238,6 +249,10 @@ def load_library(path: str = LIB_PATH):
                            ("attn_core_paged_fwd", [vp] * 7 + [ctypes.c_size_t, vp]),
                            ("attn_core_paged_prefix_fwd",
                             [vp, ctypes.c_int32] + [vp] * 8 + [ctypes.c_size_t, vp]),
+                           ("attn_core_paged_weights",
+                            [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]),
+                           ("attn_core_paged_evict",
+                            [vp, vp, ctypes.c_int32, ctypes.c_int32] + [vp] * 7 + [ctypes.c_size_t, vp]),
                            ("attn_core_page_copy", [vp, i64, i64, i64, i64, vp, i64, vp])):
         f = lib[name]
         f.argtypes, f.restype = argtypes, ctypes.c_int
@@ -664,6 +679,27 @@ def attn_core_paged_prefix_fwd(p: _CPagedParams, n_groups: int, group_starts: in
                                                      lse, workspace, workspace_bytes, stream or None)
 
 
+def attn_core_paged_weights_workspace_bytes(p: _CPagedParams) -> int:
+    return int(load_library().attn_core_paged_weights_workspace_bytes(p))
+
+
+def attn_core_paged_weights(p: _CPagedParams, q: int, k_pages: int, lse: int, decay: float, weights: int,
+                            weights_out: int, workspace: int, workspace_bytes: int, stream: int) -> int:
+    return load_library().attn_core_paged_weights(p, q, k_pages, lse, decay, weights, weights_out, workspace,
+                                                  workspace_bytes, stream or None)
+
+
+def attn_core_paged_evict_workspace_bytes(p: _CPagedParams) -> int:
+    return int(load_library().attn_core_paged_evict_workspace_bytes(p))
+
+
+def attn_core_paged_evict(p: _CPagedParams, keep: int, first: int, recent: int, out_table: int, k_pages: int,
+                          v_pages: int, weights: int, weights_out: int, kept: int, workspace: int,
+                          workspace_bytes: int, stream: int) -> int:
+    return load_library().attn_core_paged_evict(p, keep, first, recent, out_table or None, k_pages, v_pages, weights,
+                                                weights_out, kept, workspace, workspace_bytes, stream or None)
+
+
 def attn_core_page_copy(pages: int, n_planes: int, plane_stride: int, n_pages: int, page_bytes: int, pairs: int,
                         n_pairs: int, stream: int) -> int:
     """pairs: address of host int32 [n_pairs, 2]."""
@@ -876,6 +912,10 @@ class PagedBatch:
         self._kv_shape = torch.Size((int(n_tokens), int(h_kv), int(d)))
         self._page_shape = torch.Size((int(n_pages), int(h_kv), int(page_size), int(d)))
         self._lse_shape = torch.Size((int(h_q), int(n_tokens)))
+        self._weights_shape = torch.Size((int(n_seq), int(h_kv), int(max_pages) * int(page_size)))
+        self._weights_layout = _layout(self._weights_shape)
+        self._seq_shape, self._table_shape = torch.Size((int(n_seq),)), torch.Size((int(n_seq), int(max_pages)))
+        self._evict_bytes = attn_core_paged_evict_workspace_bytes(self.params)      # 0: more than it can count
         self._q_layout, self._lse_layout = _layout(self._q_shape), _layout(self._lse_shape)
 
     @property
@@ -1011,6 +1051,79 @@ def paged_prefix_fwd(batch: PagedBatch, q, k_pages, v_pages, *, out=None, lse=No
         if rc != OK:
             raise AttnCoreError(rc, "attn_core_paged_prefix_fwd")
     return out, lse
+
+
+def paged_weights(batch: PagedBatch, q, lse, k_pages, weights, *, decay: float = 1.0, out=None):
+    """Add what the batch's new tokens pay to each key of the cache (their
+    attention weights, by ``lse`` as paged_fwd returned it) to ``weights`` fp32
+    [n_seq, h_kv, max_pages * page_size], whose earlier values fade by ``decay``;
+    the new tokens' own keys start at 0.  In place, or into ``out``, which is
+    returned; sequences without new tokens are left as they were there."""
+    host = _host()
+    dev = host.device()
+    _need(q, "q", host.bf16, batch._q_shape, dev)
+    _need(k_pages, "k_pages", host.bf16, batch._page_shape, dev)
+    _need(lse, "lse", host.f32, batch._lse_shape, dev)
+    _need(weights, "weights", host.f32, batch._weights_shape, dev)
+    if out is None:
+        out = weights
+    else:
+        _need(out, "out", host.f32, batch._weights_shape, dev)
+    if batch._workspace.get_device() != dev:
+        _on_device(dev, batch._workspace)
+    if batch.params.n_tokens:
+        ws, ws_bytes = batch._ws
+        stream = host.stream(dev)
+        if stream not in batch._streams:
+            batch._used_on(stream)
+        rc = _FAST["attn_core_paged_weights"](batch._address, q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(),
+                                              float(decay), weights.data_ptr(), out.data_ptr(), ws, ws_bytes, stream)
+        if rc != OK:
+            raise AttnCoreError(rc, "attn_core_paged_weights")
+    return out
+
+
+def paged_evict(batch: PagedBatch, weights, keep, k_pages, v_pages, *, first: int = 0, recent: int = 0,
+                out_table=None, out_weights=None, kept=None):
+    """Keep ``keep[i]`` keys of sequence i (int32 CUDA tensor [n_seq]), each KV head
+    its own: the ``recent`` last, the ``first`` first, and of the others those with
+    the largest ``weights``.  They move to the front in their order, K and V within
+    the sequence's pages or to those of ``out_table`` [n_seq, max_pages]
+    (PagePool.shrink), the weights in place or into ``out_weights``.  Returns
+    ``kept`` int32 [n_seq, h_kv, max_pages * page_size]: the key that each was."""
+    host = _host()
+    dev = host.device()
+    _need(weights, "weights", host.f32, batch._weights_shape, dev)
+    _need(keep, "keep", host.i32, batch._seq_shape, dev)
+    _need(k_pages, "k_pages", host.bf16, batch._page_shape, dev)
+    _need(v_pages, "v_pages", host.bf16, batch._page_shape, dev)
+    if out_table is not None:
+        _need(out_table, "out_table", host.i32, batch._table_shape, dev)
+    if out_weights is None:
+        out_weights = weights
+    else:
+        _need(out_weights, "out_weights", host.f32, batch._weights_shape, dev)
+    if kept is None:
+        kept = host.empty(*batch._weights_layout, host.i32)
+    else:
+        _need(kept, "kept", host.i32, batch._weights_shape, dev)
+    first, recent = _bits32("first", first), _bits32("recent", recent)
+    if batch._workspace.get_device() != dev:
+        _on_device(dev, batch._workspace)
+    ws, ws_bytes = batch._ws
+    if ws_bytes < batch._evict_bytes:       # of this call's own: very many or very long sequences
+        own = host.empty((batch._evict_bytes // 4,), (1,), host.i32)
+        ws, ws_bytes = own.data_ptr(), batch._evict_bytes
+    stream = host.stream(dev)
+    if stream not in batch._streams:
+        batch._used_on(stream)
+    rc = _FAST["attn_core_paged_evict"](batch._address, keep.data_ptr(), first, recent,
+                                        0 if out_table is None else out_table.data_ptr(), k_pages.data_ptr(),
+                                        v_pages.data_ptr(), weights.data_ptr(), out_weights.data_ptr(),
+                                        kept.data_ptr(), ws, ws_bytes, stream)
+    if rc != OK:
+        raise AttnCoreError(rc, "attn_core_paged_evict")
+    return kept
 
 
 def page_copy(pages, pairs) -> None:

@@ -1128,6 +1128,15 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
                                                                                         : ATTN_CORE_OK;
 }
 
+// (sequence, KV head) lines and their chunks, which the eviction counts in 32 bits
+int check_lines(const attn_core_paged_params* p)
+{
+    const int64_t lines = (int64_t)p->n_seq * p->h_kv, length = (int64_t)p->max_pages * p->page_size;
+    if (lines >= (int64_t)INT32_MAX / 16 || lines * (length / 64 + 2) >= (int64_t)INT32_MAX / 2)
+        return ATTN_CORE_ERR_UNSUPPORTED;
+    return ATTN_CORE_OK;
+}
+
 int check_groups(const attn_core_paged_params* p, int32_t n_groups)
 {
     if (n_groups <= 0 || n_groups > p->n_seq) return ATTN_CORE_ERR_INVALID_ARG;
@@ -1166,6 +1175,97 @@ int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups
     const ac::PrefixGroups g{group_starts, prefix_pages, n_groups};
     return paged_attend(p, &g, attn_core_paged_prefix_workspace_bytes(p, n_groups), q, k_pages, v_pages, o, lse,
                         workspace, workspace_bytes, stream);
+}
+
+size_t attn_core_paged_weights_workspace_bytes(const attn_core_paged_params* p)
+{
+    return check_paged(p) ? 0 : ac::weights_ws_bytes();
+}
+
+int attn_core_paged_weights(const attn_core_paged_params* p, const void* q, const void* k_pages, const float* lse,
+                            float decay, const float* weights, float* weights_out, void* workspace,
+                            size_t workspace_bytes, void* stream)
+{
+    int rc = check_paged(p);
+    if (rc) return rc;
+    if (!q || !k_pages || !lse || !weights || !weights_out || !workspace) return ATTN_CORE_ERR_INVALID_ARG;
+    if (isnan(decay) || isinf(decay) || decay < 0.0f) return ATTN_CORE_ERR_INVALID_ARG;
+    if (weights_out == lse || weights_out == q || weights_out == k_pages) return ATTN_CORE_ERR_INVALID_ARG;
+    for (const void* x : {q, k_pages, (const void*)lse, (const void*)weights, (const void*)weights_out})
+        if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_CORE_ERR_MISALIGNED;
+    if (workspace_bytes < ac::weights_ws_bytes()) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
+    if (p->n_tokens == 0) return ATTN_CORE_OK;
+    if ((rc = check_device())) return rc;
+    if ((rc = get_encoder())) return rc;
+    ac::WeightsArgs a{};
+    a.t = paged_tables(p);
+    a.lse = lse;
+    a.in = weights;
+    a.out = weights_out;
+    a.ws = static_cast<uint8_t*>(workspace);
+    a.d = p->d;
+    a.causal = p->causal;
+    a.group = p->h_q / p->h_kv;
+    a.tpt = ac::paged_tokens_per_tile(a.group);
+    a.decay = decay;
+    const float scale = (p->scale > 0.0f) ? p->scale : 1.0f / sqrtf((float)p->d);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.timeout_ns = (uint64_t)(p->wait_timeout_ms ? p->wait_timeout_ms : 2000u) * 1000000ull;
+    a.inject_timeout = (p->flags & ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
+    if ((rc = device_sms(&a.num_sms))) return rc;
+    ac::PagedMaps m;
+    for (int i = 0; i < (p->d % 64 ? 2 : 1); ++i) {
+        const int cw = i ? 32 : 64;
+        if ((rc = encode_map_tokens(&m.q[i], q, cw, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)) ||
+            (rc = encode_map_pages(&m.k[i], k_pages, cw, p->d, p->page_size, (int64_t)p->n_pages * p->h_kv)))
+            return rc;
+    }
+    return ac::launch_weights(m, a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
+}
+
+size_t attn_core_paged_evict_workspace_bytes(const attn_core_paged_params* p)
+{
+    if (check_paged(p) || check_lines(p)) return 0;
+    return ac::evict_ws_bytes((int64_t)p->n_seq * p->h_kv, (int64_t)p->max_pages * p->page_size);
+}
+
+int attn_core_paged_evict(const attn_core_paged_params* p, const int32_t* keep, int32_t first, int32_t recent,
+                          const int32_t* out_table, void* k_pages, void* v_pages, const float* weights,
+                          float* weights_out, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = check_paged(p);
+    if (rc || (rc = check_lines(p))) return rc;
+    if (!keep || !k_pages || !v_pages || !weights || !weights_out || !kept || !workspace)
+        return ATTN_CORE_ERR_INVALID_ARG;
+    if (first < 0 || recent < 0 || k_pages == v_pages) return ATTN_CORE_ERR_INVALID_ARG;
+    if ((const void*)kept == weights || (const void*)kept == weights_out) return ATTN_CORE_ERR_INVALID_ARG;
+    if (!out_table) out_table = p->page_table;
+    for (const void* x : {(const void*)k_pages, (const void*)v_pages, (const void*)weights, (const void*)weights_out,
+                          (const void*)kept})
+        if (!aligned16(x)) return ATTN_CORE_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(keep) | reinterpret_cast<uintptr_t>(out_table)) & 3u)
+        return ATTN_CORE_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_CORE_ERR_MISALIGNED;
+    if (workspace_bytes < attn_core_paged_evict_workspace_bytes(p)) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
+    if ((rc = check_device())) return rc;
+    ac::EvictArgs a{};
+    a.t = paged_tables(p);
+    a.keep = keep;
+    a.out_table = out_table;
+    a.first = first;
+    a.recent = recent;
+    a.k_pages = static_cast<uint16_t*>(k_pages);
+    a.v_pages = static_cast<uint16_t*>(v_pages);
+    a.in = weights;
+    a.out = weights_out;
+    a.kept = kept;
+    a.ws = static_cast<uint8_t*>(workspace);
+    a.d = p->d;
+    a.timeout_ns = (uint64_t)(p->wait_timeout_ms ? p->wait_timeout_ms : 2000u) * 1000000ull;
+    a.inject_timeout = (p->flags & ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
+    if ((rc = device_sms(&a.num_sms))) return rc;
+    return ac::launch_evict(a, reinterpret_cast<cudaStream_t>(stream)) ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
 }
 
 int attn_core_page_copy(void* pages, int64_t n_planes, int64_t plane_stride, int64_t n_pages, int64_t page_bytes,

@@ -309,6 +309,50 @@ struct PrefixGroups {
 size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv);
 int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, cudaStream_t stream);
 
+// Attention weight that the cache's keys gather (weights.cu).  Maps: q and k only.
+struct WeightsArgs {
+    PagedTables t;
+    const float* lse;           // [h_q, n_tokens]
+    const float* in;            // [n_seq, h_kv, max_pages * page_size]
+    float* out;                 // may be `in`
+    uint8_t* ws;                // weights_ws_bytes()
+    int32_t d, causal;
+    int32_t group, tpt;         // as PagedArgs
+    float decay, scale_log2;
+    uint64_t timeout_ns;
+    int32_t inject_timeout;
+    int32_t num_sms;
+};
+size_t weights_ws_bytes();
+int launch_weights(const PagedMaps& maps, const WeightsArgs& a, cudaStream_t stream);
+
+// Eviction by gathered attention weight (evict.cu).
+struct EvictArgs {
+    PagedTables t;
+    const int32_t* keep;        // [n_seq]
+    const int32_t* out_table;   // [n_seq, max_pages]; may be the page table
+    int32_t first, recent;
+    uint16_t* k_pages;
+    uint16_t* v_pages;
+    const float* in;            // [n_seq, h_kv, max_pages * page_size]
+    float* out;                 // may be `in`
+    int32_t* kept;              // like `in`
+    uint8_t* ws;                // evict_ws_bytes()
+    int32_t d;
+    uint64_t timeout_ns;
+    int32_t inject_timeout;
+    int32_t num_sms;
+    // set by the launcher: parts of the workspace, and keys that a block can hold
+    uint32_t* counter;
+    int32_t* most_chunks;
+    int32_t* wait_over;
+    int32_t* ranks;
+    int32_t* flags;
+    int32_t per_line, cached;
+};
+size_t evict_ws_bytes(int64_t lines, int64_t length);
+int launch_evict(const EvictArgs& a, cudaStream_t stream);
+
 // Page copies (pages.cu): `pairs` is a host array.
 int launch_page_copy(void* pages, int64_t n_planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* pairs,
                      int64_t n_pairs, cudaStream_t stream);

@@ -56,6 +56,54 @@ class PagePool:
             table[i, :len(p)] = p
         return table, np.array([self._length[s] for s in seqs], dtype=np.int32)
 
+    def groups(self, seqs):
+        """(group_starts int32 [n_groups + 1], prefix_pages int32 [n_groups]) of
+        neighbours among these sequences that share their first pages, for
+        ``paged_prefix_fwd``.  Of nested choices (a system prompt that all share, a
+        document that some do) the batch takes those that save the most page visits,
+        (sequences - 1) * pages summed over the groups."""
+        n = len(seqs)
+        if n == 0:
+            raise ValueError("no sequences")
+        # best[j]: the most that the first j sequences save; min_common[i]: what the
+        # sequences i .. j - 1 have in common
+        best, start_of = np.zeros(n + 1, dtype=np.int64), np.zeros(n + 1, dtype=np.int64)
+        min_common, low, shared_of = np.zeros(n, dtype=np.int64), 0, np.zeros(n + 1, dtype=np.int64)
+        members = np.arange(n, 0, -1, dtype=np.int64)
+        for j in range(1, n + 1):
+            if j > 1:
+                pages = self._common(seqs[j - 2], seqs[j - 1])
+                if pages == 0:
+                    low = j - 1                 # no group reaches across
+                else:
+                    np.minimum(min_common[low:j - 1], pages, out=min_common[low:j - 1])
+            min_common[j - 1] = np.iinfo(np.int64).max // (2 * n)
+            total = best[low:j] + min_common[low:j] * (members[n - j + low:n] - 1)
+            i = low + int(np.argmax(total))
+            best[j], start_of[j] = total[i - low], i
+            shared_of[j] = min_common[i] if i < j - 1 else 0
+        starts, shared, j = [n], [], n
+        while j > 0:
+            shared.append(shared_of[j])
+            j = int(start_of[j])
+            starts.append(j)
+        return np.array(starts[::-1], dtype=np.int32), np.array(shared[::-1], dtype=np.int32)
+
+    def _common(self, a: int, b: int) -> int:
+        """First pages that two sequences have in common."""
+        x, y = self._pages[a], self._pages[b]
+        n = min(len(x), len(y))
+        if x[:n] == y[:n]:
+            return n
+        lo, hi = 0, n                           # shared pages come first, so halving finds the border
+        while lo < hi:
+            mid = (lo + hi) // 2
+            if x[mid] == y[mid]:
+                lo = mid + 1
+            else:
+                hi = mid
+        return lo
+
     # ------------------------------------------------------------ changes ---
     def _take(self) -> int:
         page = heapq.heappop(self._free)
@@ -110,6 +158,38 @@ class PagePool:
         while len(pages) > keep:
             self._drop(pages.pop())
         self._length[seq] = length
+
+    def shrink(self, seqs, lengths, max_pages: int) -> np.ndarray:
+        """These sequences keep ``lengths[i]`` keys each (``paged_evict``, one call for
+        all of them).  Returns its out_table int32 [n, max_pages]: the sequence's own
+        pages, and fresh ones in the places of those that another sequence holds too.
+        What is not needed any more is free afterwards; the eviction has to be queued
+        before anything that writes there."""
+        if len(set(seqs)) != len(seqs) or len(seqs) != len(lengths):
+            raise ValueError("each sequence is named once, with its length")
+        take = 0
+        for s, n in zip(seqs, lengths):
+            if not 0 <= n <= self._length[s]:
+                raise ValueError(f"length of sequence {s} must be in 0 .. {self._length[s]}")
+            need = -(-n // self.page_size)
+            if need > max_pages:
+                raise ValueError(f"sequence {s} keeps {need} pages, more than the table's {max_pages}")
+            take += sum(self._users[p] > 1 for p in self._pages[s][:need])
+        if take > len(self._free):
+            raise OutOfPages(f"{take} pages wanted, {len(self._free)} free")
+        table = np.full((len(seqs), int(max_pages)), -1, dtype=np.int32)
+        gone = []
+        # by the holders before the call: a page that two of the sequences leave is read by both
+        shared = {p for s in seqs for p in self._pages[s] if self._users[p] > 1}
+        for i, (s, n) in enumerate(zip(seqs, lengths)):
+            old, need = self._pages[s], -(-n // self.page_size)
+            new = [self._take() if p in shared else p for p in old[:need]]
+            gone += [p for p in old if p not in set(new)]
+            table[i, :need] = new
+            self._pages[s], self._length[s] = new, n
+        for p in gone:
+            self._drop(p)
+        return table
 
     def free(self, seq: int) -> None:
         """The sequence and its hold on its pages are gone."""

@@ -491,6 +491,52 @@ int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups
                                const int32_t* prefix_pages, const void* q, const void* k_pages, const void* v_pages,
                                void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The attention weight that each key has gathered, by which keys are evicted:
+ *   weights_out[i, g, j] = (j < kv_lens[i] - n ? decay weights[i, g, j] : 0)
+ *       + sum over the n new tokens t of sequence i that see key j and the
+ *         query heads h of KV head g: exp(scale q[t, h] . k[j] - lse[h, t]),
+ * j < kv_lens[i], with the lse that attn_core_paged_fwd (or _prefix_fwd) of the
+ * same p, q and cache returned.  fp32 [n_seq, h_kv, max_pages * page_size],
+ * each sequence its own row also where sequences share pages; weights_out may
+ * be weights, but must not overlap it otherwise.  The new tokens' own keys
+ * start at 0 whatever weights holds there.  Entries from kv_lens[i] on, and
+ * sequences without new tokens, are left as they were.  A row whose lse is
+ * -inf adds nothing; one whose lse is NaN makes the weights of all keys that
+ * it sees NaN.  decay is finite and not negative.  One kernel, where items of
+ * keys may be cut a second one that adds their parts; the same inputs give
+ * the same bits.  The workspace (256-byte aligned) is 0.3 MB: that of
+ * attn_core_paged_fwd serves. */
+size_t attn_core_paged_weights_workspace_bytes(const attn_core_paged_params* p);
+int attn_core_paged_weights(const attn_core_paged_params* p, const void* q, const void* k_pages, const float* lse,
+                            float decay, const float* weights, float* weights_out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Eviction by gathered weight.  Of the kv_lens[i] keys of sequence i, m =
+ * min(keep[i], kv_lens[i]) stay, for each KV head its own: the last r =
+ * min(recent, m), the first f = min(first, m - r), and of those between the
+ * m - r - f of largest weight (ties to the lower index; NaN is below all).
+ * They keep their order and become the keys 0 .. m - 1: key j's row of K and V
+ * moves to page out_table[i * max_pages + j / page_size] (device; NULL: the
+ * page table itself), its weight to weights_out[i, g, j], and kept[i, g, j] (int32,
+ * like the weights) is the key it was.  Entries from m on are left as they
+ * were, and so are K and V elsewhere.  kv_lens is the caller's to set to m, for
+ * the calls that follow, and a rotation's positions are not the keys' places
+ * any more: new tokens are rotated at their own (attn_core_rope_fwd) and
+ * appended without a table.
+ *
+ * Each page that out_table names (in the places of the m keys) is one that no
+ * page table of the call names, or the one that the sequence's own names in
+ * the same place and no other sequence's does; no two places name one page.
+ * So sequences that share pages move to others (PagePool.shrink).  weights_out may be weights.  keep is in device memory
+ * and may exceed the length (all keys stay); negative entries, and lengths or
+ * pages out of range, are table errors.  p's n_tokens, h_q and cu_seqlens_q are
+ * not used (but checked as ever).  A memset and two kernels; the result is
+ * exact.  Its workspace is about n_seq h_kv max_pages page_size / 8 bytes. */
+size_t attn_core_paged_evict_workspace_bytes(const attn_core_paged_params* p);
+int attn_core_paged_evict(const attn_core_paged_params* p, const int32_t* keep, int32_t first, int32_t recent,
+                          const int32_t* out_table, void* k_pages, void* v_pages, const float* weights,
+                          float* weights_out, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Copies pages inside a cache: page pairs[2i + 1] <- page pairs[2i], in every
  * plane (one per layer and per K or V; a plane holds n_pages pages of
  * page_bytes and starts plane_stride bytes after the one before).  Forking a
