@@ -1124,8 +1124,10 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
     }
     if ((rc = encode_map_tokens(&m.o, o, p->d % 64 ? 32 : 64, p->d, a.group, p->h_kv, p->n_tokens, a.tpt))) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return (groups ? ac::launch_prefix(m, a, *groups, st) : ac::launch_paged(m, a, st)) ? ATTN_CORE_ERR_CUDA
-                                                                                        : ATTN_CORE_OK;
+    const auto u16 = [](const void* x) { return static_cast<const uint16_t*>(x); };
+    const int err = groups ? ac::launch_prefix(m, a, *groups, u16(q), u16(k_pages), u16(v_pages), st)
+                           : ac::launch_paged(m, a, st);
+    return err ? ATTN_CORE_ERR_CUDA : ATTN_CORE_OK;
 }
 
 // (sequence, KV head) lines and their chunks, which the eviction counts in 32 bits

@@ -288,7 +288,7 @@ struct PagedArgs {
     // batches whose sequences share their first pages (prefix.cu; set by its launcher)
     const struct PrefixSeq* plan;
     int32_t n_plan;
-    uint32_t* records;          // where each row's parts lie
+    uint64_t* records;          // where each row's parts lie
     size_t lse_offset;          // of the parts' LSEs in the workspace
 };
 size_t paged_ws_bytes(int d);
@@ -307,7 +307,8 @@ struct PrefixGroups {
     int32_t n;
 };
 size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv);
-int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, cudaStream_t stream);
+int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, const uint16_t* q,
+                  const uint16_t* k_pages, const uint16_t* v_pages, cudaStream_t stream);
 
 // Attention weight that the cache's keys gather (weights.cu).  Maps: q and k only.
 struct WeightsArgs {

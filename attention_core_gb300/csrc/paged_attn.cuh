@@ -241,13 +241,14 @@ __host__ __device__ inline size_t record_at(const PagedTables& t, bool prefix, i
 {
     return ((size_t)(prefix ? t.n_tokens : 0) + tok) * t.h_kv + kv_head;
 }
-constexpr uint32_t kRecordNone = 0, kRecordWhole = 1, kRecordCut = 2, kRecordState = 3, kRecordJoined = 4;
-static_assert(kPagedMaxCtas <= 256, "a record holds CTAs in 8 bits");
-// `row`: the first of the token's rows in its tile
-__device__ __forceinline__ uint32_t make_record(bool whole, bool joined, int first_cta, int last_cta, int row)
+constexpr uint64_t kRecordNone = 0, kRecordWhole = 1, kRecordCut = 2, kRecordState = 3, kRecordJoined = 4,
+                   kRecordFew = 8;
+// `row`: the first of the token's rows in its tile; of a cut tile, who has its first and
+// its last part (CTAs here, warps of the kernel for few rows, kRecordFew)
+__device__ __forceinline__ uint64_t make_record(bool whole, bool joined, int first, int last, int row)
 {
-    return (whole ? kRecordWhole : kRecordCut) | (joined ? kRecordJoined : 0u) | (uint32_t)row << 3 |
-           (uint32_t)first_cta << 10 | (uint32_t)last_cta << 18;
+    return (whole ? kRecordWhole : kRecordCut) | (joined ? kRecordJoined : 0) | (uint64_t)row << 4 |
+           (uint64_t)first << 12 | (uint64_t)last << 32;
 }
 
 // Position in a ring of N slots: the slot, and the parity of its current use.

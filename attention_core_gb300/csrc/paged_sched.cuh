@@ -159,13 +159,14 @@ enum : int32_t {
     kKindAll = 1,       // every row sees every key
     kKindPrefix = 2,    // a group's shared keys
     kKindJoined = 4,    // the rows have keys in two of the plan's sequences
-    kKindBits = 3
+    kKindFew = 8,       // so few rows that the kernel for those has the sequence
+    kKindBits = 4
 };
 struct PrefixSeq {
     int32_t q0, nq, kv;
     int32_t row, page0;     // its keys: from entry page0 of this row of the page table
     int32_t kind;
-    int32_t pad[2];
+    int64_t few_units;      // units of the sequences of few rows up to and with this one
 };
 struct PrefixTables {
     const PrefixSeq* plan;
@@ -174,7 +175,7 @@ struct PrefixTables {
 __host__ __device__ inline SeqTable read_seq(const PrefixTables& t, int seq, int tpt, int)
 {
     const PrefixSeq& p = t.plan[seq];
-    return SeqTable{p.q0, SeqShape{p.nq, p.kv, tpt, !(p.kind & kKindAll)}, false};
+    return SeqTable{p.q0, SeqShape{p.kind & kKindFew ? 0 : p.nq, p.kv, tpt, !(p.kind & kKindAll)}, false};
 }
 
 // A piece of one tile: blocks [j0, j1) of it.
