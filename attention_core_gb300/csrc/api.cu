@@ -1209,7 +1209,8 @@ int attn_core_paged_weights(const attn_core_paged_params* p, const void* q, cons
     a.d = p->d;
     a.causal = p->causal;
     a.group = p->h_q / p->h_kv;
-    a.tpt = ac::paged_tokens_per_tile(a.group);
+    a.rows = ac::weights_tile_rows(a.t);
+    a.tpt = a.rows / a.group;
     a.decay = decay;
     const float scale = (p->scale > 0.0f) ? p->scale : 1.0f / sqrtf((float)p->d);
     a.scale_log2 = scale * 1.44269504088896340736f;

@@ -318,13 +318,15 @@ struct WeightsArgs {
     float* out;                 // may be `in`
     uint8_t* ws;                // weights_ws_bytes()
     int32_t d, causal;
-    int32_t group, tpt;         // as PagedArgs
+    int32_t rows;               // of a row tile (weights_tile_rows)
+    int32_t group, tpt;         // h_q / h_kv, and new tokens per row tile
     float decay, scale_log2;
     uint64_t timeout_ns;
     int32_t inject_timeout;
     int32_t num_sms;
 };
 size_t weights_ws_bytes();
+int weights_tile_rows(const PagedTables& t);
 int launch_weights(const PagedMaps& maps, const WeightsArgs& a, cudaStream_t stream);
 
 // Eviction by gathered attention weight (evict.cu).

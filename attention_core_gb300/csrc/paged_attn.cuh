@@ -67,17 +67,17 @@ namespace {
 constexpr int kFineRows = 32;
 constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
 
-// Layout of a [128 x D] tile of Q, K or V: column chunks of 64 with the 128-byte
+// Layout of a [ROWS x D] tile of Q, K or V: column chunks of 64 with the 128-byte
 // swizzle, then, for D = 96 and 160, one of 32 with the 64-byte swizzle.  (Chunks
 // of 32 throughout, as the core's tiles have, cost 5 TMA boxes a page instead of
 // 3 at D = 160, and small boxes bound the loads: about 40 cycles each.)
-template <int D>
+template <int D, int ROWS = 128>
 struct PagedGeom {
     static constexpr int WIDE = D / 64;                       // chunks of 64 columns
     static constexpr bool NARROW = D % 64 != 0;               // and one of 32
     static constexpr int CHUNKS = WIDE + (NARROW ? 1 : 0);
-    static constexpr uint32_t TILE = 128u * D * 2;
-    static constexpr uint32_t WIDE_BYTES = 128 * 128, OFF_NARROW = WIDE * WIDE_BYTES;
+    static constexpr uint32_t TILE = (uint32_t)ROWS * D * 2;
+    static constexpr uint32_t WIDE_BYTES = ROWS * 128, OFF_NARROW = WIDE * WIDE_BYTES;
     static_assert(D % 32 == 0 && (!NARROW || D % 64 == 32), "head dimension");
     __host__ __device__ static constexpr bool narrow(int ch) { return ch >= WIDE; }
     __host__ __device__ static constexpr uint32_t offset(int ch) { return (uint32_t)ch * WIDE_BYTES; }
@@ -97,7 +97,7 @@ struct PagedGeom {
     }
     __device__ static __forceinline__ uint64_t desc_narrow(uint32_t base, int kk)
     {
-        return desc_plus(smem_desc(base + OFF_NARROW, 128 * 64, 512, 4u), (uint32_t)(kk * 16 * 64) >> 4);
+        return desc_plus(smem_desc(base + OFF_NARROW, ROWS * 64, 512, 4u), (uint32_t)(kk * 16 * 64) >> 4);
     }
 };
 
