@@ -41,7 +41,7 @@ constexpr int kSiteEvict = 64;
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 __host__ __device__ inline int chunks_of(int64_t n) { return (int)((n + kMoveRows - 1) / kMoveRows); }
 
-// Workspace: [0] the next chunk, [1] the most chunks of a line, [2] a wait has run out; per line the ranks of the
+// Workspace: [0] the next chunk, [1] a wait has run out; per line the ranks of the
 // keys 0, 64, 128, ... (and the line's kept keys at the end); a flag for each chunk.
 struct EvictLayout {
     size_t ranks, flags, bytes;
@@ -83,20 +83,21 @@ __device__ __forceinline__ Line read_line(const EvictArgs& a, int seq)
     return l;
 }
 
-struct SelectShared {
-    uint32_t hist[kBins], total[kBins];
+struct alignas(16) SelectShared {
+    uint32_t hist[2][kBins];         // the first pass's two copies; then the histogram and the list of candidates
     uint32_t warp_sum[kSelectWarps];
     uint32_t bin, above;             // of the pass: where H falls, keys above it
-    uint32_t stay[kSelectWarps], tie[kSelectWarps];
+    uint32_t listed;
+    uint32_t warp_tie[kSelectWarps];
     uint32_t block_stay, block_tie;
 };
 
 }  // namespace
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a)
+__global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const EvictArgs a)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ float cache[];
+    extern __shared__ __align__(16) float cache[];        // keys; behind them, in clusters, the added histogram
     __shared__ SelectShared sh;
     const PagedTables& t = a.t;
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -104,63 +105,98 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const size_t length = (size_t)t.max_pages * t.page_size;
     const float* w = a.in + line * length;
-    float* out = a.out + line * length;
-    int32_t* kept = a.kept + line * length;
     int32_t* ranks = a.ranks + (size_t)line * a.per_line;
-    int32_t* flags = a.flags + (size_t)line * a.per_line;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const Line l = read_line(a, seq);
     if (rank == 0 && tid == 0) {
         if (l.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
         ranks[chunks_of(l.n)] = l.m;
-        atomicMax(a.most_chunks, chunks_of(l.m));
+        if (line == 0) {
+            *a.counter = 0u;
+            *a.wait_over = 0;
+        }
     }
-    for (int c = rank * kSelectThreads + tid; c < chunks_of(l.m); c += C * kSelectThreads) flags[c] = 0;
+    {
+        int32_t* flags = a.flags + (size_t)line * a.per_line;
+        for (int c = rank * kSelectThreads + tid; c < chunks_of(l.m); c += C * kSelectThreads) flags[c] = 0;
+    }
 
-    // This block's keys [k0, k1), each warp's run a multiple of 64.
-    const int run = (int)(((int64_t)l.n + (int64_t)C * kSelectWarps * 64 - 1) / ((int64_t)C * kSelectWarps * 64)) * 64;
+    // This block's keys [k0, k1), each warp's run a multiple of 128: four keys a thread at a
+    // time.  (What lies between the line's n and its row's end is read, and not used.)
+    const int run = (int)(((int64_t)l.n + (int64_t)C * kSelectWarps * 128 - 1) / ((int64_t)C * kSelectWarps * 128)) * 128;
     const int64_t share = (int64_t)run * kSelectWarps;
     const int k0 = (int)(rank * share < l.n ? rank * share : l.n), k1 = (int)(k0 + share < l.n ? k0 + share : l.n);
     const bool cached = share <= a.cached;
+    for (int b = tid; b < 2 * kBins; b += kSelectThreads) sh.hist[0][b] = 0;
+    if (tid == 0) sh.listed = 0;
     if (cached)
-        for (int k = k0 + tid; k < k1; k += kSelectThreads) cache[k - k0] = w[k];
-    auto at = [&](int k) { return cached ? cache[k - k0] : w[k]; };
+        for (int k = k0 + 4 * tid; k < k1; k += 4 * kSelectThreads)
+            *reinterpret_cast<float4*>(cache + (k - k0)) = *reinterpret_cast<const float4*>(w + k);
+    auto at = [&](int k) -> float4 {
+        return *reinterpret_cast<const float4*>(cached ? cache + (k - k0) : w + k);
+    };
+    __syncthreads();
 
     // Candidates [lo, hi), of which `want` stay: the threshold and how many ties of it.
     const int lo = l.first, hi = l.n - l.recent;
     uint32_t want = (uint32_t)(l.m - l.first - l.recent), threshold = 0xffffffffu;
     const bool all = l.m == l.n;
     if (!all && want > 0) {                             // (the same for the whole cluster)
-        const int c0 = k0 > lo ? k0 : lo, c1 = k1 < hi ? k1 : hi;
-        uint32_t found = 0, mask = 0;
+        uint32_t found = 0;
+        const int c0 = lo < k0 ? k0 : lo & ~3, c1 = k1 < hi ? k1 : hi;
+        bool listed = false;                            // the candidates left are in the list
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[b] = 0;
-            __syncthreads();
-            for (int k = c0 + tid; k < c1; k += kSelectThreads) {
-                const uint32_t u = ordered(at(k));
-                if ((u & mask) == found) atomicAdd(&sh.hist[u >> shift & (bins - 1)], 1u);
+            if (pass > 0) {
+                for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[0][b] = 0;
+                __syncthreads();
             }
-            const uint32_t* total = sh.hist;
+            if (listed) {
+                for (uint32_t i = tid; i < sh.listed; i += kSelectThreads) {
+                    const uint32_t u = sh.hist[1][i];
+                    if (pass == 1 || (u >> 10) == found >> 10) atomicAdd(&sh.hist[0][u >> shift & (bins - 1)], 1u);
+                }
+            } else {
+                // two copies of the first pass's: weights crowd in few of its bins
+                uint32_t* hist = sh.hist[pass == 0 ? warp & 1 : 0];
+                for (int k = c0 + 4 * tid; k < c1; k += 4 * kSelectThreads) {
+                    const float4 x = at(k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t u = ordered(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w);
+                        const bool open = k + e >= lo && k + e < c1;
+                        if (open && (pass == 0 || u >> (shift + (pass == 1 ? 11 : 10)) == found >> (shift + (pass == 1 ? 11 : 10))))
+                            atomicAdd(hist + (u >> shift & (bins - 1)), 1u);
+                    }
+                }
+            }
+            __syncthreads();
+            const uint32_t* total = sh.hist[0];
+            const bool second = pass == 0;              // copy to be added
             if (C > 1) {
                 // each block adds up a share of the bins and tells the others
+                uint32_t* sum_of = reinterpret_cast<uint32_t*>(cache) + a.cached;
                 cluster.sync();
                 const int mine = kBins / C;
                 for (int b = rank * mine + tid; b < (rank + 1) * mine; b += kSelectThreads) {
                     uint32_t s = 0;
-                    for (int r = 0; r < C; ++r) s += cluster.map_shared_rank(sh.hist, r)[b];
-                    for (int r = 0; r < C; ++r) cluster.map_shared_rank(sh.total, r)[b] = s;
+                    for (int r = 0; r < C; ++r) {
+                        const uint32_t* h = cluster.map_shared_rank(&sh.hist[0][0], r);
+                        s += h[b] + (second ? h[kBins + b] : 0u);
+                    }
+                    for (int r = 0; r < C; ++r) cluster.map_shared_rank(sum_of, r)[b] = s;
                 }
                 cluster.sync();
-                total = sh.total;
-            } else {
-                __syncthreads();
+                total = sum_of;
             }
             // sum from the top: thread i has the bins 2047 - 4 i down to 2044 - 4 i
-            uint32_t v[4], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum += v[i] = total[kBins - 1 - 4 * tid - i];
+            uint4 v = reinterpret_cast<const uint4*>(total)[kBins / 4 - 1 - tid];
+            if (C == 1 && second) {
+                const uint4 v1 = reinterpret_cast<const uint4*>(sh.hist[1])[kBins / 4 - 1 - tid];
+                v = make_uint4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
+            }
+            const uint32_t sum = v.x + v.y + v.z + v.w;
             uint32_t upto = sum;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -169,86 +205,133 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             }
             if (lane == 31) sh.warp_sum[warp] = upto;
             __syncthreads();
-            for (int i = 0; i < warp; ++i) upto += sh.warp_sum[i];
+            uint32_t before = lane < warp ? sh.warp_sum[lane] : 0u;
+            before = __reduce_add_sync(0xffffffffu, before);
+            upto += before;
             uint32_t above = upto - sum;
             if (above < want && want <= upto) {
+                const uint32_t n4[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (above < want && want <= above + v[i]) {
+                    if (above < want && want <= above + n4[i]) {
                         sh.bin = (uint32_t)(kBins - 1 - 4 * tid - i);
                         sh.above = above;
                     }
-                    above += v[i];
+                    above += n4[i];
                 }
             }
             __syncthreads();
             found |= sh.bin << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
             want -= sh.above;
-            __syncthreads();
+            if (pass == 0) {
+                // the keys of the bin that was found, into a list, if they are few (a block by
+                // itself; its list's overflow, or a longer one, has the passes go over all keys)
+                for (int k = c0 + 4 * tid; k - 4 * lane < c1; k += 4 * kSelectThreads) {
+                    uint32_t u[4], n = 0;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < c1) x = at(k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = ordered(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w);
+                        n += k + e >= lo && k + e < c1 && u[e] >> 21 == found >> 21;
+                    }
+                    if (!__any_sync(0xffffffffu, n > 0)) continue;
+                    uint32_t place = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o *= 2) {
+                        const uint32_t y = __shfl_up_sync(0xffffffffu, place, o);
+                        if (lane >= o) place += y;
+                    }
+                    uint32_t base = 0;
+                    if (lane == 31) base = atomicAdd(&sh.listed, place);
+                    place += __shfl_sync(0xffffffffu, base, 31) - n;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (k + e >= lo && k + e < c1 && u[e] >> 21 == found >> 21) {
+                            if (place < kBins) sh.hist[1][place] = u[e];
+                            ++place;
+                        }
+                }
+                __syncthreads();
+                listed = sh.listed <= kBins;
+            } else {
+                __syncthreads();
+            }
         }
         threshold = found;
-    } else {
-        __syncthreads();
     }
     const uint32_t ties = want;                          // keys at the threshold that stay, the first ones
 
-    // What stays of each warp's run, in order.
+    // What stays of each warp's run, in order: keys that stay for certain, and ties.
     const int w0 = k0 + warp * run < k1 ? k0 + warp * run : k1, w1 = w0 + run < k1 ? w0 + run : k1;
-    auto classes = [&](int k, float x, uint32_t& stay, uint32_t& tie) {
-        const bool sure = k < w1 && (all || k < lo || k >= hi);
-        const bool open = k < w1 && !sure;
-        const uint32_t u = open ? ordered(x) : 0u;
-        stay = __ballot_sync(0xffffffffu, sure || (open && u > threshold));
-        tie = __ballot_sync(0xffffffffu, open && u == threshold);
+    // bits e and e + 4: key k + e stays, is a tie
+    auto classes = [&](int k, const float4& x) -> uint32_t {
+        uint32_t c = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = k + e < w1, sure = all || k + e < lo || k + e >= hi;
+            const uint32_t u = ordered(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w);
+            if (in && (sure || u > threshold)) c |= 1u << e;
+            if (in && !sure && u == threshold) c |= 16u << e;
+        }
+        return c;
     };
     uint32_t stays = 0, tied = 0;
-    for (int k = w0; k < w1; k += 32) {
-        uint32_t s, e;
-        classes(k + lane, k + lane < w1 ? at(k + lane) : 0.f, s, e);
-        stays += __popc(s);
-        tied += __popc(e);
+    for (int k = w0 + 4 * lane; k < w1; k += 128) {
+        const uint32_t c = classes(k, at(k));
+        stays += __popc(c & 15u);
+        tied += __popc(c >> 4);
     }
+    stays = __reduce_add_sync(0xffffffffu, stays);
+    tied = __reduce_add_sync(0xffffffffu, tied);
     if (lane == 0) {
-        sh.stay[warp] = stays;
-        sh.tie[warp] = tied;
+        sh.warp_sum[warp] = stays;
+        sh.warp_tie[warp] = tied;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t s = 0, e = 0;
-        for (int i = 0; i < kSelectWarps; ++i) {
-            s += sh.stay[i];
-            e += sh.tie[i];
+    if (warp == 0) {
+        const uint32_t s = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? sh.warp_sum[lane] : 0u);
+        const uint32_t e = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? sh.warp_tie[lane] : 0u);
+        if (lane == 0) {
+            sh.block_stay = s;
+            sh.block_tie = e;
         }
-        sh.block_stay = s;
-        sh.block_tie = e;
     }
+    uint32_t stay0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
+    uint32_t tie0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_tie[lane] : 0u);
     if (C > 1) cluster.sync();                           // also: every block has read its keys
-    uint32_t stay0 = 0, tie0 = 0;
     for (int r = 0; r < rank; ++r) {
         stay0 += *cluster.map_shared_rank(&sh.block_stay, r);
         tie0 += *cluster.map_shared_rank(&sh.block_tie, r);
     }
-    for (int i = 0; i < warp; ++i) {
-        stay0 += sh.stay[i];
-        tie0 += sh.tie[i];
-    }
-    for (int k = w0; k < w1; k += 32) {
-        const int key = k + lane;
-        const float x = key < w1 ? at(key) : 0.f;
-        uint32_t s, e;
-        classes(key, x, s, e);
-        if (lane == 0 && k % kMoveRows == 0) ranks[k / kMoveRows] = (int32_t)(stay0 + (tie0 < ties ? tie0 : ties));
-        const uint32_t before = (1u << lane) - 1;
-        const uint32_t tb = tie0 + __popc(e & before);
-        const bool stay = (s >> lane & 1) || ((e >> lane & 1) && tb < ties);
-        if (stay) {
-            const uint32_t j = stay0 + __popc(s & before) + (tb < ties ? tb : ties);
-            kept[j] = key;
-            if (cached) out[j] = x;
+    float* out = a.out + line * length;
+    int32_t* kept = a.kept + line * length;
+    for (int k = w0 + 4 * lane; k - 4 * lane < w1; k += 128) {
+        const float4 x = k < w1 ? at(k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t c = classes(k, x);
+        uint32_t upto = __popc(c & 15u) | __popc(c >> 4) << 16;          // of 128 keys: no carry
+        const uint32_t own = upto;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        stay0 += __popc(s);
-        tie0 += __popc(e);
+        const uint32_t step = __shfl_sync(0xffffffffu, upto, 31);
+        uint32_t s = stay0 + ((upto - own) & 0xffffu), e = tie0 + ((upto - own) >> 16);
+        if ((lane & 15) == 0 && k < w1) ranks[k / kMoveRows] = (int32_t)(s + (e < ties ? e : ties));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool tie = c >> (4 + i) & 1;
+            if ((c >> i & 1) || (tie && e < ties)) {
+                const uint32_t j = s + (e < ties ? e : ties);
+                kept[j] = k + i;
+                if (cached) out[j] = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+            }
+            s += c >> i & 1;
+            e += tie;
+        }
+        stay0 += step & 0xffffu;
+        tie0 += step >> 16;
     }
     if (C > 1) cluster.sync();                           // no block leaves while another reads its counts
     if (!cached) {
@@ -271,12 +354,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     constexpr int U = D / 8, LOADS = 2 * kMoveRows * U / kMoveThreads;
     static_assert(2 * kMoveRows * U % kMoveThreads == 0, "units per thread");
     __shared__ int64_t src[kMoveRows], dst[kMoveRows];    // rows of the cache; equal: stays
-    __shared__ int ticket, within, wait_first, wait_last, leave;
+    __shared__ int ticket, within, wait_first, wait_last, leave, most;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedTables& t = a.t;
     const int tid = threadIdx.x, lines = t.n_seq * t.h_kv;
     const size_t length = (size_t)t.max_pages * t.page_size;
-    const int most = *a.most_chunks;
+    // chunks of the longest line
+    if (tid == 0) most = 0;
+    __syncthreads();
+    int longest = 0;
+    for (int s = tid; s < t.n_seq; s += kMoveThreads) {
+        const int m = read_line(a, s).m;
+        longest = m > longest ? m : longest;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if ((tid & 31) == 0) atomicMax(&most, chunks_of(longest));
+    __syncthreads();
     for (;;) {
         if (tid == 0) {
             ticket = (int)atomicAdd(a.counter, 1u);
@@ -370,21 +463,18 @@ int launch_evict_t(const EvictArgs& args, cudaStream_t st)
     const int64_t lines = (int64_t)a.t.n_seq * a.t.h_kv, length = (int64_t)a.t.max_pages * a.t.page_size;
     const EvictLayout lay = evict_layout(lines, length);
     a.counter = reinterpret_cast<uint32_t*>(a.ws);
-    a.most_chunks = reinterpret_cast<int32_t*>(a.ws) + 1;
-    a.wait_over = reinterpret_cast<int32_t*>(a.ws) + 2;
+    a.wait_over = reinterpret_cast<int32_t*>(a.ws) + 1;
     a.ranks = reinterpret_cast<int32_t*>(a.ws + lay.ranks);
     a.flags = reinterpret_cast<int32_t*>(a.ws + lay.flags);
     a.per_line = lay.per_line;
-    cudaError_t e = cudaMemsetAsync(a.ws, 0, 12, st);
-    if (e != cudaSuccess) return (int)e;
-
+    cudaError_t e;
     // Blocks per line: more while they have thousands of keys each and the lines leave
     // processors idle.
     int C = 1;
     while (C < 8 && length / C > 4096 && lines * C * 2 <= a.num_sms) C *= 2;
     const int64_t share = ((length + (int64_t)C * kSelectWarps * 64 - 1) / ((int64_t)C * kSelectWarps * 64)) * 64 * kSelectWarps;
     a.cached = (int)(share < kMostCached ? share : kMostCached);
-    const uint32_t smem = (uint32_t)a.cached * sizeof(float);
+    const uint32_t smem = (uint32_t)a.cached * sizeof(float) + (C > 1 ? kBins * sizeof(uint32_t) : 0);
     if ((e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
         cudaSuccess)
         return (int)e;

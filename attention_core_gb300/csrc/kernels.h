@@ -290,6 +290,8 @@ struct PagedArgs {
     int32_t n_plan;
     uint64_t* records;          // where each row's parts lie
     size_t lse_offset;          // of the parts' LSEs in the workspace
+    const int64_t* many_units;  // of the sequences of many rows
+    int32_t few_waits;          // it follows the plan, not the kernel for many rows
 };
 size_t paged_ws_bytes(int d);
 int paged_tokens_per_tile(int group);
@@ -347,7 +349,6 @@ struct EvictArgs {
     int32_t num_sms;
     // set by the launcher: parts of the workspace, and keys that a block can hold
     uint32_t* counter;
-    int32_t* most_chunks;
     int32_t* wait_over;
     int32_t* ranks;
     int32_t* flags;

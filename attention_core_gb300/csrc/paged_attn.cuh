@@ -123,10 +123,23 @@ struct PagedCfg {
     static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
     static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
     static constexpr uint32_t SMEM = OFF_XCH + XCH_BYTES + 1024;
-    static_assert(SMEM <= 227 * 1024, "shared memory budget");
+    // batches of shared pages turn rows over in shared memory on their way to the workspace
+    // (2 KB a warp; the O stage is free there)
+    static constexpr uint32_t OFF_TURN = STAGE_O ? OFF_OST : OFF_XCH + XCH_BYTES;
+    static constexpr uint32_t SMEM_PREFIX = STAGE_O ? SMEM : SMEM + 8 * 2048;
+    static_assert(SMEM_PREFIX <= 227 * 1024, "shared memory budget");
     static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O = 256, T_O1 = 256 + D, T_X = 256 + D;
     static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
 };
+
+// What a block of 128 keys and 128 rows costs a processor, in units of the kernel for few
+// rows (64 keys): 1.1 us against 0.3, its 32 KB at a processor's best of 107 GB/s.
+constexpr int64_t kManyUnitCost = 2;
+__device__ __forceinline__ int64_t many_ctas(int64_t many, int64_t few, int64_t ctas)
+{
+    const int64_t n = few > 0 ? quot(ctas * kManyUnitCost * many, kManyUnitCost * many + few) : ctas;
+    return n > 0 ? n : 1;
+}
 
 constexpr int kJobs = 4;
 // Barriers of block g's ring slots (g % SK for K, g % SV for V) serve every role that
@@ -439,7 +452,12 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
         all_tiles += bars->warp_tiles[w];
     }
     const bool hand_out = !PREFIX && a.counter && hand_out_tiles(total, all_tiles >> 32, all_tiles & 0xffffffff, gridDim.x, D);
-    int64_t per = quot(total + gridDim.x - 1, gridDim.x);
+    // beside the kernel for few rows, as many CTAs as this one's share of the work (prefix.cu)
+    int64_t ctas = gridDim.x;
+    if constexpr (PREFIX) {
+        ctas = many_ctas(total, a.plan[a.n_plan - 1].few_units, gridDim.x);
+    }
+    int64_t per = quot(total + ctas - 1, ctas);
     per = per > kMinUnits ? per : kMinUnits;
     const int64_t u0 = (int64_t)blockIdx.x * per;
     const int64_t u1 = u0 + per < total ? u0 + per : total;
@@ -933,7 +951,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             // a row that saw a NaN score is NaN, and has to reach O and the LSE.)
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
             // a full tile's O leaves through the stage: free once its last store has read it
-            const bool staged = C::STAGE_O && g.whole && !joined && g.n_tok == a.tpt;
+            const bool staged = C::STAGE_O && !PREFIX && g.whole && g.n_tok == a.tpt;
             if (staged && h == 0 && r == 0) bulk_wait_read0();
             if constexpr (C::SPLIT) {
                 if (h == 1) xch[r] = make_float2(m_run, l_run);
@@ -992,6 +1010,20 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                                 make_record(g.whole, joined, blockIdx.x, g.last_cta, r);
                     }
                 }
+                // batches of shared pages: the rows that this lane stores a piece of, 8 rows apart
+                size_t turned[4] = {};
+                uint32_t turned_live = 0;
+                if constexpr (PREFIX) {
+                    if (!done) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r2 = (r & ~31) + (int)lane / 4 + 8 * i, t2 = r2 / group;
+                            turned[i] = g.whole ? whole_row(t, g.m & kKindPrefix, g.q_tok + t2, g.head * group + r2 - t2 * group)
+                                                : part_row(blockIdx.x, g.from_start ? 1 : 0) + r2;
+                            if (t2 < g.n_tok && r2 < a.tpt * group) turned_live |= 1u << i;
+                        }
+                    }
+                }
                 // The TMEM loads are warp-collective; only the stores are guarded.
 #pragma unroll 1
                 for (int c32 = h; c32 < D / 32; c32 += 2) {
@@ -1020,6 +1052,28 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                                              w[1], w[2], w[3]);
                             else if (live)
                                 reinterpret_cast<uint4*>(orow)[c32 * 4 + u4] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if constexpr (PREFIX) {
+                        // 16 columns of 32 rows at a time, so that the stores are of whole sectors
+                        // (a thread storing its own row cost 2 us a tile)
+                        const uint32_t turn = sb + C::OFF_TURN + (warp - 4) * 2048;
+#pragma unroll
+                        for (int c16 = 0; c16 < 2; ++c16) {
+                            __syncwarp();
+#pragma unroll
+                            for (int u4 = 0; u4 < 4; ++u4)
+                                st_shared_v4(turn + lane * 64 + ((u4 ^ (lane >> 1 & 3)) * 16),
+                                             __float_as_uint(f[16 * c16 + 4 * u4]), __float_as_uint(f[16 * c16 + 4 * u4 + 1]),
+                                             __float_as_uint(f[16 * c16 + 4 * u4 + 2]), __float_as_uint(f[16 * c16 + 4 * u4 + 3]));
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t r2 = lane / 4 + 8 * i;
+                                const uint4 x = ld_shared_v4(turn + r2 * 64 + (((lane & 3) ^ (r2 >> 1 & 3)) * 16));
+                                if (turned_live >> i & 1)
+                                    reinterpret_cast<uint4*>(reinterpret_cast<float*>(a.ws) + turned[i] * D + c32 * 32 +
+                                                             16 * c16)[lane & 3] = x;
+                            }
                         }
                     } else if (live) {
 #pragma unroll

@@ -29,7 +29,7 @@ __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~(size
 // few rows] of d floats, their base-2 LSEs, the records, the plan.
 constexpr int kFewWarps = kPagedMaxCtas * 8;      // of the kernel for few rows, at most
 struct PrefixLayout {
-    size_t lse, records, plan, bytes;
+    size_t lse, records, plan, many, bytes;
 };
 __host__ __device__ inline size_t few_row(const PagedTables& t, int warp, int slot)
 {
@@ -42,7 +42,8 @@ inline PrefixLayout prefix_layout(int d, int n_seq, int n_groups, int64_t n_toke
     l.lse = align256(rows * d * sizeof(float));
     l.records = align256(l.lse + rows * sizeof(float));
     l.plan = align256(l.records + 2 * (size_t)n_tokens * h_kv * sizeof(uint64_t));
-    l.bytes = align256(l.plan + ((size_t)n_seq + n_groups) * sizeof(PrefixSeq));
+    l.many = align256(l.plan + ((size_t)n_seq + n_groups) * sizeof(PrefixSeq));
+    l.bytes = l.many + 256;
     return l;
 }
 
@@ -57,89 +58,124 @@ __host__ __device__ inline int few_blocks(int kv) { return kv > 0 ? (int)(((uint
 // all its sequences hold before their first new token, in whole pages, so that no row's
 // mask ends inside it; a group of one sequence shares nothing.  Groups out of order or
 // out of range are reported and share nothing either: the attention is right without.
+// The sequences' lengths are read once and kept in shared memory (the first kPlanNear of
+// them: all, in any usual batch), since this kernel's time is what the others wait for.
+constexpr int kPlanNear = 1024;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PagedTables t, int tpt, int causal,
                                                                    const PrefixGroups gr, PrefixSeq* plan,
-                                                                   uint64_t* records, int n_records)
+                                                                   uint64_t* records, int n_records,
+                                                                   int64_t* many_units)
 {
+    __shared__ int4 near[kPlanNear];                 // first token, new tokens, keys, shared pages of a sequence
+    __shared__ int64_t warp_units[kPlanThreads / 32];
+    __shared__ unsigned long long many;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = (int)(blockIdx.x * blockDim.x + threadIdx.x); i < n_records; i += (int)(gridDim.x * blockDim.x))
-        records[i] = kRecordNone;
-    if (blockIdx.x) return;
-    const int kind = causal ? 0 : kKindAll;
-    for (int s = (int)threadIdx.x; s < t.n_seq; s += kPlanThreads) {
-        const SeqTable q = read_seq(t, s, tpt, causal);
-        if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
-        plan[gr.n + s] = PrefixSeq{q.q0, q.s.nq, q.s.kv, s, 0, kind, {}};
-    }
-    bool bad = false;
-    for (int g = (int)threadIdx.x; g < gr.n; g += kPlanThreads)
-        bad |= gr.starts[g] < 0 || gr.starts[g + 1] < gr.starts[g] || gr.starts[g + 1] > t.n_seq || gr.pages[g] < 0;
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0 && t.status) atomicCAS(t.status, 0, kStatusTable);
-    const int lane = threadIdx.x & 31;
-    for (int g = (int)(threadIdx.x >> 5); g < gr.n; g += kPlanThreads / 32) {
-        PrefixSeq shared{};
-        if (!bad) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0) {
+        bool bad = false;
+        for (int g = tid; g < gr.n; g += kPlanThreads) {
             const int s0 = gr.starts[g], s1 = gr.starts[g + 1];
-            int pages = gr.pages[g] < t.max_pages ? gr.pages[g] : t.max_pages;
-            int members = 0, q0 = INT32_MAX, q1 = 0, row = INT32_MAX;
-            for (int s = s0 + lane; s < s1; s += 32) {
-                const SeqTable q = read_seq(t, s, tpt, causal);
-                if (q.s.nq <= 0) continue;
-                const int old = q.s.kv > q.s.nq ? (q.s.kv - q.s.nq) >> t.page_shift : 0;
-                pages = old < pages ? old : pages;
-                ++members;
-                q0 = q.q0 < q0 ? q.q0 : q0;
-                q1 = q.q0 + q.s.nq > q1 ? q.q0 + q.s.nq : q1;
-                row = s < row ? s : row;
-            }
-            members = __reduce_add_sync(0xffffffffu, members);
-            pages = __reduce_min_sync(0xffffffffu, pages);
-            q0 = __reduce_min_sync(0xffffffffu, q0);
-            q1 = __reduce_max_sync(0xffffffffu, q1);
-            row = __reduce_min_sync(0xffffffffu, row);
-            if (members > 1 && pages > 0) {
-                shared = PrefixSeq{q0, q1 - q0, pages << t.page_shift, row, 0, kKindAll | kKindPrefix | kKindJoined, {}};
+            bad |= s0 < 0 || s1 < s0 || s1 > t.n_seq || gr.pages[g] < 0;
+        }
+        for (int s = tid; s < t.n_seq && s < kPlanNear; s += kPlanThreads) {
+            const SeqTable q = read_seq(t, s, tpt, causal);
+            if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
+            near[s] = make_int4(q.q0, q.s.nq, q.s.kv, 0);
+        }
+        if (tid == 0) many = 0;
+        auto seq = [&](int s) -> int4 {
+            if (s < kPlanNear) return near[s];
+            const SeqTable q = read_seq(t, s, tpt, causal);
+            if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
+            return make_int4(q.q0, q.s.nq, q.s.kv, 0);
+        };
+        // (beyond kPlanNear the shared pages go by way of the plan itself)
+        for (int s = kPlanNear + tid; s < t.n_seq; s += kPlanThreads) plan[gr.n + s].page0 = 0;
+        bad = __syncthreads_or(bad);
+        if (bad && tid == 0 && t.status) atomicCAS(t.status, 0, kStatusTable);
+        for (int g = warp; g < gr.n; g += kPlanThreads / 32) {
+            PrefixSeq shared{};
+            if (!bad) {
+                const int s0 = gr.starts[g], s1 = gr.starts[g + 1];
+                int pages = gr.pages[g] < t.max_pages ? gr.pages[g] : t.max_pages;
+                int members = 0, q0 = INT32_MAX, q1 = 0, row = INT32_MAX;
                 for (int s = s0 + lane; s < s1; s += 32) {
-                    const SeqTable q = read_seq(t, s, tpt, causal);
-                    if (q.s.nq <= 0) continue;
-                    plan[gr.n + s] = PrefixSeq{q.q0, q.s.nq, q.s.kv - (pages << t.page_shift), s, pages,
-                                               kind | kKindJoined, {}};
+                    const int4 q = seq(s);
+                    if (q.y <= 0) continue;
+                    const int old = q.z > q.y ? (q.z - q.y) >> t.page_shift : 0;
+                    pages = old < pages ? old : pages;
+                    ++members;
+                    q0 = q.x < q0 ? q.x : q0;
+                    q1 = q.x + q.y > q1 ? q.x + q.y : q1;
+                    row = s < row ? s : row;
+                }
+                members = __reduce_add_sync(0xffffffffu, members);
+                pages = __reduce_min_sync(0xffffffffu, pages);
+                q0 = __reduce_min_sync(0xffffffffu, q0);
+                q1 = __reduce_max_sync(0xffffffffu, q1);
+                row = __reduce_min_sync(0xffffffffu, row);
+                if (members > 1 && pages > 0) {
+                    shared = PrefixSeq{q0, q1 - q0, pages << t.page_shift, row, 0, kKindAll | kKindPrefix | kKindJoined, 0};
+                    for (int s = s0 + lane; s < s1; s += 32) {
+                        if (s < kPlanNear)
+                            near[s].w = pages;
+                        else
+                            plan[gr.n + s].page0 = pages;
+                    }
                 }
             }
+            if (lane == 0) plan[g] = shared;
         }
-        if (lane == 0) plan[g] = shared;
-    }
-    __syncthreads();
-    // who has the sequence, and the line of the kernel for few rows
-    __shared__ int64_t warp_units[kPlanThreads / 32];
-    const int group = t.h_q / t.h_kv, n = gr.n + t.n_seq;
-    int64_t base = 0;
-    for (int s0 = 0; s0 < n; s0 += kPlanThreads) {
-        const int s = s0 + (int)threadIdx.x;
-        int64_t units = 0;
-        if (s < n) {
-            const PrefixSeq v = plan[s];
-            if (few_rows(v.nq, group)) {
-                plan[s].kind = v.kind | kKindFew;
-                units = (int64_t)few_tiles(v.nq, group) * few_blocks(v.kv) * t.h_kv;
+        __syncthreads();
+        // each sequence's own part, who has it, and the line of the kernel for few rows
+        const int group = t.h_q / t.h_kv, n = gr.n + t.n_seq;
+        int64_t base = 0;
+        for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+            const int i = i0 + tid, s = i - gr.n;
+            int64_t units = 0;
+            PrefixSeq v{};
+            if (i < n) {
+                if (s < 0) {
+                    v = plan[i];
+                } else {
+                    const int4 q = seq(s);
+                    const int pages = q.y <= 0 ? 0 : s < kPlanNear ? q.w : plan[i].page0;
+                    v = PrefixSeq{q.x, q.y, q.z - (pages << t.page_shift), s, pages,
+                                  (causal ? 0 : kKindAll) | (pages ? kKindJoined : 0), 0};
+                }
+                if (few_rows(v.nq, group)) {
+                    v.kind |= kKindFew;
+                    units = (int64_t)few_tiles(v.nq, group) * few_blocks(v.kv) * t.h_kv;
+                } else if (v.nq > 0) {
+                    const SeqShape q{v.nq, v.kv, tpt, !(v.kind & kKindAll)};
+                    atomicAdd(&many, (unsigned long long)q.units(q.tiles()) * t.h_kv);
+                }
             }
-        }
-        int64_t upto = units;
+            int64_t upto = units;
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            if (lane == 31) warp_units[warp] = upto;
+            __syncthreads();
+            int64_t before = 0, all = 0;
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                const int64_t x = warp_units[w];
+                if (w < warp) before += x;
+                all += x;
+            }
+            if (i < n) {
+                v.few_units = base + before + upto;
+                plan[i] = v;
+            }
+            base += all;
+            __syncthreads();
         }
-        if (lane == 31) warp_units[threadIdx.x >> 5] = upto;
-        __syncthreads();
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            if (w < (int)(threadIdx.x >> 5)) upto += warp_units[w];
-        }
-        if (s < n) plan[s].few_units = base + upto;
-        for (int w = 0; w < kPlanThreads / 32; ++w) base += warp_units[w];
-        __syncthreads();
+        if (tid == 0) *many_units = (int64_t)many;
     }
+    for (int i = (int)(blockIdx.x * blockDim.x) + tid; i < n_records; i += (int)(gridDim.x * blockDim.x))
+        records[i] = kRecordNone;
 }
 
 // Attention of sequences of few rows (at most two tiles of 16) over their keys.  A tile
@@ -151,7 +187,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PagedTa
 // layout is the layout that P needs.  Bound by the keys' bytes.  P goes in as two bf16
 // terms, as in paged_attn.cuh's tiles of few rows.
 // The units are blocks of 64 keys of (sequence, KV head, row tile), in equal shares for
-// all warps; pieces of a tile are joined.
+// all warps; pieces of a tile are joined.  The kernel runs beside the one for many rows:
+// that one keeps to as many processors as its part of the work is worth (many_ctas), and
+// this one's blocks of lowest number, which are placed first, find the others free.
 template <int D>
 struct FewCfg {
     static constexpr int UNITS = D / 8;                        // of 16 bytes a row
@@ -162,6 +200,20 @@ struct FewCfg {
     static constexpr uint32_t SMEM = WARPS * STAGES * STAGE;
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
+
+// The plan was written before this kernel began, but it waits for no kernel before it
+// reads: past L1.
+__device__ __forceinline__ PrefixSeq load_plan(const PrefixSeq* p)
+{
+    static_assert(sizeof(PrefixSeq) == 32, "two loads");
+    union {
+        int4 x[2];
+        PrefixSeq v;
+    } u;
+    u.x[0] = __ldcg(reinterpret_cast<const int4*>(p));
+    u.x[1] = __ldcg(reinterpret_cast<const int4*>(p) + 1);
+    return u.v;
+}
 
 struct FewSegment {
     PrefixSeq v;
@@ -177,22 +229,29 @@ struct FewWalk {
     int s, head, m, b;
     PrefixSeq v;
 
-    __device__ __forceinline__ void start(const PrefixSeq* plan, int n_plan, int h_kv, int group, int64_t u0, int64_t u1)
+    // Unit u0 is in the first of the sequences lo .. hi - 1 whose units reach beyond it.
+    __device__ __forceinline__ void start(const PrefixSeq* plan, int lo, int hi, int h_kv, int group, int64_t u0, int64_t u1)
     {
         at = u0;
         end = u1;
-        // the first sequence with units beyond u0, 32 candidates a round
-        int lo = 0, hi = n_plan;
         const int lane = threadIdx.x & 31;
-        while (hi - lo > 1) {
+        while (hi - lo > 32) {                             // 32 candidates a round
             const int step = (hi - lo + 31) / 32;
             const int last = lo + (lane + 1) * step - 1 < hi ? lo + (lane + 1) * step - 1 : hi - 1;
-            const uint32_t beyond = __ballot_sync(0xffffffffu, plan[last].few_units > u0);
+            const uint32_t beyond = __ballot_sync(0xffffffffu, __ldcg(&plan[last].few_units) > u0);
             lo += (__ffs(beyond) - 1) * step;
             hi = lo + step < hi ? lo + step : hi;
         }
-        s = lo;
-        v = plan[s];
+        const PrefixSeq c = load_plan(plan + (lo + lane < hi ? lo + lane : hi - 1));
+        const int src = __ffs(__ballot_sync(0xffffffffu, c.few_units > u0)) - 1;
+        s = lo + src;
+        v.q0 = __shfl_sync(0xffffffffu, c.q0, src);
+        v.nq = __shfl_sync(0xffffffffu, c.nq, src);
+        v.kv = __shfl_sync(0xffffffffu, c.kv, src);
+        v.row = __shfl_sync(0xffffffffu, c.row, src);
+        v.page0 = __shfl_sync(0xffffffffu, c.page0, src);
+        v.kind = __shfl_sync(0xffffffffu, c.kind, src);
+        v.few_units = __shfl_sync(0xffffffffu, c.few_units, src);
         const int blocks = few_blocks(v.kv), per_head = few_tiles(v.nq, group) * blocks;
         const int64_t rel = u0 - (v.few_units - (int64_t)per_head * h_kv);
         head = (int)quot(rel, per_head);
@@ -216,7 +275,7 @@ struct FewWalk {
                             at = end;
                             return false;
                         }
-                        v = plan[s];
+                        v = load_plan(plan + s);
                     } while (!(v.kind & kKindFew));
                     blocks = few_blocks(v.kv);
                 }
@@ -280,18 +339,28 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.group;
     const uint32_t ring = smem_u32(smem_raw) + warp * C::STAGES * C::STAGE;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.few_waits) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // neighbouring shares on different processors
-    const int me = warp * (int)gridDim.x + (int)blockIdx.x;
-    const int64_t total = a.plan[a.n_plan - 1].few_units;
-    int64_t per = quot(total + (int64_t)gridDim.x * C::WARPS - 1, (int64_t)gridDim.x * C::WARPS);
+    // The line's length, and 32 places of it in the same look: this warp's share starts
+    // between two of them.
+    const int step = (a.n_plan + 31) / 32;
+    const int last = (lane + 1) * step < a.n_plan ? (lane + 1) * step - 1 : a.n_plan - 1;
+    const int64_t upto = __ldcg(&a.plan[last].few_units), many = __ldcg(a.many_units);
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int blocks = (int)gridDim.x - (many > 0 ? (int)many_ctas(many, total, gridDim.x) : 0);
+    const int n_blocks = blocks > 0 ? blocks : 1;
+    const int me = warp * n_blocks + (int)blockIdx.x;      // neighbouring shares on different processors
+    int64_t per = quot(total + (int64_t)n_blocks * C::WARPS - 1, (int64_t)n_blocks * C::WARPS);
     per = per > 1 ? per : 1;
     const int64_t u0 = me * per, u1 = u0 + per < total ? u0 + per : total;
-    if (u0 >= u1) return;
+    if ((int)blockIdx.x >= n_blocks || u0 >= u1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int lo = (__ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1) * step;
     FewWalk load_walk;
     load_walk.per = per;
-    load_walk.start(a.plan, a.n_plan, t.h_kv, group, u0, u1);
+    load_walk.start(a.plan, lo, lo + step < a.n_plan ? lo + step : a.n_plan, t.h_kv, group, u0, u1);
     FewWalk walk = load_walk;
 
     // ---- loads: 16 keys a step, the entries of the page table 32 at a time
@@ -480,6 +549,8 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
         }
     }
     cp_async_wait<0>();
+    // the kernel that joins waits for this one, which therefore ends after the one for many rows
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // A warp per (new token, query head): the parts of the row's own keys' tile, then of
@@ -495,8 +566,9 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     const int tok = (int)(row / t.h_q), head = (int)(row % t.h_q);
     const int kv_head = head / a.group, r_head = head % a.group;
     const uint64_t own = a.records[record_at(t, false, tok, kv_head)];
+    uint64_t shared = a.records[record_at(t, true, tok, kv_head)];       // meaningless where nothing is shared
     if ((own & kRecordState) == kRecordNone) return;
-    const uint64_t shared = own & kRecordJoined ? a.records[record_at(t, true, tok, kv_head)] : kRecordNone;
+    if (!(own & kRecordJoined)) shared = kRecordNone;
     auto first = [](uint64_t r) -> int { return (int)(r >> 12 & 0xfffff); };
     auto count = [&](uint64_t r) -> int {
         const uint64_t state = r & kRecordState;
@@ -513,7 +585,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     };
     const float* lse = reinterpret_cast<const float*>(a.ws + a.lse_offset);
     const float* rows = reinterpret_cast<const float*>(a.ws) + lane;
-    constexpr int E = D / 32, AHEAD = 4;
+    constexpr int E = D / 32, AHEAD = 8;
     float x[AHEAD][E];
     auto load = [&](int p0) {
 #pragma unroll
@@ -589,17 +661,19 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     a.n_plan = g.n + t.n_seq;
     a.records = reinterpret_cast<uint64_t*>(a.ws + l.records);
     a.lse_offset = l.lse;
+    a.many_units = reinterpret_cast<const int64_t*>(a.ws + l.many);
     const int n_records = t.n_tokens * t.h_kv;
     const int clearing = n_records / (kPlanThreads * 8);
     prefix_plan_kernel<<<(unsigned)(clearing < 1 ? 1 : clearing < 64 ? clearing : 64), kPlanThreads, 0, st>>>(
-        t, a.tpt, a.causal, g, plan, a.records, n_records);
+        t, a.tpt, a.causal, g, plan, a.records, n_records, reinterpret_cast<int64_t*>(a.ws + l.many));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return (int)e;
 
+    a.few_waits = 1;
     // batches whose new tokens all together are few rows have no others (the kernel for
     // those has no wait that the test hook could let run out)
     if (!few_rows(t.n_tokens, a.group) || a.inject_timeout) {
-        constexpr uint32_t smem = PagedCfg<D>::SMEM;
+        constexpr uint32_t smem = PagedCfg<D>::SMEM_PREFIX;
         // (of head groups that the other kernel does not take, single tokens are tiles of few rows)
         const bool fine = a.group > 16 && (int64_t)t.n_tokens * a.group <= (int64_t)kFineRows * t.n_seq;
         auto kern = fine ? paged_attn_kernel<D, true, true> : paged_attn_kernel<D, false, true>;
@@ -611,6 +685,7 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
         int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
         if (want < grid) grid = want;
         if ((e = launch_behind(kern, dim3((unsigned)grid), kThreads, smem, st, m, a)) != cudaSuccess) return (int)e;
+        a.few_waits = 0;
     }
     if (a.group <= 16) {
         using C = FewCfg<D>;
