@@ -1098,7 +1098,6 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
     if (workspace_bytes < need) return ATTN_CORE_ERR_WORKSPACE_TOO_SMALL;
     if (p->n_tokens == 0) return ATTN_CORE_OK;
     if ((rc = check_device())) return rc;
-    if ((rc = get_encoder())) return rc;
     ac::PagedArgs a{};
     a.t = paged_tables(p);
     a.o = static_cast<uint16_t*>(o);
@@ -1114,7 +1113,9 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
     a.inject_timeout = (p->flags & ATTN_CORE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
     if ((rc = device_sms(&a.num_sms))) return rc;
     ac::PagedMaps m;
-    for (int i = 0; i < (p->d % 64 ? 2 : 1); ++i) {
+    const bool maps = !groups || !ac::prefix_all_few(a);
+    if (maps && (rc = get_encoder())) return rc;
+    for (int i = 0; maps && i < (p->d % 64 ? 2 : 1); ++i) {
         const int cw = i ? 32 : 64;
         const int64_t pages = (int64_t)p->n_pages * p->h_kv;
         if ((rc = encode_map_tokens(&m.q[i], q, cw, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)) ||
@@ -1122,7 +1123,8 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
             (rc = encode_map_pages(&m.v[i], v_pages, cw, p->d, p->page_size, pages)))
             return rc;
     }
-    if ((rc = encode_map_tokens(&m.o, o, p->d % 64 ? 32 : 64, p->d, a.group, p->h_kv, p->n_tokens, a.tpt))) return rc;
+    if (maps && (rc = encode_map_tokens(&m.o, o, p->d % 64 ? 32 : 64, p->d, a.group, p->h_kv, p->n_tokens, a.tpt)))
+        return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const auto u16 = [](const void* x) { return static_cast<const uint16_t*>(x); };
     const int err = groups ? ac::launch_prefix(m, a, *groups, u16(q), u16(k_pages), u16(v_pages), st)

@@ -84,17 +84,16 @@ __device__ __forceinline__ Line read_line(const EvictArgs& a, int seq)
 }
 
 struct alignas(16) SelectShared {
-    uint32_t hist[2][kBins];         // the first pass's two copies; then the histogram and the list of candidates
+    uint32_t hist[2][kBins];         // two copies in the first pass
     uint32_t warp_sum[kSelectWarps];
     uint32_t bin, above;             // of the pass: where H falls, keys above it
-    uint32_t listed;
     uint32_t warp_tie[kSelectWarps];
     uint32_t block_stay, block_tie;
 };
 
 }  // namespace
 
-__global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const EvictArgs a)
+__global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const EvictArgs a)
 {
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) float cache[];        // keys; behind them, in clusters, the added histogram
@@ -129,7 +128,6 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
     const int k0 = (int)(rank * share < l.n ? rank * share : l.n), k1 = (int)(k0 + share < l.n ? k0 + share : l.n);
     const bool cached = share <= a.cached;
     for (int b = tid; b < 2 * kBins; b += kSelectThreads) sh.hist[0][b] = 0;
-    if (tid == 0) sh.listed = 0;
     if (cached)
         for (int k = k0 + 4 * tid; k < k1; k += 4 * kSelectThreads)
             *reinterpret_cast<float4*>(cache + (k - k0)) = *reinterpret_cast<const float4*>(w + k);
@@ -145,19 +143,13 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
     if (!all && want > 0) {                             // (the same for the whole cluster)
         uint32_t found = 0;
         const int c0 = lo < k0 ? k0 : lo & ~3, c1 = k1 < hi ? k1 : hi;
-        bool listed = false;                            // the candidates left are in the list
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
             if (pass > 0) {
                 for (int b = tid; b < kBins; b += kSelectThreads) sh.hist[0][b] = 0;
                 __syncthreads();
             }
-            if (listed) {
-                for (uint32_t i = tid; i < sh.listed; i += kSelectThreads) {
-                    const uint32_t u = sh.hist[1][i];
-                    if (pass == 1 || (u >> 10) == found >> 10) atomicAdd(&sh.hist[0][u >> shift & (bins - 1)], 1u);
-                }
-            } else {
+            {
                 // two copies of the first pass's: weights crowd in few of its bins
                 uint32_t* hist = sh.hist[pass == 0 ? warp & 1 : 0];
                 for (int k = c0 + 4 * tid; k < c1; k += 4 * kSelectThreads) {
@@ -223,40 +215,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) evict_select_kernel(const E
             __syncthreads();
             found |= sh.bin << shift;
             want -= sh.above;
-            if (pass == 0) {
-                // the keys of the bin that was found, into a list, if they are few (a block by
-                // itself; its list's overflow, or a longer one, has the passes go over all keys)
-                for (int k = c0 + 4 * tid; k - 4 * lane < c1; k += 4 * kSelectThreads) {
-                    uint32_t u[4], n = 0;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k < c1) x = at(k);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u[e] = ordered(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w);
-                        n += k + e >= lo && k + e < c1 && u[e] >> 21 == found >> 21;
-                    }
-                    if (!__any_sync(0xffffffffu, n > 0)) continue;
-                    uint32_t place = n;
-#pragma unroll
-                    for (int o = 1; o < 32; o *= 2) {
-                        const uint32_t y = __shfl_up_sync(0xffffffffu, place, o);
-                        if (lane >= o) place += y;
-                    }
-                    uint32_t base = 0;
-                    if (lane == 31) base = atomicAdd(&sh.listed, place);
-                    place += __shfl_sync(0xffffffffu, base, 31) - n;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (k + e >= lo && k + e < c1 && u[e] >> 21 == found >> 21) {
-                            if (place < kBins) sh.hist[1][place] = u[e];
-                            ++place;
-                        }
-                }
-                __syncthreads();
-                listed = sh.listed <= kBins;
-            } else {
-                __syncthreads();
-            }
+            __syncthreads();
         }
         threshold = found;
     }

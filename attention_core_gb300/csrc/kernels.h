@@ -309,6 +309,7 @@ struct PrefixGroups {
     int32_t n;
 };
 size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv);
+bool prefix_all_few(const PagedArgs& a);   // no kernel that reads by tensor maps is launched
 int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, const uint16_t* q,
                   const uint16_t* k_pages, const uint16_t* v_pages, cudaStream_t stream);
 

@@ -407,7 +407,10 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     }
 
     // the plan is another kernel's, this one's set-up so far runs beside it
-    if constexpr (PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (PREFIX) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // who may read the plan now, too
+    }
 
     // ---- this CTA's share of the line: every thread sums the units of its run of
     // sequences, the block sums those, and the warp whose runs hold the share's first
@@ -493,7 +496,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     const int group = a.group;
 
     // the join may take its place on the chip (it waits for this grid's end)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (!PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true;
     if (a.inject_timeout) alive = wait_warp(wc, bar(bars->never), 0, timeout_code(kSiteInject));

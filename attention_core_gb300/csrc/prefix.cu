@@ -672,7 +672,7 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     a.few_waits = 1;
     // batches whose new tokens all together are few rows have no others (the kernel for
     // those has no wait that the test hook could let run out)
-    if (!few_rows(t.n_tokens, a.group) || a.inject_timeout) {
+    if (!prefix_all_few(a)) {
         constexpr uint32_t smem = PagedCfg<D>::SMEM_PREFIX;
         // (of head groups that the other kernel does not take, single tokens are tiles of few rows)
         const bool fine = a.group > 16 && (int64_t)t.n_tokens * a.group <= (int64_t)kFineRows * t.n_seq;
@@ -710,6 +710,8 @@ size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q
 {
     return prefix_layout(d, n_seq, n_groups, n_tokens, h_q, h_kv).bytes;
 }
+
+bool prefix_all_few(const PagedArgs& a) { return few_rows(a.t.n_tokens, a.group) && !a.inject_timeout; }
 
 int launch_prefix(const PagedMaps& m, const PagedArgs& a, const PrefixGroups& g, const uint16_t* q,
                   const uint16_t* k_pages, const uint16_t* v_pages, cudaStream_t st)
