@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libattn_core.so")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "dropout_add_ln.cu", "gelu.cu", "rope.cu", "paged.cu", "prefix.cu", "weights.cu", "evict.cu",
            "pages.cu"]
-HEADERS = ["ptx.cuh", "philox.cuh", "tile.cuh", "sched.cuh", "paged_sched.cuh", "paged_attn.cuh", "weights_sched.cuh",
+HEADERS = ["ptx.cuh", "philox.cuh", "tile.cuh", "sched.cuh", "paged_sched.cuh", "paged_attn.cuh", "prefix_plan.cuh", "weights_sched.cuh",
            "kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

@@ -272,6 +272,13 @@ struct AppendArgs {
 };
 int launch_append(const RopeTable& t, AppendArgs& a, int sms, cudaStream_t stream);
 
+// Groups of sequences that share their first pages.
+struct PrefixGroups {
+    const int32_t* starts;      // device [n + 1]
+    const int32_t* pages;       // device [n]
+    int32_t n;
+};
+
 // Attention of new tokens over the pages (paged.cu).
 struct PagedArgs {
     PagedTables t;
@@ -286,7 +293,8 @@ struct PagedArgs {
     int32_t inject_timeout;
     int32_t num_sms;
     // batches whose sequences share their first pages (prefix.cu; set by its launcher)
-    const struct PrefixSeq* plan;
+    PrefixGroups groups;
+    const struct PrefixSeq* plan;   // null: the kernels make it themselves
     int32_t n_plan;
     uint64_t* records;          // where each row's parts lie
     size_t lse_offset;          // of the parts' LSEs in the workspace
@@ -303,11 +311,6 @@ struct PagedMaps {
 int launch_paged(const PagedMaps& maps, const PagedArgs& a, cudaStream_t stream);
 
 // The same where groups of sequences share their first pages (prefix.cu).
-struct PrefixGroups {
-    const int32_t* starts;      // device [n + 1]
-    const int32_t* pages;       // device [n]
-    int32_t n;
-};
 size_t prefix_ws_bytes(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv);
 bool prefix_all_few(const PagedArgs& a);   // no kernel that reads by tensor maps is launched
 int launch_prefix(const PagedMaps& maps, const PagedArgs& a, const PrefixGroups& g, const uint16_t* q,

@@ -50,6 +50,7 @@
 
 #include "kernels.h"
 #include "paged_sched.cuh"
+#include "prefix_plan.cuh"
 #include "ptx.cuh"
 #include "tile.cuh"
 
@@ -101,7 +102,7 @@ struct PagedGeom {
     }
 };
 
-template <int D>
+template <int D, bool PREFIX = false>
 struct PagedCfg {
     using G = TileGeom<D>;                                    // the O stage
     static constexpr uint32_t TILE = PagedGeom<D>::TILE;
@@ -111,23 +112,23 @@ struct PagedCfg {
     // tile's O leaves by TMA.
     static constexpr int NQ = (D <= 64) ? 2 : 1;
     static constexpr int SK = (D <= 64) ? 6 : (D <= 96 ? 4 : (D <= 128 ? 3 : 2));
-    static constexpr int SV = (D <= 64) ? 5 : (D <= 96 ? 3 : 2);
-    static constexpr bool STAGE_O = D <= 128;
+    static constexpr int SV = (D <= 64) ? (PREFIX ? 4 : 5) : (D <= 96 ? 3 : 2);
+    static constexpr bool STAGE_O = D <= 128 && !PREFIX;
     static constexpr bool SPLIT = (D <= 128);
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_K = NQ * TILE;
     static constexpr uint32_t OFF_V = OFF_K + SK * TILE;
     static constexpr uint32_t OFF_OST = OFF_V + SV * TILE;
-    static constexpr uint32_t OFF_BAR = OFF_OST + (STAGE_O ? TILE : 0);
+    // batches of shared pages: rows are turned over there on their way to the workspace (2 KB
+    // a warp), and the plan
+    static constexpr uint32_t OFF_TURN = OFF_OST, OFF_PLAN = OFF_TURN + 8 * 2048;
+    static constexpr uint32_t OFF_BAR =
+        PREFIX ? OFF_PLAN + ((uint32_t)sizeof(PlanNear) + 127) / 128 * 128 : OFF_OST + (STAGE_O ? TILE : 0);
     static constexpr uint32_t BAR_BYTES = 1024;
     static constexpr uint32_t OFF_XCH = OFF_BAR + BAR_BYTES;
     static constexpr uint32_t XCH_BYTES = SPLIT ? 128 * 8 : 0;
     static constexpr uint32_t SMEM = OFF_XCH + XCH_BYTES + 1024;
-    // batches of shared pages turn rows over in shared memory on their way to the workspace
-    // (2 KB a warp; the O stage is free there)
-    static constexpr uint32_t OFF_TURN = STAGE_O ? OFF_OST : OFF_XCH + XCH_BYTES;
-    static constexpr uint32_t SMEM_PREFIX = STAGE_O ? SMEM : SMEM + 8 * 2048;
-    static_assert(SMEM_PREFIX <= 227 * 1024, "shared memory budget");
+    static_assert(SMEM <= 227 * 1024, "shared memory budget");
     static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O = 256, T_O1 = 256 + D, T_X = 256 + D;
     static_assert(SPLIT ? (T_O1 + D <= 512) : (T_X + 6 <= 512), "TMEM budget");
 };
@@ -245,18 +246,18 @@ __host__ __device__ inline size_t ws_cut_offset(int d)
 
 // Batches of shared pages: behind the parts come whole tiles' rows that another tile's
 // are joined with (two sets of n_tokens x h_q, of the sequences' own keys and of the
-// groups'), and a record per (set, new token, KV head) says where its rows lie.
+// groups'), and a record per (set, new token, head) says where the row lies.
 __host__ __device__ inline size_t whole_row(const PagedTables& t, bool prefix, int tok, int head)
 {
     return (size_t)kPagedMaxCtas * 2 * 128 + ((size_t)(prefix ? t.n_tokens : 0) + tok) * t.h_q + head;
 }
-__host__ __device__ inline size_t record_at(const PagedTables& t, bool prefix, int tok, int kv_head)
+__host__ __device__ inline size_t record_at(const PagedTables& t, bool prefix, int tok, int head)
 {
-    return ((size_t)(prefix ? t.n_tokens : 0) + tok) * t.h_kv + kv_head;
+    return ((size_t)(prefix ? t.n_tokens : 0) + tok) * t.h_q + head;
 }
 constexpr uint64_t kRecordNone = 0, kRecordWhole = 1, kRecordCut = 2, kRecordState = 3, kRecordJoined = 4,
                    kRecordFew = 8;
-// `row`: the first of the token's rows in its tile; of a cut tile, who has its first and
+// `row`: its row in its tile; of a cut tile, who has its first and
 // its last part (CTAs here, warps of the kernel for few rows, kRecordFew)
 __device__ __forceinline__ uint64_t make_record(bool whole, bool joined, int first, int last, int row)
 {
@@ -362,18 +363,19 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 {
     using G = TileGeom<D>;
     using P = PagedGeom<D>;
-    using C = PagedCfg<D>;
+    using C = PagedCfg<D, PREFIX>;
     const PagedTables& t = a.t;
     using Tables = std::conditional_t<PREFIX, PrefixTables, PagedTables>;
-    Tables tab;
-    if constexpr (PREFIX)
-        tab = PrefixTables{a.plan, a.n_plan, t.h_kv};
-    else
-        tab = t;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    Tables tab;
+    if constexpr (PREFIX)
+        tab = PrefixTables{a.plan ? a.plan : reinterpret_cast<const PlanNear*>(smem_raw + pad + C::OFF_PLAN)->seq, a.n_plan,
+                           t.h_kv};
+    else
+        tab = t;
     const uint32_t sb = raw + pad;
     PagedBars* bars = reinterpret_cast<PagedBars*>(smem_raw + pad + C::OFF_BAR);
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
@@ -408,8 +410,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 
     // the plan is another kernel's, this one's set-up so far runs beside it
     if constexpr (PREFIX) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (a.plan) asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // who may read the plan now, too
+        if (!a.plan) plan_near(t, a.tpt, a.causal, a.groups, *reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN));
     }
 
     // ---- this CTA's share of the line: every thread sums the units of its run of
@@ -458,7 +461,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     // beside the kernel for few rows, as many CTAs as this one's share of the work (prefix.cu)
     int64_t ctas = gridDim.x;
     if constexpr (PREFIX) {
-        ctas = many_ctas(total, a.plan[a.n_plan - 1].few_units, gridDim.x);
+        ctas = many_ctas(total, tab.plan[a.n_plan - 1].few_units, gridDim.x);
     }
     int64_t per = quot(total + ctas - 1, ctas);
     per = per > kMinUnits ? per : kMinUnits;
@@ -570,7 +573,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if constexpr (PREFIX) {
                     // the readers know the sequence by its entries and its kind
                     if (more) {
-                        const PrefixSeq v = a.plan[g.seq];
+                        const PrefixSeq v = tab.plan[g.seq];
                         g.seq = v.row;
                         g.m = v.page0 << kKindBits | v.kind;
                     }
@@ -812,7 +815,10 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if (live) {
                     for (int c = h; c < D / 8; c += 2) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
                     if (h == 0) *lrow = -INFINITY;
-                }                                              // (its record stays at kRecordNone)
+                    if constexpr (PREFIX) {
+                        if (h == 0) a.records[record_at(t, false, tok, head)] = kRecordNone;
+                    }
+                }
                 continue;
             }
             // keys that this row sees
@@ -954,7 +960,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             // a row that saw a NaN score is NaN, and has to reach O and the LSE.)
             float a0 = 0.f, a1 = 0.f, lse2 = -INFINITY;
             // a full tile's O leaves through the stage: free once its last store has read it
-            const bool staged = C::STAGE_O && !PREFIX && g.whole && g.n_tok == a.tpt;
+            const bool staged = C::STAGE_O && g.whole && g.n_tok == a.tpt;
             if (staged && h == 0 && r == 0) bulk_wait_read0();
             if constexpr (C::SPLIT) {
                 if (h == 1) xch[r] = make_float2(m_run, l_run);
@@ -1008,9 +1014,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                     else
                         reinterpret_cast<float*>(a.ws + (PREFIX ? a.lse_offset : ws_lse_offset(D)))[prow] = lse2;
                     if constexpr (PREFIX) {
-                        if (!done && g.from_start && r_head == 0)
-                            a.records[record_at(t, g.m & kKindPrefix, tok, g.head)] =
-                                make_record(g.whole, joined, blockIdx.x, g.last_cta, r);
+                        if (g.from_start)
+                            a.records[record_at(t, g.m & kKindPrefix, tok, head)] =
+                                done ? kRecordNone : make_record(g.whole, joined, blockIdx.x, g.last_cta, r);
                     }
                 }
                 // batches of shared pages: the rows that this lane stores a piece of, 8 rows apart

@@ -8,9 +8,9 @@
 // and which hides no key from any of them: 128 rows of a tile visit a block of shared
 // keys together, where the plain batch visits it once for each sequence.
 //
-// Four kernels, launched programmatically one behind the other:
-//   plan   turns tables and groups into one list of sequences (PrefixSeq): the groups'
-//          shared parts, then each sequence's own part
+// Kernels, launched programmatically one behind the other:
+//   plan   turns tables and groups into one list of sequences (prefix_plan.cuh); in small
+//          batches the next two make it themselves
 //   attend the kernel of paged_attn.cuh over the list's sequences of many rows; rows that
 //          have a part of their softmax elsewhere leave as fp32 with their LSE
 //   few    the sequences of few rows (a sample's own keys, its single token)
@@ -27,129 +27,70 @@ __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~(size
 
 // Workspace: rows [parts of cut tiles | whole tiles' rows, twice | parts of cut tiles of
 // few rows] of d floats, their base-2 LSEs, the records, the plan.
-constexpr int kFewWarps = kPagedMaxCtas * 8;      // of the kernel for few rows, at most
+constexpr int kFewWarps = kPagedMaxCtas * 12;     // of the kernel for few rows, at most
 struct PrefixLayout {
     size_t lse, records, plan, many, bytes;
 };
 __host__ __device__ inline size_t few_row(const PagedTables& t, int warp, int slot)
 {
-    return (size_t)kPagedMaxCtas * 2 * 128 + 2 * (size_t)t.n_tokens * t.h_q + ((size_t)warp * 2 + slot) * 16;
+    return (size_t)kPagedMaxCtas * 2 * 128 + 2 * (size_t)t.n_tokens * t.h_q + ((size_t)warp * 2 + slot) * kFewTile;
 }
 inline PrefixLayout prefix_layout(int d, int n_seq, int n_groups, int64_t n_tokens, int h_q, int h_kv)
 {
-    const size_t rows = (size_t)kPagedMaxCtas * 2 * 128 + 2 * (size_t)n_tokens * h_q + (size_t)kFewWarps * 2 * 16;
+    const size_t rows = (size_t)kPagedMaxCtas * 2 * 128 + 2 * (size_t)n_tokens * h_q + (size_t)kFewWarps * 2 * kFewTile;
     PrefixLayout l;
     l.lse = align256(rows * d * sizeof(float));
     l.records = align256(l.lse + rows * sizeof(float));
-    l.plan = align256(l.records + 2 * (size_t)n_tokens * h_kv * sizeof(uint64_t));
+    l.plan = align256(l.records + 2 * (size_t)n_tokens * h_q * sizeof(uint64_t));
     l.many = align256(l.plan + ((size_t)n_seq + n_groups) * sizeof(PrefixSeq));
     l.bytes = l.many + 256;
     return l;
 }
 
-// Sequences of few rows: at most two tiles of 16 rows (16 / group tokens each).
-constexpr int kFewKeys = 64;
-__host__ __device__ inline bool few_rows(int nq, int group) { return nq > 0 && group <= 16 && nq <= 2 * (16 / group); }
-__host__ __device__ inline int few_tiles(int nq, int group) { return (nq + 16 / group - 1) / (16 / group); }
-__host__ __device__ inline int few_blocks(int kv) { return kv > 0 ? (int)(((uint32_t)kv + kFewKeys - 1) / kFewKeys) : 1; }
-
-// Block 0 plans; all blocks clear the records of the sequences' own rows (a token that
-// no tile covers must not find an earlier call's).  What a group shares in fact is what
-// all its sequences hold before their first new token, in whole pages, so that no row's
-// mask ends inside it; a group of one sequence shares nothing.  Groups out of order or
-// out of range are reported and share nothing either: the attention is right without.
-// The sequences' lengths are read once and kept in shared memory (the first kPlanNear of
-// them: all, in any usual batch), since this kernel's time is what the others wait for.
-constexpr int kPlanNear = 1024;
+// The plan of a batch of more sequences than a block keeps at hand: block 0 plans; all
+// blocks clear the records of the sequences' own rows (a token that no tile covers must
+// not find an earlier call's).
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PagedTables t, int tpt, int causal,
                                                                    const PrefixGroups gr, PrefixSeq* plan,
                                                                    uint64_t* records, int n_records,
                                                                    int64_t* many_units)
 {
-    __shared__ int4 near[kPlanNear];                 // first token, new tokens, keys, shared pages of a sequence
     __shared__ int64_t warp_units[kPlanThreads / 32];
     __shared__ unsigned long long many;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x == 0) {
-        bool bad = false;
-        for (int g = tid; g < gr.n; g += kPlanThreads) {
-            const int s0 = gr.starts[g], s1 = gr.starts[g + 1];
-            bad |= s0 < 0 || s1 < s0 || s1 > t.n_seq || gr.pages[g] < 0;
-        }
-        for (int s = tid; s < t.n_seq && s < kPlanNear; s += kPlanThreads) {
-            const SeqTable q = read_seq(t, s, tpt, causal);
-            if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
-            near[s] = make_int4(q.q0, q.s.nq, q.s.kv, 0);
-        }
         if (tid == 0) many = 0;
-        auto seq = [&](int s) -> int4 {
-            if (s < kPlanNear) return near[s];
-            const SeqTable q = read_seq(t, s, tpt, causal);
-            if (q.bad && t.status) atomicCAS(t.status, 0, kStatusTable);
-            return make_int4(q.q0, q.s.nq, q.s.kv, 0);
-        };
-        // (beyond kPlanNear the shared pages go by way of the plan itself)
-        for (int s = kPlanNear + tid; s < t.n_seq; s += kPlanThreads) plan[gr.n + s].page0 = 0;
+        bool bad = false;
+        for (int g = tid; g < gr.n; g += kPlanThreads) bad |= bad_group(gr, g, t.n_seq);
+        for (int s = tid; s < t.n_seq; s += kPlanThreads) plan[gr.n + s].page0 = 0;
         bad = __syncthreads_or(bad);
         if (bad && tid == 0 && t.status) atomicCAS(t.status, 0, kStatusTable);
         for (int g = warp; g < gr.n; g += kPlanThreads / 32) {
             PrefixSeq shared{};
             if (!bad) {
                 const int s0 = gr.starts[g], s1 = gr.starts[g + 1];
-                int pages = gr.pages[g] < t.max_pages ? gr.pages[g] : t.max_pages;
-                int members = 0, q0 = INT32_MAX, q1 = 0, row = INT32_MAX;
-                for (int s = s0 + lane; s < s1; s += 32) {
-                    const int4 q = seq(s);
-                    if (q.y <= 0) continue;
-                    const int old = q.z > q.y ? (q.z - q.y) >> t.page_shift : 0;
-                    pages = old < pages ? old : pages;
-                    ++members;
-                    q0 = q.x < q0 ? q.x : q0;
-                    q1 = q.x + q.y > q1 ? q.x + q.y : q1;
-                    row = s < row ? s : row;
-                }
-                members = __reduce_add_sync(0xffffffffu, members);
-                pages = __reduce_min_sync(0xffffffffu, pages);
-                q0 = __reduce_min_sync(0xffffffffu, q0);
-                q1 = __reduce_max_sync(0xffffffffu, q1);
-                row = __reduce_min_sync(0xffffffffu, row);
-                if (members > 1 && pages > 0) {
-                    shared = PrefixSeq{q0, q1 - q0, pages << t.page_shift, row, 0, kKindAll | kKindPrefix | kKindJoined, 0};
-                    for (int s = s0 + lane; s < s1; s += 32) {
-                        if (s < kPlanNear)
-                            near[s].w = pages;
-                        else
-                            plan[gr.n + s].page0 = pages;
-                    }
+                GroupShape shape;
+                shape.pages = gr.pages[g] < t.max_pages ? gr.pages[g] : t.max_pages;
+                for (int s = s0 + lane; s < s1; s += 32) shape.add(s, read_lengths(t, s, tpt, causal), t.page_shift);
+                if (shape.join()) {
+                    shared = shape.shared(t.page_shift);
+                    for (int s = s0 + lane; s < s1; s += 32) plan[gr.n + s].page0 = shape.pages;
                 }
             }
             if (lane == 0) plan[g] = shared;
         }
         __syncthreads();
-        // each sequence's own part, who has it, and the line of the kernel for few rows
-        const int group = t.h_q / t.h_kv, n = gr.n + t.n_seq;
+        const int n = gr.n + t.n_seq;
         int64_t base = 0;
         for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
             const int i = i0 + tid, s = i - gr.n;
             int64_t units = 0;
             PrefixSeq v{};
             if (i < n) {
-                if (s < 0) {
-                    v = plan[i];
-                } else {
-                    const int4 q = seq(s);
-                    const int pages = q.y <= 0 ? 0 : s < kPlanNear ? q.w : plan[i].page0;
-                    v = PrefixSeq{q.x, q.y, q.z - (pages << t.page_shift), s, pages,
-                                  (causal ? 0 : kKindAll) | (pages ? kKindJoined : 0), 0};
-                }
-                if (few_rows(v.nq, group)) {
-                    v.kind |= kKindFew;
-                    units = (int64_t)few_tiles(v.nq, group) * few_blocks(v.kv) * t.h_kv;
-                } else if (v.nq > 0) {
-                    const SeqShape q{v.nq, v.kv, tpt, !(v.kind & kKindAll)};
-                    atomicAdd(&many, (unsigned long long)q.units(q.tiles()) * t.h_kv);
-                }
+                v = plan[i];
+                if (s >= 0) v = own_part(s, read_lengths(t, s, tpt, causal), v.page0, t.page_shift, causal);
+                units = assign(v, t, tpt, &many);
             }
             int64_t upto = units;
 #pragma unroll
@@ -178,14 +119,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PagedTa
         records[i] = kRecordNone;
 }
 
-// Attention of sequences of few rows (at most two tiles of 16) over their keys.  A tile
-// of 128 rows takes several microseconds from its Q to its O however few of them are used,
-// one after another on a processor: 64 samples' own 250 keys took 60 us that way.  Here a
-// warp has a tile's piece by itself, eight on a processor, each with its own ring of
+// Attention of sequences of few rows (kMostFewRows) over their keys.  A tile of 128 rows
+// takes several microseconds from its Q to its O however few of them are used, one after
+// another on a processor: 64 samples' own 250 keys took 60 us that way.  Here a warp has a
+// piece of a tile of 8 rows by itself, a dozen on a processor, each with its own ring of
 // 16-key steps of K and V (cp.async; 8 KB a step, so that about 100 KB are on their way to
-// a processor) and its own softmax: S = Q K^T and O += P V by mma.m16n8k16, whose scores'
-// layout is the layout that P needs.  Bound by the keys' bytes.  P goes in as two bf16
-// terms, as in paged_attn.cuh's tiles of few rows.
+// a processor) and its own softmax.  The scores are formed with the keys as the 16 rows
+// and the tile's as the 8 columns of mma.m16n8k16, S^T = K Q^T and O^T += V^T P^T: as many
+// products as there are 16 x 16 pieces of K and V, where rows by keys would be twice as
+// many, half of them empty.  P goes in as two bf16 terms, as in paged_attn.cuh's tiles of
+// few rows.  A step takes a warp about XX cycles.
 // The units are blocks of 64 keys of (sequence, KV head, row tile), in equal shares for
 // all warps; pieces of a tile are joined.  The kernel runs beside the one for many rows:
 // that one keeps to as many processors as its part of the work is worth (many_ctas), and
@@ -195,30 +138,37 @@ struct FewCfg {
     static constexpr int UNITS = D / 8;                        // of 16 bytes a row
     static constexpr uint32_t PITCH = (UNITS + 1) * 16;        // odd in 16 bytes: ldmatrix meets no bank twice
     static constexpr uint32_t TILE = 16 * PITCH, STAGE = 2 * TILE;
-    static constexpr int STAGES = D <= 96 ? 4 : 3;
-    static constexpr int WARPS = D <= 128 ? 8 : 7;
-    static constexpr uint32_t SMEM = WARPS * STAGES * STAGE;
+    static constexpr int COPIES = 16 * UNITS / 32;             // of 16 bytes a lane, for a step's K
+    static constexpr int STAGES = D <= 64 ? 4 : D <= 96 ? 3 : 2;
+    static constexpr int WARPS = D <= 64 ? 12 : D <= 96 ? 11 : D <= 128 ? 12 : 10;
+    static constexpr uint32_t OFF_PLAN = WARPS * STAGES * STAGE, SMEM = OFF_PLAN + sizeof(PlanNear);
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
-// The plan was written before this kernel began, but it waits for no kernel before it
-// reads: past L1.
-__device__ __forceinline__ PrefixSeq load_plan(const PrefixSeq* p)
-{
-    static_assert(sizeof(PrefixSeq) == 32, "two loads");
-    union {
-        int4 x[2];
-        PrefixSeq v;
-    } u;
-    u.x[0] = __ldcg(reinterpret_cast<const int4*>(p));
-    u.x[1] = __ldcg(reinterpret_cast<const int4*>(p) + 1);
-    return u.v;
-}
+// The plan, in shared memory or written by its kernel, which ended before this one began;
+// but this one waits for no kernel before it reads, so it reads that past L1.
+struct PlanView {
+    const PrefixSeq* seq;
+    int n;
+    bool near;
+    __device__ __forceinline__ int64_t units(int i) const { return near ? seq[i].few_units : __ldcg(&seq[i].few_units); }
+    __device__ __forceinline__ PrefixSeq at(int i) const
+    {
+        static_assert(sizeof(PrefixSeq) == 32, "two loads");
+        if (near) return seq[i];
+        union {
+            int4 x[2];
+            PrefixSeq v;
+        } u;
+        u.x[0] = __ldcg(reinterpret_cast<const int4*>(seq + i));
+        u.x[1] = __ldcg(reinterpret_cast<const int4*>(seq + i) + 1);
+        return u.v;
+    }
+};
 
 struct FewSegment {
     PrefixSeq v;
-    int head, q_tok, n_tok;
-    int first_pos;          // position of the tile's first token among the sequence's keys
+    int head, row0, n_rows; // rows of the sequence: new tokens times the head group
     int k0, k1;             // keys [k0, k1)
     bool whole, from_start;
     int last;               // of a cut tile's first piece: the warp of its last one
@@ -230,7 +180,7 @@ struct FewWalk {
     PrefixSeq v;
 
     // Unit u0 is in the first of the sequences lo .. hi - 1 whose units reach beyond it.
-    __device__ __forceinline__ void start(const PrefixSeq* plan, int lo, int hi, int h_kv, int group, int64_t u0, int64_t u1)
+    __device__ __forceinline__ void start(const PlanView& plan, int lo, int hi, int h_kv, int group, int64_t u0, int64_t u1)
     {
         at = u0;
         end = u1;
@@ -238,11 +188,11 @@ struct FewWalk {
         while (hi - lo > 32) {                             // 32 candidates a round
             const int step = (hi - lo + 31) / 32;
             const int last = lo + (lane + 1) * step - 1 < hi ? lo + (lane + 1) * step - 1 : hi - 1;
-            const uint32_t beyond = __ballot_sync(0xffffffffu, __ldcg(&plan[last].few_units) > u0);
+            const uint32_t beyond = __ballot_sync(0xffffffffu, plan.units(last) > u0);
             lo += (__ffs(beyond) - 1) * step;
             hi = lo + step < hi ? lo + step : hi;
         }
-        const PrefixSeq c = load_plan(plan + (lo + lane < hi ? lo + lane : hi - 1));
+        const PrefixSeq c = plan.at(lo + lane < hi ? lo + lane : hi - 1);
         const int src = __ffs(__ballot_sync(0xffffffffu, c.few_units > u0)) - 1;
         s = lo + src;
         v.q0 = __shfl_sync(0xffffffffu, c.q0, src);
@@ -252,7 +202,7 @@ struct FewWalk {
         v.page0 = __shfl_sync(0xffffffffu, c.page0, src);
         v.kind = __shfl_sync(0xffffffffu, c.kind, src);
         v.few_units = __shfl_sync(0xffffffffu, c.few_units, src);
-        const int blocks = few_blocks(v.kv), per_head = few_tiles(v.nq, group) * blocks;
+        const int blocks = few_blocks(v.kv), per_head = few_tiles(v.nq * group) * blocks;
         const int64_t rel = u0 - (v.few_units - (int64_t)per_head * h_kv);
         head = (int)quot(rel, per_head);
         const int in_head = (int)(rel - (int64_t)head * per_head);
@@ -260,34 +210,32 @@ struct FewWalk {
         b = in_head - m * blocks;
     }
 
-    __device__ __forceinline__ bool next(const PrefixSeq* plan, int n_plan, int h_kv, int group, FewSegment& g)
+    __device__ __forceinline__ bool next(const PlanView& plan, int h_kv, int group, FewSegment& g)
     {
         if (at >= end) return false;
         int blocks = few_blocks(v.kv);
         if (b >= blocks) {
             b = 0;
-            if (++m >= few_tiles(v.nq, group)) {
+            if (++m >= few_tiles(v.nq * group)) {
                 m = 0;
                 if (++head >= h_kv) {
                     head = 0;
                     do {
-                        if (++s >= n_plan) {               // only past the line's end
+                        if (++s >= plan.n) {               // only past the line's end
                             at = end;
                             return false;
                         }
-                        v = load_plan(plan + s);
+                        v = plan.at(s);
                     } while (!(v.kind & kKindFew));
                     blocks = few_blocks(v.kv);
                 }
             }
         }
         const int take = end - at < blocks - b ? (int)(end - at) : blocks - b;
-        const int tpt = 16 / group;
         g.v = v;
         g.head = head;
-        g.q_tok = v.q0 + m * tpt;
-        g.n_tok = v.nq - m * tpt < tpt ? v.nq - m * tpt : tpt;
-        g.first_pos = v.kv - v.nq + m * tpt;
+        g.row0 = m * kFewTile;
+        g.n_rows = v.nq * group - g.row0 < kFewTile ? v.nq * group - g.row0 : kFewTile;
         g.k0 = b * kFewKeys;
         g.k1 = (b + take) * kFewKeys < v.kv ? (b + take) * kFewKeys : v.kv;
         g.whole = take == blocks;
@@ -302,6 +250,10 @@ struct FewWalk {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -318,6 +270,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// The 8 x 8 matrix whose rows the lines of lanes hold, transposed.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 // D [16 x 8] += A [16 x 16] B [16 x 8], bf16 in, fp32 sums
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -339,13 +298,18 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.group;
     const uint32_t ring = smem_u32(smem_raw) + warp * C::STAGES * C::STAGE;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (a.few_waits) asm volatile("griddepcontrol.wait;" ::: "memory");
+    PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + C::OFF_PLAN);
+    if (!a.plan)
+        plan_near(t, a.tpt, a.causal, a.groups, *near);
+    else if (a.few_waits)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PlanView plan{a.plan ? a.plan : near->seq, a.n_plan, !a.plan};
 
     // The line's length, and 32 places of it in the same look: this warp's share starts
     // between two of them.
     const int step = (a.n_plan + 31) / 32;
     const int last = (lane + 1) * step < a.n_plan ? (lane + 1) * step - 1 : a.n_plan - 1;
-    const int64_t upto = __ldcg(&a.plan[last].few_units), many = __ldcg(a.many_units);
+    const int64_t upto = plan.units(last), many = a.plan ? __ldcg(a.many_units) : (int64_t)near->many;
     const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
     const int blocks = (int)gridDim.x - (many > 0 ? (int)many_ctas(many, total, gridDim.x) : 0);
     const int n_blocks = blocks > 0 ? blocks : 1;
@@ -360,13 +324,13 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
     const int lo = (__ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1) * step;
     FewWalk load_walk;
     load_walk.per = per;
-    load_walk.start(a.plan, lo, lo + step < a.n_plan ? lo + step : a.n_plan, t.h_kv, group, u0, u1);
+    load_walk.start(plan, lo, lo + step < a.n_plan ? lo + step : a.n_plan, t.h_kv, group, u0, u1);
     FewWalk walk = load_walk;
 
     // ---- loads: 16 keys a step, the entries of the page table 32 at a time
     FewSegment lg;
     int lk = 0, window = 0, entry = -1;
-    bool loading = load_walk.next(a.plan, a.n_plan, t.h_kv, group, lg);
+    bool loading = load_walk.next(plan, t.h_kv, group, lg);
     auto fetch_entries = [&](int first) {
         window = first;
         const int i = first + lane, n = (lg.v.kv + t.page_size - 1) >> t.page_shift;
@@ -376,10 +340,14 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
         lk = lg.k0;
         fetch_entries(lk >> t.page_shift);
     }
+    uint32_t copy_to[C::COPIES];                           // where this lane's 16 bytes go in a tile
+#pragma unroll
+    for (int i = 0; i < C::COPIES; ++i)
+        copy_to[i] = (uint32_t)((lane + 32 * i) / C::UNITS) * C::PITCH + (uint32_t)((lane + 32 * i) % C::UNITS) * 16;
     int load_slot = 0;
     auto issue = [&]() {
         while (loading && lk >= lg.k1) {
-            loading = load_walk.next(a.plan, a.n_plan, t.h_kv, group, lg);
+            loading = load_walk.next(plan, t.h_kv, group, lg);
             if (loading) {
                 lk = lg.k0;
                 fetch_entries(lk >> t.page_shift);
@@ -393,13 +361,22 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
             const size_t row0 = there ? ((size_t)page * t.h_kv + lg.head) * t.page_size + (lk & (t.page_size - 1)) : 0;
             const int rows = there ? lg.k1 - lk : 0;           // what lies behind is zeros
             const uint32_t dst = ring + load_slot * C::STAGE;
+            // (a page's rows of one head are contiguous)
+            const uint16_t* kp = k_pages + row0 * D + lane * 8;
+            const uint16_t* vp = v_pages + row0 * D + lane * 8;
+            if (rows >= 16) {
 #pragma unroll
-            for (int i = 0; i < 16 * C::UNITS / 32; ++i) {
-                const int x = lane + 32 * i, r = x / C::UNITS, u = x % C::UNITS;
-                const size_t from = (row0 + (r < rows ? r : 0)) * D + u * 8;
-                const uint32_t to = dst + r * C::PITCH + u * 16, bytes = r < rows ? 16 : 0;
-                cp_async16(to, k_pages + from, bytes);
-                cp_async16(to + C::TILE, v_pages + from, bytes);
+                for (int i = 0; i < C::COPIES; ++i) {
+                    cp_async16(dst + copy_to[i], kp + i * 256);
+                    cp_async16(dst + copy_to[i] + C::TILE, vp + i * 256);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::COPIES; ++i) {
+                    const bool in = (lane + 32 * i) / C::UNITS < rows;
+                    cp_async16(dst + copy_to[i], in ? kp + i * 256 : k_pages, in ? 16 : 0);
+                    cp_async16(dst + copy_to[i] + C::TILE, in ? vp + i * 256 : v_pages, in ? 16 : 0);
+                }
             }
             lk += 16;
         }
@@ -409,142 +386,162 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) issue();
 
-    const int r0 = lane >> 2, c0 = (lane & 3) * 2;         // this thread's rows r0, r0 + 8; columns c0, c0 + 1 of 8
-    const uint32_t k_lane = ((lane & 7) + (lane >> 4 & 1) * 8) * C::PITCH + (lane >> 3 & 1) * 16;
-    const uint32_t v_lane = (lane & 15) * C::PITCH + (lane >> 4) * 16;
+    // a product's fragments: this thread's line of 8, and its first of two columns of 8
+    const int line = lane >> 2, c0 = (lane & 3) * 2;
+    const uint32_t k_lane = ((lane & 7) + (lane >> 3 & 1) * 8) * C::PITCH + (lane >> 4) * 16;
+    const uint32_t v_lane = ((lane & 7) + (lane >> 4) * 8) * C::PITCH + (lane >> 3 & 1) * 16;
     float* rows_ws = reinterpret_cast<float*>(a.ws);
     float* lse_ws = reinterpret_cast<float*>(a.ws + a.lse_offset);
     int slot = 0;
     FewSegment g;
-    while (walk.next(a.plan, a.n_plan, t.h_kv, group, g)) {
-        // Q as A operands, and the keys that each row sees
-        uint32_t qa[D / 16][4];
-        bool live[2];
-        int lim[2], tok[2], head[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = r0 + 8 * h, rt = r / group;
-            live[h] = rt < g.n_tok;
-            tok[h] = g.q_tok + (live[h] ? rt : 0);
-            head[h] = g.head * group + (live[h] ? r - rt * group : 0);
-            lim[h] = g.v.kv;
-            if (!(g.v.kind & kKindAll)) {
-                const int seen = g.first_pos + rt + 1;
-                lim[h] = seen < g.v.kv ? (seen > 0 ? seen : 0) : g.v.kv;
-            }
-            const uint16_t* from = q + ((size_t)tok[h] * t.h_q + head[h]) * D + c0;
+    while (walk.next(plan, t.h_kv, group, g)) {
+        // Q as a B operand
+        uint32_t qb[D / 16][2];
+        {
+            const int r = g.row0 + line, rt = r / group;
+            const bool live = line < g.n_rows;
+            const uint16_t* from =
+                q + ((size_t)(g.v.q0 + (live ? rt : 0)) * t.h_q + g.head * group + (live ? r - rt * group : 0)) * D + c0;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                qa[kk][h] = live[h] ? *reinterpret_cast<const uint32_t*>(from + kk * 16) : 0u;
-                qa[kk][2 + h] = live[h] ? *reinterpret_cast<const uint32_t*>(from + kk * 16 + 8) : 0u;
+                qb[kk][0] = live ? *reinterpret_cast<const uint32_t*>(from + kk * 16) : 0u;
+                qb[kk][1] = live ? *reinterpret_cast<const uint32_t*>(from + kk * 16 + 8) : 0u;
             }
         }
-        const int plain = g.v.kind & kKindAll ? g.v.kv : g.first_pos + 1;       // keys that all rows see
-        float o[D / 8][4];
+        // the two rows whose columns of the scores this thread has, and the keys that they see
+        int lim[2];
+        bool live[2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+            live[e] = c0 + e < g.n_rows;
+            lim[e] = g.v.kv;
+            if (!(g.v.kind & kKindAll)) {
+                const int seen = g.v.kv - g.v.nq + (g.row0 + c0 + e) / group + 1;
+                lim[e] = seen < g.v.kv ? (seen > 0 ? seen : 0) : g.v.kv;
+            }
+        }
+        // keys that all rows see
+        const int plain = g.v.kind & kKindAll ? g.v.kv : g.v.kv - g.v.nq + g.row0 / group + 1;
+        float o[D / 16][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         for (int k = g.k0; k < g.k1; k += 16) {
             cp_async_wait<C::STAGES - 2>();
             __syncwarp();
             const uint32_t ks = ring + slot * C::STAGE + k_lane, vs = ring + slot * C::STAGE + C::TILE + v_lane;
-            float x[2][4] = {};
+            // (several chains of products: one that waits for the one before takes 56 cycles)
+            constexpr int CHAINS = 3;
+            float x[CHAINS][4] = {};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t b[4];
-                ldmatrix4(ks + kk * 32, b);
-                mma_16x8x16(x[0], qa[kk], b[0], b[1]);
-                mma_16x8x16(x[1], qa[kk], b[2], b[3]);
+                uint32_t ka[4];
+                ldmatrix4(ks + kk * 32, ka);
+                mma_16x8x16(x[kk % CHAINS], ka, qb[kk][0], qb[kk][1]);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[0][e] = x[0][e] + x[1][e] + x[2][e];
             const int last = k + 16 < g.k1 ? k + 16 : g.k1;
-            if (k + 16 > plain || last < k + 16) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int left = (lim[h] < last ? lim[h] : last) - k;
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (8 * n + c0 + e >= left) x[n][2 * h + e] = -INFINITY;
-                }
-            }
+            const bool masked = k + 16 > plain || last < k + 16;
+            uint32_t hi[2], lo[2];
             float m_new[2];
             bool moves = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float mx = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                m_new[h] = fmaxf(m_run[h], mx * a.scale_log2);
-                moves |= live[h] && m_new[h] > m_run[h] + 8.0f;
+            for (int e = 0; e < 2; ++e) {
+                if (masked) {
+                    const int left = (lim[e] < last ? lim[e] : last) - k;
+                    if (line >= left) x[0][e] = -INFINITY;
+                    if (line + 8 >= left) x[0][2 + e] = -INFINITY;
+                }
+                float mx = fmaxf(x[0][e], x[0][2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                m_new[e] = fmaxf(m_run[e], mx * a.scale_log2);
+                moves |= live[e] && m_new[e] > m_run[e] + 8.0f;
             }
             if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float f = m_run[h] == -INFINITY ? 0.f : ex2_approx(m_run[h] - m_new[h]);
-                    l_run[h] *= f;
+                for (int e = 0; e < 2; ++e) {
+                    const float f = m_run[e] == -INFINITY ? 0.f : ex2_approx(m_run[e] - m_new[e]);
+                    l_run[e] *= f;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[i][2 * h] *= f;
-                        o[i][2 * h + 1] *= f;
+                    for (int i = 0; i < D / 16; ++i) {
+                        o[i][e] *= f;
+                        o[i][2 + e] *= f;
                     }
-                    m_run[h] = m_new[h];
+                    m_run[e] = m_new[e];
                 }
             }
-            uint32_t hi[4], lo[4];
+            float p[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float m_ref = m_run[h] == -INFINITY ? 0.f : m_run[h];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = ex2_approx(fmaf(x[n][2 * h], a.scale_log2, -m_ref));
-                    const float p1 = ex2_approx(fmaf(x[n][2 * h + 1], a.scale_log2, -m_ref));
-                    l_run[h] += p0 + p1;
-                    const uint32_t w = pack_bf16x2(p0, p1);
-                    hi[2 * n + h] = w;
-                    lo[2 * n + h] = pack_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
-                }
+            for (int e = 0; e < 2; ++e) {
+                const float m_ref = m_run[e] == -INFINITY ? 0.f : m_run[e];
+                p[e] = ex2_approx(fmaf(x[0][e], a.scale_log2, -m_ref));
+                p[2 + e] = ex2_approx(fmaf(x[0][2 + e], a.scale_log2, -m_ref));
+                l_run[e] += p[e] + p[2 + e];
             }
+            // [8 keys x 8 rows] pieces, turned into the B operand of P V's products
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t b[4];
-                ldmatrix4_trans(vs + i * 32, b);
-                mma_16x8x16(o[2 * i], hi, b[0], b[1]);
-                mma_16x8x16(o[2 * i + 1], hi, b[2], b[3]);
-                mma_16x8x16(o[2 * i], lo, b[0], b[1]);
-                mma_16x8x16(o[2 * i + 1], lo, b[2], b[3]);
+            for (int n = 0; n < 2; ++n) {
+                const uint32_t w = pack_bf16x2(p[2 * n], p[2 * n + 1]);
+                hi[n] = movmatrix(w);
+                lo[n] = movmatrix(pack_bf16x2(p[2 * n] - __uint_as_float(w << 16),
+                                              p[2 * n + 1] - __uint_as_float(w & 0xffff0000u)));
+            }
+            constexpr int GROUP = D == 64 ? 4 : D / 32;
+#pragma unroll
+            for (int i0 = 0; i0 < D / 16; i0 += GROUP) {
+                uint32_t va[GROUP][4];
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) {
+                    ldmatrix4_trans(vs + (i0 + i) * 32, va[i]);
+                    mma_16x8x16(o[i0 + i], va[i], hi[0], hi[1]);
+                }
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i) mma_16x8x16(o[i0 + i], va[i], lo[0], lo[1]);
             }
             __syncwarp();
             issue();
             if (++slot == C::STAGES) slot = 0;
         }
+        const bool joined = g.v.kind & kKindJoined, prefix = g.v.kind & kKindPrefix, done = g.whole && !joined;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float l = l_run[h];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
+        for (int e = 0; e < 2; ++e) {
+            float l = l_run[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
             const float inv = l == 0.f ? 0.f : 1.0f / l;       // NaN stays
-            const float lse2 = l == 0.f ? -INFINITY : m_run[h] + log2f(l);
-            if (!live[h]) continue;
-            const bool joined = g.v.kind & kKindJoined, prefix = g.v.kind & kKindPrefix;
-            if (g.whole && !joined) {
-                uint32_t* to = reinterpret_cast<uint32_t*>(a.o + ((size_t)tok[h] * t.h_q + head[h]) * D + c0);
+            const float lse2 = l == 0.f ? -INFINITY : m_run[e] + log2f(l);
+            if (!live[e]) continue;
+            const int r = g.row0 + c0 + e, rt = r / group;
+            const int tok = g.v.q0 + rt, head = g.head * group + r - rt * group;
+            uint64_t* record = a.records + record_at(t, prefix, tok, head);
+            if (done) {
+                uint16_t* to = a.o + ((size_t)tok * t.h_q + head) * D + line;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) to[i * 4] = pack_bf16x2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
-                if (c0 == 0) a.lse[(size_t)head[h] * t.n_tokens + tok[h]] = lse2 * 0.693147180559945309f;
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t w = pack_bf16x2(o[i][e] * inv, o[i][2 + e] * inv);
+                    to[i * 16] = (uint16_t)(w & 0xffffu);
+                    to[i * 16 + 8] = (uint16_t)(w >> 16);
+                }
+                if (line == 0) {
+                    a.lse[(size_t)head * t.n_tokens + tok] = lse2 * 0.693147180559945309f;
+                    *record = kRecordNone;
+                }
                 continue;
             }
-            const int r = r0 + 8 * h;
-            const size_t row = g.whole ? whole_row(t, prefix, tok[h], head[h]) : few_row(t, me, g.from_start ? 1 : 0) + r;
-            float* to = rows_ws + row * D + c0;
+            const size_t row = g.whole ? whole_row(t, prefix, tok, head) : few_row(t, me, g.from_start ? 1 : 0) + c0 + e;
+            float* to = rows_ws + row * D + line;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
-            if (c0 == 0) {
+            for (int i = 0; i < D / 16; ++i) {
+                to[i * 16] = o[i][e] * inv;
+                to[i * 16 + 8] = o[i][2 + e] * inv;
+            }
+            if (line == 0) {
                 lse_ws[row] = lse2;
-                if (g.from_start && r % group == 0)
-                    a.records[record_at(t, prefix, tok[h], g.head)] =
-                        make_record(g.whole, joined, me, g.last, r) | kRecordFew;
+                if (g.from_start) *record = make_record(g.whole, joined, me, g.last, c0 + e) | kRecordFew;
             }
         }
     }
@@ -564,11 +561,27 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     if (row >= (int64_t)t.n_tokens * t.h_q) return;
     const int lane = threadIdx.x & 31;
     const int tok = (int)(row / t.h_q), head = (int)(row % t.h_q);
-    const int kv_head = head / a.group, r_head = head % a.group;
-    const uint64_t own = a.records[record_at(t, false, tok, kv_head)];
-    uint64_t shared = a.records[record_at(t, true, tok, kv_head)];       // meaningless where nothing is shared
+    const uint64_t own = a.records[record_at(t, false, tok, head)];
+    uint64_t shared = a.records[record_at(t, true, tok, head)];       // meaningless where nothing is shared
+    if (!a.plan) {
+        // no plan's kernel has cleared the records: a token of no sequence finds anything
+        bool mine = false;
+        for (int s = lane; s < t.n_seq; s += 32) {
+            const SeqTable q = read_seq(t, s, a.tpt, a.causal);
+            mine |= tok >= q.q0 && tok - q.q0 < q.s.nq;
+        }
+        if (!__any_sync(0xffffffffu, mine)) return;
+    }
     if ((own & kRecordState) == kRecordNone) return;
     if (!(own & kRecordJoined)) shared = kRecordNone;
+    // (after a wait that ran out a record may be anything)
+    auto sound = [&](uint64_t r) -> bool {
+        const uint64_t state = r & kRecordState, who = r >> 12 & 0xfffff, last = r >> 32;
+        return state == kRecordNone || state == kRecordWhole ||
+               (state == kRecordCut && who <= last && last < (r & kRecordFew ? kFewWarps : kPagedMaxCtas) &&
+                (int)(r >> 4 & 255) < (r & kRecordFew ? kFewTile : 128));
+    };
+    if (!sound(own) || !sound(shared)) return;
     auto first = [](uint64_t r) -> int { return (int)(r >> 12 & 0xfffff); };
     auto count = [&](uint64_t r) -> int {
         const uint64_t state = r & kRecordState;
@@ -581,7 +594,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
         const int i = prefix ? p - n_own : p;
         if ((r & kRecordState) == kRecordWhole) return whole_row(t, prefix, tok, head);
         const int who = first(r) + i, piece = i == 0 ? 1 : 0;
-        return (r & kRecordFew ? few_row(t, who, piece) : part_row(who, piece)) + (int)(r >> 4 & 255) + r_head;
+        return (r & kRecordFew ? few_row(t, who, piece) : part_row(who, piece)) + (int)(r >> 4 & 255);
     };
     const float* lse = reinterpret_cast<const float*>(a.ws + a.lse_offset);
     const float* rows = reinterpret_cast<const float*>(a.ws) + lane;
@@ -635,18 +648,18 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
 }
 
 template <typename... Args>
-cudaError_t launch_behind(void (*kern)(Args...), dim3 grid, int threads, uint32_t smem, cudaStream_t st, Args... args)
+cudaError_t launch_behind(bool early, void (*kern)(Args...), dim3 grid, int threads, uint32_t smem, cudaStream_t st, Args... args)
 {
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -656,27 +669,29 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
 {
     const PagedTables& t = a.t;
     const PrefixLayout l = prefix_layout(D, t.n_seq, g.n, t.n_tokens, t.h_q, t.h_kv);
-    PrefixSeq* plan = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
-    a.plan = plan;
     a.n_plan = g.n + t.n_seq;
+    a.groups = g;
     a.records = reinterpret_cast<uint64_t*>(a.ws + l.records);
     a.lse_offset = l.lse;
     a.many_units = reinterpret_cast<const int64_t*>(a.ws + l.many);
-    const int n_records = t.n_tokens * t.h_kv;
-    const int clearing = n_records / (kPlanThreads * 8);
-    prefix_plan_kernel<<<(unsigned)(clearing < 1 ? 1 : clearing < 64 ? clearing : 64), kPlanThreads, 0, st>>>(
-        t, a.tpt, a.causal, g, plan, a.records, n_records, reinterpret_cast<int64_t*>(a.ws + l.many));
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return (int)e;
-
+    a.plan = nullptr;
+    cudaError_t e;
+    if (a.n_plan > kPlanNear) {
+        PrefixSeq* plan = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
+        a.plan = plan;
+        const int n_records = t.n_tokens * t.h_q;
+        const int clearing = n_records / (kPlanThreads * 8);
+        prefix_plan_kernel<<<(unsigned)(clearing < 1 ? 1 : clearing < 64 ? clearing : 64), kPlanThreads, 0, st>>>(
+            t, a.tpt, a.causal, g, plan, a.records, n_records, reinterpret_cast<int64_t*>(a.ws + l.many));
+        if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
+    }
+    bool first = !a.plan;            // the first kernel waits for all that came before
     a.few_waits = 1;
     // batches whose new tokens all together are few rows have no others (the kernel for
     // those has no wait that the test hook could let run out)
     if (!prefix_all_few(a)) {
-        constexpr uint32_t smem = PagedCfg<D>::SMEM_PREFIX;
-        // (of head groups that the other kernel does not take, single tokens are tiles of few rows)
-        const bool fine = a.group > 16 && (int64_t)t.n_tokens * a.group <= (int64_t)kFineRows * t.n_seq;
-        auto kern = fine ? paged_attn_kernel<D, true, true> : paged_attn_kernel<D, false, true>;
+        constexpr uint32_t smem = PagedCfg<D, true>::SMEM;
+        auto kern = paged_attn_kernel<D, false, true>;     // (the tiles that are fine, kFineRows, are not its)
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
             return (int)e;
         const int64_t blocks = ((int64_t)t.max_pages * t.page_size + 127) / 128;
@@ -684,24 +699,26 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
         const int64_t want = ((2 * row_tiles + a.n_plan) * t.h_kv * blocks + kMinUnits - 1) / kMinUnits;
         int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
         if (want < grid) grid = want;
-        if ((e = launch_behind(kern, dim3((unsigned)grid), kThreads, smem, st, m, a)) != cudaSuccess) return (int)e;
+        if ((e = launch_behind(!first, kern, dim3((unsigned)grid), kThreads, smem, st, m, a)) != cudaSuccess)
+            return (int)e;
+        first = false;
         a.few_waits = 0;
     }
-    if (a.group <= 16) {
+    {
         using C = FewCfg<D>;
         auto kern = prefix_few_kernel<D>;
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM)) != cudaSuccess)
             return (int)e;
         const int64_t blocks = ((int64_t)t.max_pages * t.page_size + kFewKeys - 1) / kFewKeys;
-        const int64_t want = 2 * (int64_t)a.n_plan * t.h_kv * blocks;              // units, at most
+        const int64_t want = (kMostFewRows / kFewTile) * (int64_t)a.n_plan * t.h_kv * blocks;      // units, at most
         int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
         if (want < grid) grid = want;
-        if ((e = launch_behind(kern, dim3((unsigned)grid), C::WARPS * 32, C::SMEM, st, a, q, k_pages, v_pages)) !=
+        if ((e = launch_behind(!first, kern, dim3((unsigned)grid), C::WARPS * 32, C::SMEM, st, a, q, k_pages, v_pages)) !=
             cudaSuccess)
             return (int)e;
     }
     const int64_t rows = (int64_t)t.n_tokens * t.h_q;
-    return (int)launch_behind(prefix_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, st, a);
+    return (int)launch_behind(true, prefix_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, st, a);
 }
 
 }  // namespace

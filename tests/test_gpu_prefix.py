@@ -118,6 +118,25 @@ def test_cut_tiles(hq, hkv, d, ps, n, pages, own):
     assert int(p.status.item()) == 0
 
 
+@pytest.mark.parametrize("n", [62, 63, 64, 150, 1100])
+def test_many_sequences(n):
+    """On both sides of what a block plans for itself (128 sequences and groups)."""
+    gen = torch.Generator().manual_seed(n)
+    groups = [(2, 1 + i % 5) for i in range(n // 2)] + [(n % 2, 3)]
+    own = [int(x) for x in torch.randint(1, 60, (n,), generator=gen)]
+    nq = [1 + (i % 7 == 3) * 2 for i in range(n)]
+    own = [max(a, b) for a, b in zip(own, nq)]
+    p = shared(groups, nq, own, 4, 2, 64, 16, outside=[(1, 30), (40, 50)])
+    o, lse = run(p)
+    check_attention(o, lse, attend(p), p)
+    assert int(p.status.item()) == 0
+    # one group of all: more rows than a tile
+    p = shared([(n, 9)], nq, own, 4, 2, 64, 16, seed=1)
+    o, lse = run(p)
+    check_attention(o, lse, attend(p), p)
+    assert int(p.status.item()) == 0
+
+
 def test_empty_groups_and_sequences():
     p = shared([(2, 3), (0, 5), (3, 2)], [1, 0, 0, 2, 0], [4, 6, 1, 9, 0], 8, 2, 128, 16, n_tokens=5)
     o, lse = run(p)
