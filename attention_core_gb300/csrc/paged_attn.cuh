@@ -412,7 +412,19 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     if constexpr (PREFIX) {
         if (a.plan) asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // who may read the plan now, too
-        if (!a.plan) plan_near(t, a.tpt, a.causal, a.groups, *reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN));
+        PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN);
+        if (!a.plan)
+            plan_near(t, a.tpt, a.causal, a.groups, *near);
+        else
+            __syncthreads();
+        // CTAs without a share make room at once for the kernel for few rows
+        const int64_t many = a.plan ? *a.many_units : (int64_t)near->many;
+        if ((many == 0 || (int64_t)blockIdx.x >= many_ctas(many, tab.plan[a.n_plan - 1].few_units, gridDim.x)) &&
+            !a.inject_timeout) {
+            tc_fence_after();
+            if (warp == 1) tmem_dealloc(bars->tmem_base, 512);
+            return;
+        }
     }
 
     // ---- this CTA's share of the line: every thread sums the units of its run of

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     };
     const float* lse = reinterpret_cast<const float*>(a.ws + a.lse_offset);
     const float* rows = reinterpret_cast<const float*>(a.ws) + lane;
-    constexpr int E = D / 32, AHEAD = 8;
+    constexpr int E = D / 32, AHEAD = E <= 4 ? 16 : 8;      // divides 32
     float x[AHEAD][E];
     auto load = [&](int p0) {
 #pragma unroll
