@@ -122,13 +122,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PagedTa
 // Attention of sequences of few rows (kMostFewRows) over their keys.  A tile of 128 rows
 // takes several microseconds from its Q to its O however few of them are used, one after
 // another on a processor: 64 samples' own 250 keys took 60 us that way.  Here a warp has a
-// piece of a tile of 8 rows by itself, a dozen on a processor, each with its own ring of
+// piece of a tile of 8 rows by itself, eight on a processor, each with its own ring of
 // 16-key steps of K and V (cp.async; 8 KB a step, so that about 100 KB are on their way to
 // a processor) and its own softmax.  The scores are formed with the keys as the 16 rows
 // and the tile's as the 8 columns of mma.m16n8k16, S^T = K Q^T and O^T += V^T P^T: as many
 // products as there are 16 x 16 pieces of K and V, where rows by keys would be twice as
 // many, half of them empty.  P goes in as two bf16 terms, as in paged_attn.cuh's tiles of
-// few rows.  A step takes a warp about XX cycles.
+// few rows.  A step takes a warp about 1400 cycles at d = 96 (the copies' issue 430, scores
+// 380, softmax 380, P V 160), so that 152 processors ask for more than HBM gives.
 // The units are blocks of 64 keys of (sequence, KV head, row tile), in equal shares for
 // all warps; pieces of a tile are joined.  The kernel runs beside the one for many rows:
 // that one keeps to as many processors as its part of the work is worth (many_ctas), and
@@ -139,8 +140,8 @@ struct FewCfg {
     static constexpr uint32_t PITCH = (UNITS + 1) * 16;        // odd in 16 bytes: ldmatrix meets no bank twice
     static constexpr uint32_t TILE = 16 * PITCH, STAGE = 2 * TILE;
     static constexpr int COPIES = 16 * UNITS / 32;             // of 16 bytes a lane, for a step's K
-    static constexpr int STAGES = D <= 64 ? 4 : D <= 96 ? 3 : 2;
-    static constexpr int WARPS = D <= 64 ? 12 : D <= 96 ? 11 : D <= 128 ? 12 : 10;
+    static constexpr int STAGES = D <= 96 ? 4 : D <= 128 ? 3 : 2;
+    static constexpr int WARPS = D <= 64 ? 12 : D <= 128 ? 8 : 10;
     static constexpr uint32_t OFF_PLAN = WARPS * STAGES * STAGE, SMEM = OFF_PLAN + sizeof(PlanNear);
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
