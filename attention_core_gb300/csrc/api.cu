@@ -1136,7 +1136,8 @@ int paged_attend(const attn_core_paged_params* p, const ac::PrefixGroups* groups
 int check_lines(const attn_core_paged_params* p)
 {
     const int64_t lines = (int64_t)p->n_seq * p->h_kv, length = (int64_t)p->max_pages * p->page_size;
-    if (lines >= (int64_t)INT32_MAX / 16 || lines * (length / 64 + 2) >= (int64_t)INT32_MAX / 2)
+    if (length > ((int64_t)1 << 30) || lines >= (int64_t)INT32_MAX / 16 ||
+        lines * (length / 64 + 2) >= (int64_t)INT32_MAX / 2)
         return ATTN_CORE_ERR_UNSUPPORTED;
     return ATTN_CORE_OK;
 }

@@ -530,7 +530,10 @@ int attn_core_paged_weights(const attn_core_paged_params* p, const void* q, cons
  * So sequences that share pages move to others (PagePool.shrink).  weights_out may be weights.  keep is in device memory
  * and may exceed the length (all keys stay); negative entries, and lengths or
  * pages out of range, are table errors.  p's n_tokens, h_q and cu_seqlens_q are
- * not used (but checked as ever).  Two kernels; the result is exact.  Its workspace is about n_seq h_kv max_pages page_size / 8 bytes. */
+ * not used (but checked as ever).  Two kernels; the result is exact.  Limits
+ * (ATTN_CORE_ERR_UNSUPPORTED): max_pages * page_size <= 2^30, and n_seq h_kv
+ * (max_pages page_size / 64 + 2) < 2^30.  The workspace (256-byte aligned) is
+ * about n_seq h_kv max_pages page_size / 8 bytes. */
 size_t attn_core_paged_evict_workspace_bytes(const attn_core_paged_params* p);
 int attn_core_paged_evict(const attn_core_paged_params* p, const int32_t* keep, int32_t first, int32_t recent,
                           const int32_t* out_table, void* k_pages, void* v_pages, const float* weights,

@@ -118,6 +118,18 @@ def test_cut_items(hq, hkv, d, nq, nk):
     assert int(p.status.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,ps", [(8, 1, 128, 16), (6, 2, 96, 32), (32, 1, 64, 64), (3, 3, 160, 16)])
+def test_one_chunk_among_single_tokens(hq, hkv, d, ps):
+    """Batches of single tokens on average, which have row tiles of 32 rows, with one
+    sequence of many such tiles, whose items are cut."""
+    nq = [1] * 60 + [200] + [1] * 200
+    nk = [1 + (37 * i) % 400 for i in range(261)]
+    nk[60] = 700
+    p = Paged(nq, nk, hq, hkv, d, ps, seed=8)
+    run(p, decay=0.5, in_place=True)
+    assert int(p.status.item()) == 0
+
+
 def test_long_context():
     p = Paged([1, 1], [70000, 33000], 8, 1, 64, 128, seed=3)
     run(p)
