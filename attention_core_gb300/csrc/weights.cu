@@ -639,7 +639,7 @@ int launch_weights_t(const PagedMaps& m, const WeightsArgs& a, cudaStream_t st)
     if (want < grid) grid = want;
     kern<<<(unsigned)grid, kWeightsThreads, smem, st>>>(m, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
-    if (grid > 1 && (int64_t)a.t.n_tokens > (int64_t)kItemSnap * a.tpt) {     // else no sequence has items to cut
+    if (grid > 1 && (int64_t)a.t.n_tokens > (int64_t)(kItemSnap - 1) * a.tpt) {     // else no sequence has items to cut
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;
@@ -661,7 +661,7 @@ int weights_tile_rows(const PagedTables& t)
     const int64_t group = t.h_q / t.h_kv, items = ((int64_t)t.max_pages * t.page_size + kItemKeys - 1) / kItemKeys;
     // new tokens that make tiles of few rows, on average, and units that 31 bits count
     const bool few = group <= kFewWeightRows && t.n_tokens * group <= (int64_t)kFewWeightRows * t.n_seq &&
-                     (t.n_tokens / (kFewWeightRows / group) + 1) * items < INT32_MAX;
+                     (t.n_tokens / (kFewWeightRows / group) + 2) * items < INT32_MAX;
     return few ? kFewWeightRows : 128;
 }
 

@@ -47,7 +47,7 @@ static void one()
         int64_t sum = 0;
         for (int k = 0; k < s.items(); ++k) {
             WANT(s.units(k) == sum);
-            WANT(s.cost(k) >= 1);
+            WANT(s.cost(k) >= 2);
             for (int j = k * kItemKeys; j < s.kv && j < (k + 1) * kItemKeys; j += 1 + rand() % 60) {
                 const int m0 = s.first_tile(j);
                 WANT(m0 < s.tiles() && sees(s, m0, j) && (m0 == 0 || !sees(s, m0 - 1, j)));
@@ -81,13 +81,13 @@ static void one()
             WANT(x.nq == g.nq && x.kv == g.kv && g.q0 == cu[g.seq] && g.i1 > g.i0 && g.i1 <= x.items());
             if (g.whole) {
                 for (int i = g.i0; i < g.i1; ++i)
-                    pieces[{g.seq, g.head, i}].push_back({x.tiles() - x.cost(i), x.tiles(), c});
+                    pieces[{g.seq, g.head, i}].push_back({x.first_tile(i * kItemKeys), x.tiles(), c});
                 continue;
             }
             WANT(g.i1 == g.i0 + 1 && g.m1 > g.m0);
             pieces[{g.seq, g.head, g.i0}].push_back({g.m0, g.m1, c});
             ++cuts;
-            WANT(x.cost(g.i0) > kItemSnap && g.m1 - g.m0 < x.cost(g.i0));
+            WANT(x.cost(g.i0) > kItemSnap && g.m1 - g.m0 < x.tiles() - x.first_tile(g.i0 * kItemKeys));
             if (g.from_start) {
                 ++starts;
                 WANT(g.last_cta > c && g.last_cta < ctas);
