@@ -294,11 +294,12 @@ struct PagedArgs {
     int32_t num_sms;
     // batches whose sequences share their first pages (prefix.cu; set by its launcher)
     PrefixGroups groups;
-    const struct PrefixSeq* plan;   // null: the kernels make it themselves
+    const struct PrefixSeq* plan;   // null: the kernel makes it itself, and writes it to plan_out
+    struct PrefixSeq* plan_out;
     int32_t n_plan;
     uint64_t* records;          // where each row's parts lie
     size_t lse_offset;          // of the parts' LSEs in the workspace
-    const int64_t* many_units;  // of the sequences of many rows
+    int64_t* many_units;        // of the sequences of many rows
     int32_t few_waits;          // it follows the plan, not the kernel for many rows
 };
 size_t paged_ws_bytes(int d);

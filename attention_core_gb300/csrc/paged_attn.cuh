@@ -410,13 +410,24 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
 
     // the plan is another kernel's, this one's set-up so far runs beside it
     if constexpr (PREFIX) {
-        if (a.plan) asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // who may read the plan now, too
         PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN);
-        if (!a.plan)
-            plan_near(t, a.tpt, a.causal, a.groups, *near);
-        else
+        if (a.plan) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             __syncthreads();
+        } else {
+            // CTA 0 writes the plan down for the kernel for few rows, which starts once all
+            // CTAs have said that it may (its late blocks then leave after one look)
+            if (blockIdx.x) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            plan_near(t, a.tpt, a.causal, a.groups, *near);
+            if (blockIdx.x == 0) {
+                for (int i = threadIdx.x; i < a.n_plan; i += kThreads) a.plan_out[i] = near->seq[i];
+                if (threadIdx.x == 0) *a.many_units = (int64_t)near->many;
+                __threadfence();
+                __syncthreads();
+                asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            }
+        }
         // CTAs without a share make room at once for the kernel for few rows
         const int64_t many = a.plan ? *a.many_units : (int64_t)near->many;
         if ((many == 0 || (int64_t)blockIdx.x >= many_ctas(many, tab.plan[a.n_plan - 1].few_units, gridDim.x)) &&

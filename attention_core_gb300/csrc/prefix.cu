@@ -674,16 +674,16 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     a.groups = g;
     a.records = reinterpret_cast<uint64_t*>(a.ws + l.records);
     a.lse_offset = l.lse;
-    a.many_units = reinterpret_cast<const int64_t*>(a.ws + l.many);
+    a.many_units = reinterpret_cast<int64_t*>(a.ws + l.many);
     a.plan = nullptr;
+    a.plan_out = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
     cudaError_t e;
     if (a.n_plan > kPlanNear) {
-        PrefixSeq* plan = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
-        a.plan = plan;
+        a.plan = a.plan_out;
         const int n_records = t.n_tokens * t.h_q;
         const int clearing = n_records / (kPlanThreads * 8);
         prefix_plan_kernel<<<(unsigned)(clearing < 1 ? 1 : clearing < 64 ? clearing : 64), kPlanThreads, 0, st>>>(
-            t, a.tpt, a.causal, g, plan, a.records, n_records, reinterpret_cast<int64_t*>(a.ws + l.many));
+            t, a.tpt, a.causal, g, a.plan_out, a.records, n_records, a.many_units);
         if ((e = cudaGetLastError()) != cudaSuccess) return (int)e;
     }
     bool first = !a.plan;            // the first kernel waits for all that came before
@@ -714,8 +714,10 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
         const int64_t want = (kMostFewRows / kFewTile) * (int64_t)a.n_plan * t.h_kv * blocks;      // units, at most
         int64_t grid = a.num_sms < kPagedMaxCtas ? a.num_sms : kPagedMaxCtas;
         if (want < grid) grid = want;
-        if ((e = launch_behind(!first, kern, dim3((unsigned)grid), C::WARPS * 32, C::SMEM, st, a, q, k_pages, v_pages)) !=
-            cudaSuccess)
+        PagedArgs few = a;
+        if (!few.few_waits) few.plan = a.plan_out;         // the kernel for many rows has written it down
+        if ((e = launch_behind(!first, kern, dim3((unsigned)grid), C::WARPS * 32, C::SMEM, st, few, q, k_pages,
+                               v_pages)) != cudaSuccess)
             return (int)e;
     }
     const int64_t rows = (int64_t)t.n_tokens * t.h_q;
