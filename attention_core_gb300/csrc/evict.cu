@@ -10,8 +10,11 @@
 //   until H is reached.  The line is read once and kept in shared memory; a line longer
 //   than a block's share is split over the blocks of a cluster, whose histograms and
 //   counts are added through distributed shared memory.  Then every warp counts what
-//   stays of its run of keys by ballots, and places it.  Bound by latency: three
-//   histograms, two cluster barriers each.
+//   stays of its run of keys, four a lane at a time, and places it.  Bound by the passes'
+//   latency: three histograms (two copies of the first, whose bins weights crowd into) and
+//   two passes over the keys; 30 us for 512 lines of up to 8192 keys and for 8 of 131072.
+//   Two blocks a processor: with four, the waiting blocks of the next kernel found their
+//   places unevenly, and that kernel took 25 us longer.
 // move: chunks of 64 kept rows of K and V, 16-byte units through registers.  Bound by
 //   the rows' bytes, read and written once.  Rows may move within their own pages: kept
 //   row j came from src >= j, so the rows [a, a + 64) that a chunk overwrites are wanted
@@ -20,6 +23,9 @@
 //   in a flag, and writes once the chunks that read its rows (two at most, by select's
 //   ranks) have loaded: a chunk waits only for chunks that were handed out before, which
 //   wait for nothing before they have loaded.
+// Measured on one GB300, 8 KV heads of 128: 64 sequences of up to 8192 keys cut to 2048
+// 196 us (the move 165 of them, 6.4 TB/s), one of 131072 keys cut to 32768 74 us, one of
+// 600 keys 8 us in a graph.
 #include <cooperative_groups.h>
 #include <stddef.h>
 

@@ -8,7 +8,17 @@
 // TMEM lanes: a thread owns a key and adds up its columns, so the sum over rows needs no
 // exchange between threads, and each weight has one owner and one order of addition.
 //
-// Bounds: single tokens the keys' bytes; chunks the exponentials and the product alike.
+// Bounds: single tokens the keys' bytes; chunks the products (1024 cycles for a row tile
+// and 256 keys at d = 128) and the exponentials (1024: 4 cycles for a warp's), beside which
+// the issuing and summing warps' own work still stands.  Measured on one GB300:
+//   one new token of 64 sequences of up to 8192 keys, 64/8 heads of 128   114 us (6.0 TB/s)
+//   2048 new tokens over 8192 keys, 64/8 heads of 128            187 us (1.29 PFLOP/s)
+//   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160          43 us
+//   one new token over 500 keys                                     9 us in a graph
+// Tried and left out: a part of the exponentials by a polynomial on the FMA pipe (they do
+// not bound the loop: 190 -> 236 us); two issuing warps, one for each half (192 us, and one
+// launch in about 600 of single tokens ended in a launch failure whose cause was not
+// found; with one issuing warp 24000 launches gave the same bits).
 //
 // Persistent, one CTA per SM, equal shares of the work (weights_sched.cuh).  640 threads:
 //   warp 0  runs of items, in a ring of jobs that the others read, and their K by TMA: an
