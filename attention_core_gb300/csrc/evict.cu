@@ -38,7 +38,6 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kMoveRows = 64, kMoveThreads = 256;
 constexpr int kBins = 2048;
 constexpr int kMostCached = 45056;       // keys that a block keeps in shared memory (176 KB)
@@ -91,16 +90,20 @@ __device__ __forceinline__ Line read_line(const EvictArgs& a, int seq)
 
 struct alignas(16) SelectShared {
     uint32_t hist[2][kBins];         // two copies in the first pass
-    uint32_t warp_sum[kSelectWarps];
+    uint32_t warp_sum[32];
     uint32_t bin, above;             // of the pass: where H falls, keys above it
-    uint32_t warp_tie[kSelectWarps];
+    uint32_t warp_tie[32];
     uint32_t block_stay, block_tie;
 };
 
 }  // namespace
 
-__global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const EvictArgs a)
+// T threads: 512, two blocks a processor; 1024 where lines are split over clusters, whose
+// processors have one block each.
+template <int T>
+__global__ void __launch_bounds__(T, 1024 / T) evict_select_kernel(const EvictArgs a)
 {
+    constexpr int kSelectThreads = T, kSelectWarps = T / 32, B = kBins / T;     // B bins a thread
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) float cache[];        // keys; behind them, in clusters, the added histogram
     __shared__ SelectShared sh;
@@ -188,13 +191,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const E
                 cluster.sync();
                 total = sum_of;
             }
-            // sum from the top: thread i has the bins 2047 - 4 i down to 2044 - 4 i
-            uint4 v = reinterpret_cast<const uint4*>(total)[kBins / 4 - 1 - tid];
-            if (C == 1 && second) {
-                const uint4 v1 = reinterpret_cast<const uint4*>(sh.hist[1])[kBins / 4 - 1 - tid];
-                v = make_uint4(v.x + v1.x, v.y + v1.y, v.z + v1.z, v.w + v1.w);
+            // sum from the top: thread i has the B bins down from 2047 - B i
+            uint32_t v[B], sum = 0;
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const int b = kBins - 1 - B * tid - i;
+                v[i] = total[b];
+                if (C == 1 && second) v[i] += sh.hist[1][b];
+                sum += v[i];
             }
-            const uint32_t sum = v.x + v.y + v.z + v.w;
             uint32_t upto = sum;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -208,14 +213,13 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const E
             upto += before;
             uint32_t above = upto - sum;
             if (above < want && want <= upto) {
-                const uint32_t n4[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (above < want && want <= above + n4[i]) {
-                        sh.bin = (uint32_t)(kBins - 1 - 4 * tid - i);
+                for (int i = 0; i < B; ++i) {
+                    if (above < want && want <= above + v[i]) {
+                        sh.bin = (uint32_t)(kBins - 1 - B * tid - i);
                         sh.above = above;
                     }
-                    above += n4[i];
+                    above += v[i];
                 }
             }
             __syncthreads();
@@ -437,11 +441,13 @@ int launch_evict_t(const EvictArgs& args, cudaStream_t st)
     // processors idle.
     int C = 1;
     while (C < 8 && length / C > 4096 && lines * C * 2 <= a.num_sms) C *= 2;
-    const int64_t share = ((length + (int64_t)C * kSelectWarps * 64 - 1) / ((int64_t)C * kSelectWarps * 64)) * 64 * kSelectWarps;
+    const int threads = C > 1 ? 1024 : 512;
+    const int64_t step = (int64_t)threads * 4;             // keys that a block has at a time
+    const int64_t share = (length + C * step - 1) / (C * step) * step;
     a.cached = (int)(share < kMostCached ? share : kMostCached);
     const uint32_t smem = (uint32_t)a.cached * sizeof(float) + (C > 1 ? kBins * sizeof(uint32_t) : 0);
-    if ((e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-        cudaSuccess)
+    auto select = C > 1 ? evict_select_kernel<1024> : evict_select_kernel<512>;
+    if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
         return (int)e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -449,12 +455,12 @@ int launch_evict_t(const EvictArgs& args, cudaStream_t st)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(lines * C));
-    cfg.blockDim = dim3(kSelectThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a)) != cudaSuccess) return (int)e;
+    if ((e = cudaLaunchKernelEx(&cfg, select, a)) != cudaSuccess) return (int)e;
 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -160,6 +160,15 @@ def test_groups_that_do_not_fit_are_reported(starts, pages):
     assert int(p.status.item()) == ac.ERR_DEVICE_TABLE
 
 
+def test_tokens_without_a_key():
+    """New tokens of sequences that hold nothing, in a group and outside."""
+    p = shared([(3, 0)], [1, 2, 1], [0, 0, 5], 8, 2, 128, 16, outside=[(1, 0), (40, 0), (1, 3)])
+    o, lse = run(p)
+    check_attention(o, lse, attend(p), p)
+    assert (lse[:, :3] == -math.inf).all() and (o[4:45] == 0).all()
+    assert int(p.status.item()) == 0
+
+
 def test_more_pages_than_the_sequences_hold():
     p = shared([(2, 4)], [1, 1], [1, 1], 8, 2, 128, 16)
     p.pages.fill_(1 << 30)
