@@ -15,7 +15,8 @@
 //   2048 new tokens over 8192 keys, 64/8 heads of 128            187 us (1.29 PFLOP/s)
 //   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160          43 us
 //   one new token over 500 keys                                     9 us in a graph
-// Tried and left out: a part of the exponentials by a polynomial on the FMA pipe (they do
+// Tried and left out: row tiles of 256 rows whose columns a half's two warpgroups share (half
+// the products and commits, one score buffer a half: 203 us); a part of the exponentials by a polynomial on the FMA pipe (they do
 // not bound the loop: 190 -> 236 us); two issuing warps, one for each half (192 us, and one
 // launch in about 600 of single tokens ended in a launch failure whose cause was not
 // found; with one issuing warp 24000 launches gave the same bits).
@@ -410,8 +411,11 @@ paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a
             const ItemShape s = shape(g);
             const int tiles = s.tiles(), m1 = g.whole ? tiles : g.m1;
             const int last_rows = (g.nq - (tiles - 1) * tpt) * group;
-            const uint32_t ids_all = idesc_bf16(128, 0, false, false) | (uint32_t)((tpt * group + 15) / 16 * 2) << 17;
-            const uint32_t ids_last = idesc_bf16(128, 0, false, false) | (uint32_t)((last_rows + 15) / 16 * 2) << 17;
+            // all of a full tile's columns, those of rows that no tile has among them: they are read
+            const uint32_t ids_all = idesc_bf16(128, ROWS, false, false);
+            const uint32_t ids_last =
+                last_rows == tpt * group
+                    ? ids_all : idesc_bf16(128, 0, false, false) | (uint32_t)((last_rows + 15) / 16 * 2) << 17;
             for (int i = g.i0; ok && i < g.i1; ++i) {
                 const bool two = g.kv - i * kItemKeys > 128;
                 const int first = g.whole ? s.first_tile(i * kItemKeys) : g.m0;

@@ -100,8 +100,29 @@ def test_chunks(hq, hkv, d, ps, causal):
     assert int(p.status.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,ps,nq", [(48, 1, 64, 16, 30), (56, 1, 128, 32, 40), (100, 1, 96, 64, 12), (48, 1, 128, 16, 300),
+                                            (34, 2, 64, 16, 200), (6, 2, 128, 64, 1400), (33, 1, 160, 16, 90)])
+def test_head_groups_that_leave_much_of_a_tile(hq, hkv, d, ps, nq):
+    """Row tiles with rows that no token has, after scores of NaN in the same columns
+    (what the tensor memory held before must not count)."""
+    bad = Paged([nq], [nq + 300], hq, hkv, d, ps, seed=9)
+    lse = torch.zeros(hq, nq, device=DEV)
+    bad.q.fill_(math.nan)
+    w = torch.zeros((1, hkv, bad.table.shape[1] * ps), device=DEV)
+    ac.paged_weights(bad.batch(), bad.q, lse, bad.k_pages, w)
+    full = Paged([128], [500], 1, 1, d, ps, seed=9)
+    full.q.fill_(math.nan)
+    for n in (128, 32):
+        ac.paged_weights(full.batch(), full.q, torch.zeros(1, 128, device=DEV), full.k_pages,
+                         torch.zeros((1, 1, full.table.shape[1] * ps), device=DEV))
+    p = Paged([nq, 3], [nq + 300, 40], hq, hkv, d, ps, seed=9)
+    run(p)
+    assert int(p.status.item()) == 0
+
+
 @pytest.mark.parametrize("hq,hkv,d,nq,nk", [(16, 2, 128, 1500, 2100), (8, 8, 96, 900, 900), (5, 1, 64, 1025, 5000),
-                                            (4, 2, 160, 2000, 2300)])
+                                            (4, 2, 160, 2000, 2300), (64, 1, 128, 70, 900), (1, 1, 64, 5000, 5000),
+                                            (2, 1, 96, 1100, 400)])
 def test_cut_items(hq, hkv, d, nq, nk):
     """Many row tiles over few keys: items are cut and their parts joined; the same
     bits again, on another stream, with anything in the workspace."""
