@@ -184,7 +184,8 @@ class PagePool:
         for i, (s, n) in enumerate(zip(seqs, lengths)):
             old, need = self._pages[s], -(-n // self.page_size)
             new = [self._take() if p in shared else p for p in old[:need]]
-            gone += [p for p in old if p not in set(new)]
+            stays = set(new)
+            gone += [p for p in old if p not in stays]
             table[i, :need] = new
             self._pages[s], self._length[s] = new, n
         for p in gone:
