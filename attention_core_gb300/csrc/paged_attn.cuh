@@ -419,6 +419,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             // CTA 0 writes the plan down for the kernel for few rows, which starts once all
             // CTAs have said that it may (its late blocks then leave after one look)
             if (blockIdx.x) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            prefetch_table(t);
             plan_near(t, a.tpt, a.causal, a.groups, *near);
             if (blockIdx.x == 0) {
                 for (int i = threadIdx.x; i < a.n_plan; i += kThreads) a.plan_out[i] = near->seq[i];

@@ -307,9 +307,10 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
     const uint32_t ring = smem_u32(smem_raw) + warp * C::STAGES * C::STAGE;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + C::OFF_PLAN);
-    if (!a.plan)
+    if (!a.plan) {
+        prefetch_table(t);
         plan_near(t, a.tpt, a.causal, a.groups, *near);
-    else if (a.few_waits)
+    } else if (a.few_waits)
         asm volatile("griddepcontrol.wait;" ::: "memory");
     const PlanView plan{a.plan ? a.plan : near->seq, a.n_plan, !a.plan};
 
@@ -560,7 +561,7 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
 
 // A warp per (new token, query head): the parts of the row's own keys' tile, then of
 // the group's.  As the join of cut tiles (paged.cu), with the rows found by records.
-template <int D>
+template <int D, int AHEAD>
 __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -606,7 +607,8 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     };
     const float* lse = reinterpret_cast<const float*>(a.ws + a.lse_offset);
     const float* rows = reinterpret_cast<const float*>(a.ws) + lane;
-    constexpr int E = D / 32, AHEAD = E <= 4 ? 16 : 8;      // divides 32
+    constexpr int E = D / 32;
+    static_assert(32 % AHEAD == 0, "parts 32 at a time");
     float x[AHEAD][E];
     auto load = [&](int p0) {
 #pragma unroll
@@ -727,8 +729,11 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
                                v_pages)) != cudaSuccess)
             return (int)e;
     }
-    const int64_t rows = (int64_t)t.n_tokens * t.h_q;
-    return (int)launch_behind(true, prefix_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, st, a);
+    // Sixteen parts' loads at a time where few rows have many parts; eight where there are
+    // more rows than those blocks' registers let in at once (64 samples: 3 us less).
+    const int64_t blocks = ((int64_t)t.n_tokens * t.h_q + 3) / 4;
+    auto join = D <= 128 && blocks <= 6 * (int64_t)a.num_sms ? prefix_join_kernel<D, 16> : prefix_join_kernel<D, 8>;
+    return (int)launch_behind(true, join, dim3((unsigned)blocks), 128, 0, st, a);
 }
 
 }  // namespace

@@ -80,6 +80,15 @@ __device__ __forceinline__ int64_t assign(PrefixSeq& v, const PagedTables& t, in
     return 0;
 }
 
+// The page table towards L2, a line a thread, while the plan is made: whoever loads keys
+// waits for its entries next.
+__device__ __forceinline__ void prefetch_table(const PagedTables& t)
+{
+    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (at * 32 < (int64_t)t.n_seq * t.max_pages)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(t.page_table + at * 32) : "memory");
+}
+
 // The plan of a batch of few sequences, which each block makes for itself in shared
 // memory: 2 us, where a kernel for it and the wait for that one cost 5.
 constexpr int kPlanNear = 128;                       // sequences and groups together
