@@ -25,7 +25,7 @@
 //   wait for nothing before they have loaded.
 // Measured on one GB300, 8 KV heads of 128: 64 sequences of up to 8192 keys cut to 2048
 // 196 us (the move 165 of them, 6.4 TB/s), one of 131072 keys cut to 32768 74 us, one of
-// 600 keys 8 us in a graph.
+// 600 keys 7 us in a graph.
 #include <cooperative_groups.h>
 #include <stddef.h>
 

@@ -17,7 +17,7 @@
 //   join   a warp per row adds its parts up
 //
 // Measured on one GB300 (64/8 heads of 128 but where said): 64 samples of a prompt of 8192
-// keys with up to 500 of their own 46 us (paged_fwd over the same batch: 218), 16 questions
+// keys with up to 500 of their own 43 us (paged_fwd over the same batch: 218), 16 questions
 // about 131072 keys 105 us (5.2 TB/s; 820), 6 prompts of up to 4000 keys with 8 samples each, 8/8
 // heads of 96, 42 us (86), 2 x 16 sequences with up to 8 drafted tokens over 2000 keys, 16 heads
 // of 160, 29 us (85), four samples of 512 keys 12 us in a graph.  What bounds the short ones is

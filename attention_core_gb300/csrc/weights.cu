@@ -12,7 +12,7 @@
 // and 256 keys at d = 128) and the exponentials (1024: 4 cycles for a warp's), beside which
 // the issuing and summing warps' own work still stands.  Measured on one GB300:
 //   one new token of 64 sequences of up to 8192 keys, 64/8 heads of 128   114 us (6.0 TB/s)
-//   2048 new tokens over 8192 keys, 64/8 heads of 128            187 us (1.29 PFLOP/s)
+//   2048 new tokens over 8192 keys, 64/8 heads of 128            186 us (1.30 PFLOP/s)
 //   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160          43 us
 //   one new token over 500 keys                                     9 us in a graph
 // Tried and left out: row tiles of 256 rows whose columns a half's two warpgroups share (half
