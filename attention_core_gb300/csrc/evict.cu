@@ -447,7 +447,10 @@ int launch_evict_t(const EvictArgs& args, cudaStream_t st)
     a.cached = (int)(share < kMostCached ? share : kMostCached);
     const uint32_t smem = (uint32_t)a.cached * sizeof(float) + (C > 1 ? kBins * sizeof(uint32_t) : 0);
     auto select = C > 1 ? evict_select_kernel<1024> : evict_select_kernel<512>;
-    if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    // The limit is the kernel's, not the call's: a size that follows the lengths would be
+    // lowered by another thread's shorter lines between here and this call's launch.
+    constexpr int most_smem = kMostCached * sizeof(float) + kBins * sizeof(uint32_t);
+    if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem)) != cudaSuccess)
         return (int)e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
