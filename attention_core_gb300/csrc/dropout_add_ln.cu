@@ -343,6 +343,16 @@ dal_reduce_kernel(const DalArgs a, int n_part)
 
 namespace {
 
+// The dynamic shared memory that a kernel for up to `columns` columns may take, 8 bytes
+// each.  The limit is the kernel's, not the call's: one that follows the call's hidden
+// size would be lowered by another thread's shorter rows before this call's launch.
+template <typename K>
+cudaError_t allow_columns(K kern, int columns)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                8 * (columns < kDalMaxHidden ? columns : kDalMaxHidden));
+}
+
 // Grids: as many CTAs as are resident at once (rows are grid-strided), so no
 // CTA waits for another to finish before it starts.
 template <typename K>
@@ -361,7 +371,7 @@ int launch_fwd_nv(bool drop, const DalArgs& a, int sms, cudaStream_t st)
 {
     const int smem = 8 * a.hidden;     // two stages of an x row and a residual row (bf16)
     auto kern = drop ? dal_fwd_kernel<NV, true> : dal_fwd_kernel<NV, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_columns(kern, 8 * kFwdThreads * NV);
     if (e != cudaSuccess) return (int)e;
     int grid = 0;
     if (int rc = resident_grid(kern, kFwdThreads, smem, sms, a.n_rows, &grid)) return rc;
@@ -374,7 +384,7 @@ int launch_bwd_nv(bool drop, const DalArgs& a, int sms, cudaStream_t st)
 {
     const int smem = 8 * a.hidden;     // [2][hidden] fp32 column sums
     auto kern = drop ? dal_bwd_kernel<NV, true, NT> : dal_bwd_kernel<NV, false, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_columns(kern, 8 * NT * NV);
     if (e != cudaSuccess) return (int)e;
     const int cap = a.n_rows < kDalMaxPartial ? a.n_rows : kDalMaxPartial;
     int grid = 0;
