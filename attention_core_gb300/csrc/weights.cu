@@ -129,7 +129,9 @@ __device__ __forceinline__ bool next_run(WeightsBars* bars, const WaitCtx& wc, R
 
 }  // namespace
 
-template <int D, int ROWS>
+// PADDED: row tiles of 128 with rows that no tile has, whose scores of infinite keys are
+// looked for: 3% of a chunk's time, which batches of full tiles go without.
+template <int D, int ROWS, bool PADDED>
 __global__ void __launch_bounds__(kWeightsThreads, 1)
 paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a)
 {
@@ -171,7 +173,7 @@ paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a
         tmem_relinquish();
     }
     // Rows that no tile has (head groups that do not divide the tile): zeros, so that their
-    // scores are finite and -inf takes their place in the exponent.
+    // scores of finite keys are finite and -inf takes their place in the exponent.
     const int tile_rows = a.tpt * a.group;
     if (tile_rows < ROWS) {
         for (int s = 0; s < C::SQ; ++s)
@@ -518,8 +520,10 @@ paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a
                             const float* nl = bars->nlse[rq.slot];
                             const uint4 counts = *reinterpret_cast<const uint4*>(bars->counts[rq.slot]);
                             const int pos = e + m * tpt;                        // of the tile's first token
-                            if (!C::FEW && (counts.x & counts.y & counts.z & counts.w) == 0xffffffffu &&
-                                (!a.causal || key0 + 127 <= pos)) {
+                            const bool plain = !C::FEW && (counts.x & counts.y & counts.z & counts.w) == 0xffffffffu &&
+                                               (!a.causal || key0 + 127 <= pos);
+                            float part = 0.f;
+                            if (plain) {
                                 uint64_t acc[4] = {0, 0, 0, 0};
                                 uint32_t x[2][32];       // the next 32 columns are on their way
                                 tmem_ld32_issue(tS, x[0]);
@@ -544,13 +548,17 @@ paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a
                                 }
                                 float lo, hi;
                                 f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
-                                sum += lo + hi;
-                            } else {
+                                part = lo + hi;
+                            }
+                            // an infinite key's score is NaN in the rows that no tile has (0 x inf): it is
+                            // summed again, without them
+                            const bool again = plain && part != part;
+                            if (!plain || (PADDED && __any_sync(0xffffffffu, again))) {
                                 // rows that do not count, or whose mask hides this key, are left out
                                 // whatever their score is
                                 const int rows = (g.nq - m * tpt < tpt ? g.nq - m * tpt : tpt) * group;
                                 const int skip0 = a.causal && key > pos ? (key - pos) * group : 0;
-                                float part = 0.f;
+                                float counted = 0.f;
 #pragma unroll 1
                                 for (int c0 = 0; c0 < rows; c0 += 32) {
                                     uint32_t x[32];
@@ -565,10 +573,11 @@ paged_weights_kernel(const __grid_constant__ PagedMaps maps, const WeightsArgs a
                                         const float p = ex2_approx(fmaf(__uint_as_float(x[c]), a.scale_log2, nl[c0 + c]));
                                         if (bits >> c & 1) p4[c & 3] += p;
                                     }
-                                    part += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                                    counted += (p4[0] + p4[1]) + (p4[2] + p4[3]);
                                 }
-                                sum += part;
+                                if (!plain || again) part = counted;
                             }
+                            sum += part;
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar(bars->s_empty[w][u]));
@@ -639,11 +648,11 @@ size_t weights_ws_bytes() { return kWeightsParts + kPagedMaxCtas * sizeof(CutIte
 
 namespace {
 
-template <int D, int ROWS>
+template <int D, int ROWS, bool PADDED>
 int launch_weights_t(const PagedMaps& m, const WeightsArgs& a, cudaStream_t st)
 {
     constexpr uint32_t smem = WeightsCfg<D, ROWS>::SMEM;
-    auto kern = paged_weights_kernel<D, ROWS>;
+    auto kern = paged_weights_kernel<D, ROWS, PADDED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return (int)e;
     const int64_t tiles = ((int64_t)a.t.n_tokens + a.tpt - 1) / a.tpt + a.t.n_seq;
@@ -681,12 +690,17 @@ int weights_tile_rows(const PagedTables& t)
 
 int launch_weights(const PagedMaps& m, const WeightsArgs& a, cudaStream_t st)
 {
-    const bool few = a.rows == kFewWeightRows;
+    const auto launch = [&](auto head_dim) {
+        constexpr int D = decltype(head_dim)::value;
+        if (a.rows == kFewWeightRows) return launch_weights_t<D, kFewWeightRows, false>(m, a, st);
+        return a.tpt * a.group < a.rows ? launch_weights_t<D, 128, true>(m, a, st)
+                                        : launch_weights_t<D, 128, false>(m, a, st);
+    };
     switch (a.d) {
-        case 64: return few ? launch_weights_t<64, kFewWeightRows>(m, a, st) : launch_weights_t<64, 128>(m, a, st);
-        case 96: return few ? launch_weights_t<96, kFewWeightRows>(m, a, st) : launch_weights_t<96, 128>(m, a, st);
-        case 128: return few ? launch_weights_t<128, kFewWeightRows>(m, a, st) : launch_weights_t<128, 128>(m, a, st);
-        case 160: return few ? launch_weights_t<160, kFewWeightRows>(m, a, st) : launch_weights_t<160, 128>(m, a, st);
+        case 64: return launch(std::integral_constant<int, 64>());
+        case 96: return launch(std::integral_constant<int, 96>());
+        case 128: return launch(std::integral_constant<int, 128>());
+        case 160: return launch(std::integral_constant<int, 160>());
         default: return (int)cudaErrorInvalidValue;
     }
 }
