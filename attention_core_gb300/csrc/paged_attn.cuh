@@ -411,8 +411,16 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     // the plan is another kernel's, this one's set-up so far runs beside it
     if constexpr (PREFIX) {
         PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN);
+        // The kernel for few rows may start from launch_dependents on, which orders no memory:
+        // CTA 0 releases the call's stamp once the plan is there, and that kernel acquires it.
+        auto plan_is_ready = [&] {
+            if (threadIdx.x == 0)
+                asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.plan_ready), "l"(a.stamp) : "memory");
+            __syncthreads();
+        };
         if (a.plan) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (blockIdx.x == 0) plan_is_ready();
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             __syncthreads();
         } else {
@@ -424,8 +432,8 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
             if (blockIdx.x == 0) {
                 for (int i = threadIdx.x; i < a.n_plan; i += kThreads) a.plan_out[i] = near->seq[i];
                 if (threadIdx.x == 0) *a.many_units = (int64_t)near->many;
-                __threadfence();
                 __syncthreads();
+                plan_is_ready();
                 asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             }
         }

@@ -22,6 +22,9 @@
 // heads of 96, 42 us (86), 2 x 16 sequences with up to 8 drafted tokens over 2000 keys, 16 heads
 // of 160, 29 us (85), four samples of 512 keys 12 us in a graph.  What bounds the short ones is
 // the chain plan - set-up - first loads (8 us) and the join behind (5 us).
+#include <atomic>
+#include <chrono>
+
 #include "paged_attn.cuh"
 
 namespace ac {
@@ -33,7 +36,8 @@ constexpr int kPlanThreads = 1024;
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Workspace: rows [parts of cut tiles | whole tiles' rows, twice | parts of cut tiles of
-// few rows] of d floats, their base-2 LSEs, the records, the plan.
+// few rows] of d floats, their base-2 LSEs, the records, the plan, its units of many rows
+// and the call's stamp.
 constexpr int kFewWarps = kPagedMaxCtas * 12;     // of the kernel for few rows, at most
 struct PrefixLayout {
     size_t lse, records, plan, many, bytes;
@@ -153,8 +157,8 @@ struct FewCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
-// The plan, in shared memory or written by its kernel, which ended before this one began;
-// but this one waits for no kernel before it reads, so it reads that past L1.
+// The plan, in shared memory or in the workspace, where it is read past L1: there a kernel
+// wrote it that may still be running (await_plan).
 struct PlanView {
     const PrefixSeq* seq;
     int n;
@@ -173,6 +177,21 @@ struct PlanView {
         return u.v;
     }
 };
+
+// The plan is ready, and so is all that came before the call: the kernel for many rows,
+// beside which this one runs, has released the call's stamp, before it said that this one
+// may start.  So one look finds it; where several do not, this kernel waits for that one's
+// end, which shows all that it wrote.
+__device__ __forceinline__ void await_plan(const PagedArgs& a)
+{
+    bool ready = false;
+    for (int looks = 0; looks < 64 && !ready; ++looks) {
+        uint64_t seen;
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(a.plan_ready) : "memory");
+        ready = seen == a.stamp;
+    }
+    if (!__all_sync(0xffffffffu, ready)) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 struct FewSegment {
     PrefixSeq v;
@@ -312,6 +331,8 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
         plan_near(t, a.tpt, a.causal, a.groups, *near);
     } else if (a.few_waits)
         asm volatile("griddepcontrol.wait;" ::: "memory");
+    else
+        await_plan(a);
     const PlanView plan{a.plan ? a.plan : near->seq, a.n_plan, !a.plan};
 
     // The line's length, and 32 places of it in the same look: this warp's share starts
@@ -566,6 +587,8 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedTables& t = a.t;
+    // a replay of the call from a graph has the same stamp, and may not find it
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.plan_ready = 0;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (int64_t)t.n_tokens * t.h_q) return;
     const int lane = threadIdx.x & 31;
@@ -673,6 +696,14 @@ cudaError_t launch_behind(bool early, void (*kern)(Args...), dim3 grid, int thre
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// A number for each call, from a start that what lies in memory is not (the workspace's
+// contents before a call do not matter).
+uint64_t next_stamp()
+{
+    static std::atomic<uint64_t> next{((uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() << 20) | 1};
+    return next.fetch_add(1, std::memory_order_relaxed);
+}
+
 template <int D>
 int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, const uint16_t* q, const uint16_t* k_pages,
                     const uint16_t* v_pages, cudaStream_t st)
@@ -684,6 +715,8 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     a.records = reinterpret_cast<uint64_t*>(a.ws + l.records);
     a.lse_offset = l.lse;
     a.many_units = reinterpret_cast<int64_t*>(a.ws + l.many);
+    a.plan_ready = reinterpret_cast<uint64_t*>(a.many_units) + 1;
+    a.stamp = next_stamp();
     a.plan = nullptr;
     a.plan_out = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
     cudaError_t e;
