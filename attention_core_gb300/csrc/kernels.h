@@ -300,8 +300,8 @@ struct PagedArgs {
     uint64_t* records;          // where each row's parts lie
     size_t lse_offset;          // of the parts' LSEs in the workspace
     int64_t* many_units;        // of the sequences of many rows
-    uint64_t* plan_ready;       // holds this call's stamp from when the plan and many_units may be read
-    uint64_t stamp;             //   until the call's end: a number that no call before had
+    uint64_t* stamp_at;         // what the kernel for many rows says to the one for few: `stamp`, it has
+    uint64_t stamp;             //   begun, stamp + 1, plan_out and many_units are written; no call before had them
     int32_t few_waits;          // it follows the plan, not the kernel for many rows
 };
 size_t paged_ws_bytes(int d);

@@ -411,30 +411,27 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     // the plan is another kernel's, this one's set-up so far runs beside it
     if constexpr (PREFIX) {
         PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + pad + C::OFF_PLAN);
-        // The kernel for few rows may start from launch_dependents on, which orders no memory:
-        // CTA 0 releases the call's stamp once the plan is there, and that kernel acquires it.
-        auto plan_is_ready = [&] {
-            if (threadIdx.x == 0)
-                asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.plan_ready), "l"(a.stamp) : "memory");
-            __syncthreads();
+        // the kernel for few rows, which starts beside this one, goes by what CTA 0 says
+        // (plan_written)
+        auto say = [&](uint64_t what) {
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.stamp_at), "l"(a.stamp + what) : "memory");
         };
         if (a.plan) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            if (blockIdx.x == 0) plan_is_ready();
+            say(1);
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             __syncthreads();
         } else {
-            // CTA 0 writes the plan down for the kernel for few rows, which starts once all
-            // CTAs have said that it may (its late blocks then leave after one look)
-            if (blockIdx.x) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            say(0);
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             prefetch_table(t);
             plan_near(t, a.tpt, a.causal, a.groups, *near);
             if (blockIdx.x == 0) {
                 for (int i = threadIdx.x; i < a.n_plan; i += kThreads) a.plan_out[i] = near->seq[i];
                 if (threadIdx.x == 0) *a.many_units = (int64_t)near->many;
                 __syncthreads();
-                plan_is_ready();
-                asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                say(1);
             }
         }
         // CTAs without a share make room at once for the kernel for few rows

@@ -178,19 +178,27 @@ struct PlanView {
     }
 };
 
-// The plan is ready, and so is all that came before the call: the kernel for many rows,
-// beside which this one runs, has released the call's stamp, before it said that this one
-// may start.  So one look finds it; where several do not, this kernel waits for that one's
-// end, which shows all that it wrote.
-__device__ __forceinline__ void await_plan(const PagedArgs& a)
+// What the kernel for many rows says to this one, which starts beside it: launch_dependents
+// orders no memory, so CTA 0 there releases the call's stamp, first as soon as it begins
+// and again, one higher, once the plan is written.  Either shows all that came before the
+// call, the second the plan; a block that finds the first plans for itself, rather than
+// wait (late blocks, which mostly find no share left, read the plan).  Where neither is
+// there after several looks, the wait for that kernel's end shows everything.
+__device__ __forceinline__ bool plan_written(const PagedArgs& a)
 {
-    bool ready = false;
-    for (int looks = 0; looks < 64 && !ready; ++looks) {
+    __shared__ uint64_t said;
+    if (threadIdx.x == 0) {
         uint64_t seen;
-        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(a.plan_ready) : "memory");
-        ready = seen == a.stamp;
+        int looks = 0;
+        do
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(a.stamp_at) : "memory");
+        while ((seen -= a.stamp) > 1 && ++looks < 64);
+        said = seen;
     }
-    if (!__all_sync(0xffffffffu, ready)) asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    if (said == 0 && a.n_plan <= kPlanNear) return false;
+    if (said != 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return true;
 }
 
 struct FewSegment {
@@ -326,20 +334,19 @@ prefix_few_kernel(const PagedArgs a, const uint16_t* q, const uint16_t* k_pages,
     const uint32_t ring = smem_u32(smem_raw) + warp * C::STAGES * C::STAGE;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     PlanNear* near = reinterpret_cast<PlanNear*>(smem_raw + C::OFF_PLAN);
-    if (!a.plan) {
-        prefetch_table(t);
+    if (a.few_waits) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool at_hand = a.few_waits ? !a.plan : !plan_written(a);
+    if (at_hand) {
+        if (a.few_waits) prefetch_table(t);
         plan_near(t, a.tpt, a.causal, a.groups, *near);
-    } else if (a.few_waits)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-    else
-        await_plan(a);
-    const PlanView plan{a.plan ? a.plan : near->seq, a.n_plan, !a.plan};
+    }
+    const PlanView plan{at_hand ? near->seq : a.plan, a.n_plan, at_hand};
 
     // The line's length, and 32 places of it in the same look: this warp's share starts
     // between two of them.
     const int step = (a.n_plan + 31) / 32;
     const int last = (lane + 1) * step < a.n_plan ? (lane + 1) * step - 1 : a.n_plan - 1;
-    const int64_t upto = plan.units(last), many = a.plan ? __ldcg(a.many_units) : (int64_t)near->many;
+    const int64_t upto = plan.units(last), many = at_hand ? (int64_t)near->many : __ldcg(a.many_units);
     const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
     const int blocks = (int)gridDim.x - (many > 0 ? (int)many_ctas(many, total, gridDim.x) : 0);
     const int n_blocks = blocks > 0 ? blocks : 1;
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PagedArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedTables& t = a.t;
     // a replay of the call from a graph has the same stamp, and may not find it
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.plan_ready = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.stamp_at = 0;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (int64_t)t.n_tokens * t.h_q) return;
     const int lane = threadIdx.x & 31;
@@ -696,12 +703,12 @@ cudaError_t launch_behind(bool early, void (*kern)(Args...), dim3 grid, int thre
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// A number for each call, from a start that what lies in memory is not (the workspace's
+// Two numbers for each call, from a start that what lies in memory is not (the workspace's
 // contents before a call do not matter).
 uint64_t next_stamp()
 {
-    static std::atomic<uint64_t> next{((uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() << 20) | 1};
-    return next.fetch_add(1, std::memory_order_relaxed);
+    static std::atomic<uint64_t> next{((uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() << 20) | 2};
+    return next.fetch_add(2, std::memory_order_relaxed);
 }
 
 template <int D>
@@ -715,7 +722,7 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     a.records = reinterpret_cast<uint64_t*>(a.ws + l.records);
     a.lse_offset = l.lse;
     a.many_units = reinterpret_cast<int64_t*>(a.ws + l.many);
-    a.plan_ready = reinterpret_cast<uint64_t*>(a.many_units) + 1;
+    a.stamp_at = reinterpret_cast<uint64_t*>(a.many_units) + 1;
     a.stamp = next_stamp();
     a.plan = nullptr;
     a.plan_out = reinterpret_cast<PrefixSeq*>(a.ws + l.plan);
