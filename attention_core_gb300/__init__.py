@@ -863,7 +863,10 @@ class PagedBatch:
     ``group_starts`` [n_groups + 1] and ``prefix_pages`` [n_groups], two more such
     tables, make it a batch for paged_prefix_fwd: the sequences group_starts[g] ..
     group_starts[g + 1] - 1 name the same pages in their first prefix_pages[g]
-    columns (PagePool.groups finds them)."""
+    columns (PagePool.groups finds them).  A smaller count costs speed; one that
+    reaches into columns that differ gives wrong results, unnoticed, so the counts
+    follow the page table (a fork's copied page, PagePool.shrink), also where a
+    captured graph is replayed."""
 
     def __init__(self, cu_seqlens_q, kv_lens, page_table, *, n_tokens: int, h_q: int, h_kv: int, d: int,
                  page_size: int, n_pages: int, causal: bool = True, scale: float = 0.0, dev_status: int = 0,

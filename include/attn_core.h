@@ -480,7 +480,12 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
  * in device memory (group_starts [n_groups + 1], prefix_pages [n_groups]) and
  * followed by captured graphs; groups may be empty, and sequences outside all
  * groups share nothing.  Of a group's pages those count that all its sequences
- * (which have new tokens) hold before their first new token.  Groups that are
+ * (which have new tokens) hold before their first new token, so a count beyond
+ * their lengths does no harm, nor does one that is smaller than what they
+ * share, 0 among them.  A count beyond the columns in which the rows really
+ * agree is not noticed: the sequences then attend to another one's keys there.
+ * So counts are lowered, under a captured graph too, whenever a row's page is
+ * replaced (copied before a write, or moved by an eviction).  Groups that are
  * out of order or range write ATTN_CORE_ERR_DEVICE_TABLE to dev_status and
  * share nothing.  1 <= n_groups <= n_seq.  The workspace holds the rows of
  * shared and own keys in fp32 until they are joined: about 8 n_tokens h_q d
