@@ -488,8 +488,9 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
  * replaced (copied before a write, or moved by an eviction).  Groups that are
  * out of order or range write ATTN_CORE_ERR_DEVICE_TABLE to dev_status and
  * share nothing.  1 <= n_groups <= n_seq.  The workspace holds the rows of
- * shared and own keys in fp32 until they are joined: about 8 n_tokens h_q d
- * bytes more than attn_core_paged_fwd's.  Two to four kernels; the same inputs
+ * shared and own keys in fp32 until they are joined, and the parts of sequences
+ * of few rows: about 8 n_tokens h_q (d + 3) + 123000 d bytes more than
+ * attn_core_paged_fwd's (16 MB more at d = 128 for a few tokens).  Two to four kernels; the same inputs
  * give the same bits. */
 size_t attn_core_paged_prefix_workspace_bytes(const attn_core_paged_params* p, int32_t n_groups);
 int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups, const int32_t* group_starts,
