@@ -83,8 +83,7 @@ int launch_paged_t(const PagedMaps& m, const PagedArgs& args, cudaStream_t st)
 {
     constexpr uint32_t smem = PagedCfg<D>::SMEM;
     // new tokens that make tiles of few rows, on average
-    const bool fine = (int64_t)args.t.n_tokens * args.group <= (int64_t)kFineRows * args.t.n_seq;
-    auto kern = fine ? paged_attn_kernel<D, true, false> : paged_attn_kernel<D, false, false>;
+    auto kern = fine_batch(args) ? paged_attn_kernel<D, true, false> : paged_attn_kernel<D, false, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return (int)e;
     // The most units that the tables can ask for bounds the grid (short batches

@@ -66,6 +66,7 @@ namespace {
 // 9.6 -> 10.6 in a graph (few blocks, one after another: their longer chain shows).  A
 // kernel of its own: the choice inside the loop cost the others 3 to 4%.
 constexpr int kFineRows = 32;
+inline bool fine_batch(const PagedArgs& a) { return (int64_t)a.t.n_tokens * a.group <= (int64_t)kFineRows * a.t.n_seq; }
 constexpr int kPagedMaxCtas = 160;   // workspace slots; a GB300 has 152 SMs
 
 // Layout of a [ROWS x D] tile of Q, K or V: column chunks of 64 with the 128-byte
@@ -354,7 +355,8 @@ __device__ __forceinline__ bool next_work(PagedBars* bars, const WaitCtx& wc, Ri
 
 }  // namespace
 
-// FINE: tiles of at most kFineRows rows carry P in two terms.
+// FINE: tiles of at most kFineRows rows carry P in two terms, and those of a group's shared
+// keys, whose rows would be such tiles' one by one.
 // PREFIX: the sequences are a plan's (PrefixSeq), whose rows may have their keys in two
 // of them; such rows go to the workspace, and records say where each row's parts lie.
 template <int D, bool FINE, bool PREFIX>
@@ -526,6 +528,9 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
     const uint32_t tmem = (uint32_t)uniform((int)bars->tmem_base);
     const WaitCtx wc{&bars->abort_flag, t.status, a.timeout_ns};
     const int group = a.group;
+    auto two_terms = [&](const Segment& g) {
+        return FINE && (g.n_tok * group <= kFineRows || (PREFIX && (g.m & kKindPrefix)));
+    };
 
     // the join may take its place on the chip (it waits for this grid's end)
     if constexpr (!PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -806,7 +811,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                 if (pending) ok = issue_pv();
                 pending = true;
                 first = j == g.j0;
-                fine = FINE && g.n_tok * group <= kFineRows;
+                fine = two_terms(g);
             }
             if (!ok) break;
             qr.advance();
@@ -961,7 +966,7 @@ paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a)
                         pw[e] = pack_bf16x2(lo, hi);
                     }
                     tmem_st16(tS + 16 * part, pw);
-                    if (FINE && g.n_tok * group <= kFineRows) {
+                    if (two_terms(g)) {
                         // what the rounding left, into the half's other 32 columns (p formed
                         // again, which costs the other tiles no registers)
 #pragma unroll

@@ -17,10 +17,10 @@
 //   join   a warp per row adds its parts up
 //
 // Measured on one GB300 (64/8 heads of 128 but where said): 64 samples of a prompt of 8192
-// keys with up to 500 of their own 43 us (paged_fwd over the same batch: 218), 16 questions
-// about 131072 keys 105 us (5.2 TB/s; 820), 6 prompts of up to 4000 keys with 8 samples each, 8/8
-// heads of 96, 42 us (86), 2 x 16 sequences with up to 8 drafted tokens over 2000 keys, 16 heads
-// of 160, 29 us (85), four samples of 512 keys 12 us in a graph.  What bounds the short ones is
+// keys with up to 500 of their own 49 us (paged_fwd over the same batch: 218), 16 questions
+// about 131072 keys 108 us (5.1 TB/s; 820), 6 prompts of up to 4000 keys with 8 samples each, 8/8
+// heads of 96, 36 us (86), 2 x 16 sequences with up to 8 drafted tokens over 2000 keys, 16 heads
+// of 160, 31 us (85), four samples of 512 keys 12 us in a graph.  What bounds the short ones is
 // the chain plan - set-up - first loads (8 us) and the join behind (5 us).
 #include <atomic>
 #include <chrono>
@@ -741,7 +741,10 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     // those has no wait that the test hook could let run out)
     if (!prefix_all_few(a)) {
         constexpr uint32_t smem = PagedCfg<D, true>::SMEM;
-        auto kern = paged_attn_kernel<D, false, true>;     // (the tiles that are fine, kFineRows, are not its)
+        // P of the shared keys in two terms where paged_attn has two for these batches: 64
+        // samples 44 -> 49 us, a long document 104 -> 108, drafts 29 -> 31, and O off by
+        // 1.7e-3 in the 2-norm, its own rounding, where one term leaves 2.3e-3
+        auto kern = fine_batch(a) ? paged_attn_kernel<D, true, true> : paged_attn_kernel<D, false, true>;
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
             return (int)e;
         const int64_t blocks = ((int64_t)t.max_pages * t.page_size + 127) / 128;

@@ -476,7 +476,9 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
  * whose page_table rows name the same pages in their first prefix_pages[g]
  * columns (only one row's entries are read there).  The shared keys are
  * visited once for all rows of the group instead of once for each sequence;
- * O and LSE are those of attn_core_paged_fwd up to rounding.  Both tables are
+ * O and LSE are those of attn_core_paged_fwd up to rounding (with at least as
+ * many terms of P; the last bits of a row depend on its group's other rows too,
+ * whose maxima move together).  Both tables are
  * in device memory (group_starts [n_groups + 1], prefix_pages [n_groups]) and
  * followed by captured graphs; groups may be empty, and sequences outside all
  * groups share nothing.  Of a group's pages those count that all its sequences
@@ -490,8 +492,8 @@ int attn_core_paged_fwd(const attn_core_paged_params* p, const void* q, const vo
  * share nothing.  1 <= n_groups <= n_seq.  The workspace holds the rows of
  * shared and own keys in fp32 until they are joined, and the parts of sequences
  * of few rows: about 8 n_tokens h_q (d + 3) + 123000 d bytes more than
- * attn_core_paged_fwd's (16 MB more at d = 128 for a few tokens).  Two to four kernels; the same inputs
- * give the same bits. */
+ * attn_core_paged_fwd's (16 MB more at d = 128 for a few tokens).  Two to four
+ * kernels; the same inputs give the same bits. */
 size_t attn_core_paged_prefix_workspace_bytes(const attn_core_paged_params* p, int32_t n_groups);
 int attn_core_paged_prefix_fwd(const attn_core_paged_params* p, int32_t n_groups, const int32_t* group_starts,
                                const int32_t* prefix_pages, const void* q, const void* k_pages, const void* v_pages,
