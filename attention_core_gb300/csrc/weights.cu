@@ -16,10 +16,17 @@
 //   8 sequences, up to 500 new tokens over 4001 keys, 16 heads of 160          43 us
 //   one new token over 500 keys                                     9 us in a graph
 // Tried and left out: row tiles of 256 rows whose columns a half's two warpgroups share (half
-// the products and commits, one score buffer a half: 203 us); a part of the exponentials by a polynomial on the FMA pipe (they do
-// not bound the loop: 190 -> 236 us); two issuing warps, one for each half (192 us, and one
-// launch in about 600 of single tokens ended in a launch failure whose cause was not
-// found; with one issuing warp 24000 launches gave the same bits).
+// the products and commits, one score buffer a half: 203 us); a part of the exponentials by a
+// polynomial on the FMA pipe (they do not bound the loop: 190 -> 236 us); two issuing warps,
+// one for each half (192 us, and one launch in about 600 of single tokens ended in a launch
+// failure; with one issuing warp 24000 launches gave the same bits).  That form's source is
+// not kept.  What a second issuer changes, by reading: a row tile's slot is free after two
+// commits, not one; and a commit covers the products of its own thread alone, so each issuer
+// needs a drain barrier of its own.  With one between them the faster issuer's commit lets
+// both leave, and the other's last commits can arrive when the CTA's shared memory is no
+// longer its own: rare, with right results before, as was seen.  Here one thread issues and
+// commits everything, waits for its last commit before the CTA's last barrier, and TMEM is
+// given back behind that one.
 //
 // Persistent, one CTA per SM, equal shares of the work (weights_sched.cuh).  640 threads:
 //   warp 0  runs of items, in a ring of jobs that the others read, and their K by TMA: an
