@@ -17,7 +17,7 @@
 //   join   a warp per row adds its parts up
 //
 // Measured on one GB300 (64/8 heads of 128 but where said): 64 samples of a prompt of 8192
-// keys with up to 500 of their own 49 us (paged_fwd over the same batch: 218), 16 questions
+// keys with up to 500 of their own 48 us (paged_fwd over the same batch: 218), 16 questions
 // about 131072 keys 108 us (5.1 TB/s; 820), 6 prompts of up to 4000 keys with 8 samples each, 8/8
 // heads of 96, 36 us (86), 2 x 16 sequences with up to 8 drafted tokens over 2000 keys, 16 heads
 // of 160, 31 us (85), four samples of 512 keys 12 us in a graph.  What bounds the short ones is
@@ -742,7 +742,7 @@ int launch_prefix_t(const PagedMaps& m, PagedArgs a, const PrefixGroups& g, cons
     if (!prefix_all_few(a)) {
         constexpr uint32_t smem = PagedCfg<D, true>::SMEM;
         // P of the shared keys in two terms where paged_attn has two for these batches: 64
-        // samples 44 -> 49 us, a long document 104 -> 108, drafts 29 -> 31, and O off by
+        // samples 44 -> 48 us, a long document 104 -> 108, drafts 29 -> 31, and O off by
         // 1.7e-3 in the 2-norm, its own rounding, where one term leaves 2.3e-3
         auto kern = fine_batch(a) ? paged_attn_kernel<D, true, true> : paged_attn_kernel<D, false, true>;
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)

@@ -55,3 +55,50 @@ def test_a_plan_is_the_calls_own(groups, each):
         wrong += sum((bits(x) != w).sum() for x, w in zip(out[i], want[i]))
     assert int(wrong) == 0
     assert all(int(x.status.item()) == 0 for x in p)
+
+
+def test_lengths_that_change_between_calls_of_one_graph():
+    """Two calls of one batch in a graph, its lengths changed between them: the second
+    finds the first's plan and stamps where it puts its own."""
+    p = of_lengths(2, 12, 40, 37, 3)
+    full = p.kv_lens.clone()
+    # the first call's lengths end inside the shared pages for one group's sequences
+    short = torch.where(torch.arange(24, device=DEV) % 12 < 5, full, full - (full % 16)).to(torch.int32)
+    batch = p.batch(group_starts=p.starts, prefix_pages=p.pages)
+    out = [(torch.empty_like(p.q), torch.empty((p.h_q, p.n_tokens), device=DEV)) for _ in range(2)]
+
+    def both():
+        for lens, (o, lse) in zip((short, full), out):
+            p.kv_lens.copy_(lens)
+            ac.paged_prefix_fwd(batch, p.q, p.k_pages, p.v_pages, out=o, lse=lse)
+    both()
+    whole = p.keys, p.values, p.nk
+    for lens, x in zip((short, full), out):
+        p.nk = lens.tolist()
+        p.keys, p.values = ([k[:n] for k, n in zip(y, p.nk)] for y in whole[:2])
+        check_attention(*x, attend(p), p)
+    want = [[bits(x).clone() for x in y] for y in out]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(100):
+        for y in out:
+            for x in y:
+                x.zero_()
+        graph.replay()
+        wrong += sum((bits(x) != w).sum() for y, v in zip(out, want) for x, w in zip(y, v))
+    assert int(wrong) == 0 and int(p.status.item()) == 0
+
+
+def test_few_tokens_among_many_sequences():
+    """More sequences than a block plans for, nearly all without new tokens."""
+    nq = [1 if i % 9 == 0 else 0 for i in range(180)]
+    p = shared([(90, 4), (60, 7), (30, 2)], nq, [1 + 3 * i for i in range(180)], 1, 1, 64, 16, seed=7)
+    batch = p.batch(group_starts=p.starts, prefix_pages=p.pages)
+    for _ in range(2):
+        o, lse = ac.paged_prefix_fwd(batch, p.q, p.k_pages, p.v_pages)
+        check_attention(o, lse, attend(p), p)
+        batch.workspace.fill_(255)
+    assert int(p.status.item()) == 0
