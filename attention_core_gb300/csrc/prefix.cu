@@ -158,7 +158,7 @@ struct FewCfg {
 };
 
 // The plan, in shared memory or in the workspace, where it is read past L1: there a kernel
-// wrote it that may still be running (await_plan).
+// wrote it that may still be running (plan_written).
 struct PlanView {
     const PrefixSeq* seq;
     int n;
